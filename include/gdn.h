@@ -57,13 +57,14 @@
 #ifndef GDN_H
 #define GDN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
 #endif
 
-#define GDN_VERSION 3
+#define GDN_VERSION 4
 
 enum gdn_status {
     GDN_OK = 0,
@@ -440,6 +441,151 @@ int gdn_verify_tree_step(const int32_t *node_prev, int N_prev, const int32_t *pa
                          float *S_ckpt, float *H, void *o, void *y, void *hist_out,
                          int B, int N, int Hk, int Hv, int dk, int dv, int W,
                          int in_dtype, int o_dtype, float l2_eps, void *stream);
+
+/*
+ * The paged key/value cache and the window attention of a verify step -- what
+ * the full-attention layers between the GDN layers of a hybrid model need in
+ * the same loop: every sequence appends a window (a chain of drafts or a draft
+ * tree), attends it over its context, and is cut back to the accepted path.
+ *
+ *   pool    [planes][n_pages][Hkv][page][D]  dtype; plane 2l holds the keys of
+ *           layer l and plane 2l+1 its values (any number of planes)
+ *   k_pages, v_pages  one plane each, [n_pages][Hkv][page][D]
+ *   table   [rows][P] int32: the page ids of one sequence a row, slot s for the
+ *           tokens s*page .. s*page+page-1; an entry outside [0, n_pages) is
+ *           an empty slot (written as -1)
+ *   ref     [n_pages] int32: how many table entries hold the page (0: free)
+ *   lens    [rows] int32: committed tokens of a sequence (below 0 taken as 0)
+ * page is a power of two, 16..1024; D is 64, 128 or 256; Hkv >= 1; the
+ * addressed bytes may pass 2^32.  int32 arrays need 4-byte alignment, the
+ * others 16.  Pages are taken lowest free id first and every result is a
+ * function of the inputs alone.  A slot that is empty, or past the table, is
+ * never read or written through: keys there are not seen, tokens not stored.
+ *
+ * gdn_kv_reserve -- pages for the next add[b] tokens of every sequence, the
+ * slots lens[b]/page .. (lens[b]+add[b]-1)/page.  The empty ones among them
+ * get the lowest free pages (ref becomes 1) in order of sequence, then slot.
+ *   granted[b] <- add[b], or 0 where add[b] <= 0, where the window would pass
+ *   slot P-1 (such a sequence asks for no page), or where the pages that the
+ *   sequences 0..b ask for together are more than there are free (a sequence
+ *   that needs no page is always granted).  What is not granted takes nothing.
+ *   lens, add, granted [B]; table [B][P]; B <= 65536
+ */
+int gdn_kv_reserve(const int32_t *lens, const int32_t *add, int32_t *table, int32_t *ref,
+                   int32_t *granted, int B, int P, int n_pages, int page, void *stream);
+
+/*
+ * gdn_kv_append -- the window's keys and values to the positions lens[b]+t,
+ * t < count[b] (clamped into 0..K; NULL: K), of one layer, byte copies.
+ *   k, v [B][K][Hkv][D]; token (b, t) starts kv_stride elements after the one
+ *   before it (>= Hkv*D and a multiple of 16 bytes: a slice of a stacked
+ *   projection row will do); lens, count [B]; table [B][P]
+ */
+int gdn_kv_append(const void *k, const void *v, long long kv_stride, void *k_pages, void *v_pages,
+                  const int32_t *lens, const int32_t *count, const int32_t *table,
+                  int B, int K, int Hkv, int D, int page, int n_pages, int P, int dtype, void *stream);
+
+/*
+ * gdn_kv_rollback_tree -- the cache cut back to the accepted path of a window
+ * of N tree nodes (the cache side of gdn_rollback_tree).  Sequence b keeps the
+ * path root..node[b] (none where node[b] is outside [0, count[b])): in every
+ * plane its i-th token moves from position lens[b]+path[i] to lens[b]+i (byte
+ * copies), lens_out[b] <- lens[b] + |path|, and every page of a slot from
+ * ceil(lens_out[b]/page) on is given back (ref -1, slot -1).
+ *   node, lens, lens_out [B]; parent [B][N] as the tree calls above, NULL for a
+ *   chain (parent i-1: node = accepted tokens - 1); count [B] or NULL (N);
+ *   1 <= N <= 64; table [B][P]; lens_out may be lens
+ */
+int gdn_kv_rollback_tree(const int32_t *node, const int32_t *parent, const int32_t *lens,
+                         const int32_t *count, int32_t *table, int32_t *ref, void *pool,
+                         int32_t *lens_out, int B, int N, int P, int planes, int n_pages,
+                         int Hkv, int page, int D, int dtype, void *stream);
+
+/*
+ * gdn_kv_free -- the rows given back: ref -1 for each page they hold, the
+ * slots -1, lens 0.  rows [n] int32 (values outside [0, B) are passed over; a
+ * row named twice is freed once); table [B][P], lens [B].
+ */
+int gdn_kv_free(const int32_t *rows, int32_t *lens, int32_t *table, int32_t *ref,
+                int n, int B, int P, int n_pages, void *stream);
+
+/*
+ * gdn_kv_fork -- row dst[i] becomes a copy of row src[i]: its full pages are
+ * shared (ref +1), a partial last page is copied in every plane into the lowest
+ * free page (in order of i), lens[dst] <- lens[src].
+ *   granted[i] <- 1, or 0 (nothing changes) where src[i] or dst[i] is outside
+ *   [0, B) or they are the same, where the row dst[i] still holds a page
+ *   (gdn_kv_free it first), where row src[i] lacks a page of its tokens, or
+ *   where the partial pages of the forks 0..i are more than the free ones (a
+ *   fork without a partial page is always granted).
+ *   src, dst, granted [n]; 0 <= n <= 4096; one call names a row as dst at most
+ *   once and not as src as well
+ */
+int gdn_kv_fork(const int32_t *src, const int32_t *dst, int32_t *lens, int32_t *table, int32_t *ref,
+                void *pool, int32_t *granted, int n, int B, int P, int planes, int n_pages,
+                int Hkv, int page, int D, int dtype, void *stream);
+
+/*
+ * gdn_kv_compact -- the U pages in use (ref > 0) moved to the ids 0..U-1: the
+ * k-th one with an id >= U (ascending) goes to the k-th free id below U, in
+ * every plane.  table_out and ref_out are table and ref under the new ids
+ * (free pages' ref 0); empty slots stay as they are.
+ *   table, table_out [entries]; ref, ref_out [n_pages]; none may overlap
+ *   workspace: gdn_kv_compact_workspace bytes, 16-byte aligned, its contents
+ *   not kept between calls
+ */
+int gdn_kv_compact(const int32_t *table, const int32_t *ref, void *pool, int32_t *table_out,
+                   int32_t *ref_out, void *workspace, size_t workspace_bytes, long long entries,
+                   int planes, int n_pages, int Hkv, int page, int D, int dtype, void *stream);
+
+/* bytes that gdn_kv_compact needs as workspace for n_pages */
+int gdn_kv_compact_workspace(int n_pages, size_t *bytes);
+
+/*
+ * gdn_kv_copy -- page src[i] to page dst[i] in every plane, i < n (a pair with
+ * an id outside [0, n_pages) is passed over).  No page may be a source and a
+ * destination, or a destination twice, in one call.
+ */
+int gdn_kv_copy(const int32_t *src, const int32_t *dst, void *pool, int n, int planes, int n_pages,
+                int Hkv, int page, int D, int dtype, void *stream);
+
+/*
+ * gdn_attn_verify -- attention of a window of K tokens over the paged cache;
+ * K = 1 is the decode step.  Query head h reads key/value head h / (Hq/Hkv).
+ * Row (b, t, h), t < count[b], sees the committed keys at 0..lens[b]-1 and the
+ * window's keys lens[b]+i of the nodes i on the path from a root to t (chain:
+ * i <= t):
+ *   x_j = scale * q . k_j,   o = sum_j e^{x_j} v_j / sum_j e^{x_j},
+ *   lse = log sum_j e^{x_j}
+ * over the keys it sees, with x, the sums and the running maximum in fp32 (for
+ * bf16 the weights e^{x_j - max} enter the product with v rounded to bf16).  A
+ * row that sees no key has o = 0, lse = -inf.  What is in unseen keys and values
+ * (NaN, infinities) changes nothing.  Rows t >= count[b] are left untouched.
+ *
+ * prefix_len > 0 (a multiple of page, at most P*page): every sequence with
+ * lens[b] >= prefix_len holds the SAME pages in its first prefix_len/page slots
+ * (forks of one prompt).  Their rows then read those pages once for all; shorter
+ * sequences attend on their own.  The results are those of prefix_len = 0 up to
+ * the order of the sums.
+ *
+ *   q [B][K][Hq][D] dtype, token (b, t) starting q_stride elements after the
+ *   one before it (>= Hq*D, a multiple of 16 bytes); k_pages, v_pages;
+ *   lens [B]; count [B] or NULL (K each; clamped into 0..K); parent [B][K] as the
+ *   tree calls, or NULL for a chain; table [B][P]
+ *   o [B][K][Hq][D] dtype; lse [B][K][Hq] float or NULL
+ *   workspace: gdn_attn_workspace bytes, 16-byte aligned, its contents not kept
+ *   between calls (calls on different streams need one each)
+ *   0 <= B <= 4096, 1 <= K <= 64, Hq % Hkv == 0, scale finite
+ */
+int gdn_attn_verify(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
+                    const int32_t *lens, const int32_t *count, const int32_t *parent,
+                    const int32_t *table, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                    int B, int K, int Hq, int Hkv, int D, int page, int n_pages, int P,
+                    int prefix_len, float scale, int dtype, void *stream);
+
+/* bytes that gdn_attn_verify needs as workspace for these sizes */
+int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, int prefix_len,
+                       int dtype, size_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@
 // the CUDA context).
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
+#include "gdn_kv_internal.h"
 
 #include <cstdarg>
 #include <cstdint>
@@ -78,6 +79,44 @@ int check_gdn_shape(const char* fn, int B, int K, int Hk, int Hv, int dk, int dv
     REQUIRE(eps >= 0.0f, GDN_EINVAL, "%s: l2_eps < 0", fn);
     return GDN_OK;
 }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// shared checks of the cache's geometry; fills g
+int check_kv(const char* fn, int planes, int n_pages, int Hkv, int page, int D, int dtype, gdn::KvGeom& g)
+{
+    REQUIRE(valid_dtype(dtype), GDN_EINVAL, "%s: bad dtype code %d", fn, dtype);
+    REQUIRE(planes >= 1 && n_pages >= 1 && Hkv >= 1, GDN_EINVAL, "%s: planes = %d, n_pages = %d, Hkv = %d must be >= 1",
+            fn, planes, n_pages, Hkv);
+    REQUIRE(page >= 1, GDN_EINVAL, "%s: page = %d < 1", fn, page);
+    REQUIRE(D == 64 || D == 128 || D == 256, GDN_EUNSUPPORTED, "%s: D = %d not in {64, 128, 256}", fn, D);
+    REQUIRE(page >= 16 && page <= 1024 && (page & (page - 1)) == 0, GDN_EUNSUPPORTED,
+            "%s: page = %d is not a power of two in 16..1024", fn, page);
+    REQUIRE(n_pages <= gdn::kKvPagesMax, GDN_EUNSUPPORTED, "%s: n_pages = %d > %d", fn, n_pages, gdn::kKvPagesMax);
+    REQUIRE(Hkv <= 1024, GDN_EUNSUPPORTED, "%s: Hkv = %d > 1024", fn, Hkv);
+    REQUIRE(planes <= 65535, GDN_EUNSUPPORTED, "%s: planes = %d > 65535", fn, planes);
+    g.planes = planes;
+    g.n_pages = n_pages;
+    g.Hkv = Hkv;
+    g.page_log2 = 0;
+    while ((1 << g.page_log2) < page) ++g.page_log2;
+    g.row_bytes = D * (int)elem_size(dtype);
+    return GDN_OK;
+}
+
+// outputs that overlap one another or an input; a pair of null spans never does
+bool any_overlap(const Span* outs, int n_out, const Span* ins, int n_in)
+{
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(outs[i], ins[j])) return true;
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+Span ints(const int32_t* p, size_t n) { return Span{p, p ? n * 4 : 0}; }
 
 }  // namespace
 
@@ -612,6 +651,235 @@ int gdn_verify_tree_step(const int32_t* node_prev, int N_prev, const int32_t* pa
     a.S_ckpt = S_ckpt;
     a.pick = true;
     return launch_status(gdn::launch_verify(a, in_dtype == GDN_BF16, o_dtype == GDN_BF16, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_reserve(const int32_t* lens, const int32_t* add, int32_t* table, int32_t* ref, int32_t* granted, int B,
+                   int P, int n_pages, int page, void* stream)
+{
+    const char* fn = "gdn_kv_reserve";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, 1, n_pages, 1, page, 64, GDN_F32, g);
+    if (rc) return rc;
+    REQUIRE(B >= 0 && P >= 1, GDN_EINVAL, "%s: B = %d, P = %d", fn, B, P);
+    REQUIRE(B <= 65536, GDN_EUNSUPPORTED, "%s: B = %d > 65536", fn, B);
+    if (B == 0) return ok();
+    REQUIRE(lens && add && table && ref && granted, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned4(lens) && aligned4(add) && aligned4(table) && aligned4(ref) && aligned4(granted), GDN_EINVAL,
+            "%s: pointers must be 4-byte aligned", fn);
+    const Span outs[] = {ints(table, (size_t)B * P), ints(ref, n_pages), ints(granted, B)};
+    const Span ins[] = {ints(lens, B), ints(add, B)};
+    REQUIRE(!any_overlap(outs, 3, ins, 2), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const gdn::KvReserveArgs a{lens, add, table, ref, granted, B, P, n_pages, g.page_log2};
+    return launch_status(gdn::launch_kv_reserve(a, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_append(const void* k, const void* v, long long kv_stride, void* k_pages, void* v_pages,
+                  const int32_t* lens, const int32_t* count, const int32_t* table, int B, int K, int Hkv, int D,
+                  int page, int n_pages, int P, int dtype, void* stream)
+{
+    const char* fn = "gdn_kv_append";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, 1, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(B >= 0 && K >= 1 && P >= 1, GDN_EINVAL, "%s: B = %d, K = %d, P = %d", fn, B, K, P);
+    REQUIRE(B <= 65535 && K <= 65536, GDN_EUNSUPPORTED, "%s: B = %d or K = %d too large", fn, B, K);
+    if (B == 0) return ok();
+    REQUIRE(k && v && k_pages && v_pages && lens && table, GDN_EINVAL, "%s: null pointer", fn);
+    const size_t es = elem_size(dtype), token = (size_t)Hkv * D;
+    REQUIRE(kv_stride >= (long long)token && kv_stride < (1LL << 40) && kv_stride * es % 16 == 0, GDN_EINVAL,
+            "%s: kv_stride = %lld is below Hkv*D or no multiple of 16 bytes", fn, kv_stride);
+    REQUIRE(aligned16(k) && aligned16(v) && aligned16(k_pages) && aligned16(v_pages), GDN_EINVAL,
+            "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE(aligned4(lens) && aligned4(count) && aligned4(table), GDN_EINVAL, "%s: lens, count and table must be "
+            "4-byte aligned", fn);
+    const size_t in = (((size_t)B * K - 1) * kv_stride + token) * es, plane = (size_t)n_pages * g.page_bytes();
+    const Span outs[] = {Span{k_pages, plane}, Span{v_pages, plane}};
+    const Span ins[] = {Span{k, in}, Span{v, in}, ints(lens, B), ints(count, B), ints(table, (size_t)B * P)};
+    REQUIRE(!any_overlap(outs, 2, ins, 5), GDN_EINVAL, "%s: a plane overlaps another buffer", fn);
+    const gdn::KvAppendArgs a{k, v, (size_t)kv_stride * es, k_pages, v_pages, lens, count, table, B, K, P, g};
+    return launch_status(gdn::launch_kv_append(a, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_rollback_tree(const int32_t* node, const int32_t* parent, const int32_t* lens, const int32_t* count,
+                         int32_t* table, int32_t* ref, void* pool, int32_t* lens_out, int B, int N, int P, int planes,
+                         int n_pages, int Hkv, int page, int D, int dtype, void* stream)
+{
+    const char* fn = "gdn_kv_rollback_tree";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(B >= 0 && N >= 1 && P >= 1, GDN_EINVAL, "%s: B = %d, N = %d, P = %d", fn, B, N, P);
+    REQUIRE(N <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: N = %d > %d", fn, N, gdn::kKvWindowMax);
+    REQUIRE(B <= 65535, GDN_EUNSUPPORTED, "%s: B = %d too large", fn, B);
+    if (B == 0) return ok();
+    REQUIRE(node && lens && table && ref && pool && lens_out, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned16(pool), GDN_EINVAL, "%s: pool must be 16-byte aligned", fn);
+    REQUIRE(aligned4(node) && aligned4(parent) && aligned4(lens) && aligned4(count) && aligned4(table) &&
+                aligned4(ref) && aligned4(lens_out),
+            GDN_EINVAL, "%s: int32 pointers must be 4-byte aligned", fn);
+    const Span outs[] = {ints(table, (size_t)B * P), ints(ref, n_pages), ints(lens_out, B),
+                         Span{pool, (size_t)planes * n_pages * g.page_bytes()}};
+    const Span ins[] = {ints(node, B), ints(parent, (size_t)B * N), ints(count, B),
+                        ints(lens == lens_out ? nullptr : lens, B)};
+    REQUIRE(!any_overlap(outs, 4, ins, 4), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const Span len_in[] = {ints(lens, B)};
+    const Span rest[] = {outs[0], outs[1], outs[3]};
+    for (const Span& o : rest) REQUIRE(!overlap(o, len_in[0]), GDN_EINVAL, "%s: an output overlaps lens", fn);
+    const gdn::KvRollbackArgs a{node, parent, lens, count, table, ref, pool, lens_out, B, N, P, g};
+    return launch_status(gdn::launch_kv_rollback(a, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_free(const int32_t* rows, int32_t* lens, int32_t* table, int32_t* ref, int n, int B, int P, int n_pages,
+                void* stream)
+{
+    const char* fn = "gdn_kv_free";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, 1, n_pages, 1, 16, 64, GDN_F32, g);
+    if (rc) return rc;
+    REQUIRE(n >= 0 && B >= 0 && P >= 1, GDN_EINVAL, "%s: n = %d, B = %d, P = %d", fn, n, B, P);
+    if (n == 0 || B == 0) return ok();
+    REQUIRE(rows && lens && table && ref, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned4(rows) && aligned4(lens) && aligned4(table) && aligned4(ref), GDN_EINVAL,
+            "%s: pointers must be 4-byte aligned", fn);
+    const Span outs[] = {ints(lens, B), ints(table, (size_t)B * P), ints(ref, n_pages)};
+    const Span ins[] = {ints(rows, n)};
+    REQUIRE(!any_overlap(outs, 3, ins, 1), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    return launch_status(gdn::launch_kv_free(rows, lens, table, ref, n, B, P, n_pages, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_fork(const int32_t* src, const int32_t* dst, int32_t* lens, int32_t* table, int32_t* ref, void* pool,
+                int32_t* granted, int n, int B, int P, int planes, int n_pages, int Hkv, int page, int D, int dtype,
+                void* stream)
+{
+    const char* fn = "gdn_kv_fork";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(n >= 0 && B >= 1 && P >= 1, GDN_EINVAL, "%s: n = %d, B = %d, P = %d", fn, n, B, P);
+    REQUIRE(n <= gdn::kKvForkMax, GDN_EUNSUPPORTED, "%s: n = %d > %d", fn, n, gdn::kKvForkMax);
+    if (n == 0) return ok();
+    REQUIRE(src && dst && lens && table && ref && pool && granted, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned16(pool), GDN_EINVAL, "%s: pool must be 16-byte aligned", fn);
+    REQUIRE(aligned4(src) && aligned4(dst) && aligned4(lens) && aligned4(table) && aligned4(ref) && aligned4(granted),
+            GDN_EINVAL, "%s: int32 pointers must be 4-byte aligned", fn);
+    const Span outs[] = {ints(lens, B), ints(table, (size_t)B * P), ints(ref, n_pages), ints(granted, n),
+                         Span{pool, (size_t)planes * n_pages * g.page_bytes()}};
+    const Span ins[] = {ints(src, n), ints(dst, n)};
+    REQUIRE(!any_overlap(outs, 5, ins, 2), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const gdn::KvForkArgs a{src, dst, lens, table, ref, pool, granted, n, B, P, g};
+    return launch_status(gdn::launch_kv_fork(a, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_compact_workspace(int n_pages, size_t* bytes)
+{
+    const char* fn = "gdn_kv_compact_workspace";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, 1, n_pages, 1, 16, 64, GDN_F32, g);
+    if (rc) return rc;
+    REQUIRE(bytes, GDN_EINVAL, "%s: null bytes", fn);
+    *bytes = gdn::kv_compact_words(n_pages) * 4;
+    return ok();
+}
+
+int gdn_kv_compact(const int32_t* table, const int32_t* ref, void* pool, int32_t* table_out, int32_t* ref_out,
+                   void* workspace, size_t workspace_bytes, long long entries, int planes, int n_pages, int Hkv,
+                   int page, int D, int dtype, void* stream)
+{
+    const char* fn = "gdn_kv_compact";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(entries >= 0 && entries < (1LL << 40), GDN_EINVAL, "%s: entries = %lld", fn, entries);
+    REQUIRE(ref && pool && ref_out && workspace && (entries == 0 || (table && table_out)), GDN_EINVAL,
+            "%s: null pointer", fn);
+    REQUIRE(aligned16(pool) && aligned16(workspace), GDN_EINVAL, "%s: pool and workspace must be 16-byte aligned", fn);
+    REQUIRE(aligned4(table) && aligned4(ref) && aligned4(table_out) && aligned4(ref_out), GDN_EINVAL,
+            "%s: int32 pointers must be 4-byte aligned", fn);
+    const size_t need = gdn::kv_compact_words(n_pages) * 4;
+    REQUIRE(workspace_bytes >= need, GDN_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+    const Span outs[] = {ints(table_out, entries), ints(ref_out, n_pages), Span{workspace, need},
+                         Span{pool, (size_t)planes * n_pages * g.page_bytes()}};
+    const Span ins[] = {ints(table, entries), ints(ref, n_pages)};
+    REQUIRE(!any_overlap(outs, 4, ins, 2), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const gdn::KvCompactArgs a{table, ref, pool, table_out, ref_out, static_cast<int32_t*>(workspace), entries, g};
+    return launch_status(gdn::launch_kv_compact(a, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_copy(const int32_t* src, const int32_t* dst, void* pool, int n, int planes, int n_pages, int Hkv, int page,
+                int D, int dtype, void* stream)
+{
+    const char* fn = "gdn_kv_copy";
+    gdn::KvGeom g;
+    int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(n >= 0, GDN_EINVAL, "%s: n = %d < 0", fn, n);
+    if (n == 0) return ok();
+    REQUIRE(src && dst && pool, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned16(pool) && aligned4(src) && aligned4(dst), GDN_EINVAL,
+            "%s: pool must be 16-byte, src and dst 4-byte aligned", fn);
+    const Span outs[] = {Span{pool, (size_t)planes * n_pages * g.page_bytes()}};
+    const Span ins[] = {ints(src, n), ints(dst, n)};
+    REQUIRE(!any_overlap(outs, 1, ins, 2), GDN_EINVAL, "%s: the pool overlaps src or dst", fn);
+    return launch_status(gdn::launch_kv_copy(src, dst, pool, n, g, (hipStream_t)stream), fn);
+}
+
+static int check_attn(const char* fn, int B, int K, int Hq, int Hkv, int D, int page, int P, int prefix_len, int dtype,
+                      int n_pages, gdn::KvGeom& g)
+{
+    int rc = check_kv(fn, 1, n_pages, Hkv, page, D, dtype, g);
+    if (rc) return rc;
+    REQUIRE(B >= 0 && K >= 1 && P >= 1, GDN_EINVAL, "%s: B = %d, K = %d, P = %d", fn, B, K, P);
+    REQUIRE(Hq >= 1 && Hq % Hkv == 0, GDN_EINVAL, "%s: Hq = %d is not a multiple of Hkv = %d", fn, Hq, Hkv);
+    REQUIRE(prefix_len >= 0 && prefix_len % page == 0 && prefix_len / page <= P, GDN_EINVAL,
+            "%s: prefix_len = %d is no multiple of page = %d within %d slots", fn, prefix_len, page, P);
+    REQUIRE(K <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: K = %d > %d", fn, K, gdn::kKvWindowMax);
+    REQUIRE(B <= gdn::kAttnBatchMax, GDN_EUNSUPPORTED, "%s: B = %d > %d", fn, B, gdn::kAttnBatchMax);
+    REQUIRE(Hq <= 1024, GDN_EUNSUPPORTED, "%s: Hq = %d > 1024", fn, Hq);
+    REQUIRE((long long)P * page < (1LL << 31), GDN_EUNSUPPORTED, "%s: %d slots of %d tokens pass 2^31", fn, P, page);
+    return GDN_OK;
+}
+
+int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, int prefix_len, int dtype, size_t* bytes)
+{
+    const char* fn = "gdn_attn_workspace";
+    gdn::KvGeom g;
+    int rc = check_attn(fn, B, K, Hq, Hkv, D, page, P, prefix_len, dtype, 1, g);
+    if (rc) return rc;
+    REQUIRE(bytes, GDN_EINVAL, "%s: null bytes", fn);
+    *bytes = gdn::attn_work_bytes(B, K, Hq, Hkv, D, g.page_log2, P, prefix_len, dtype == GDN_BF16);
+    return ok();
+}
+
+int gdn_attn_verify(const void* q, long long q_stride, const void* k_pages, const void* v_pages, const int32_t* lens,
+                    const int32_t* count, const int32_t* parent, const int32_t* table, void* o, float* lse,
+                    void* workspace, size_t workspace_bytes, int B, int K, int Hq, int Hkv, int D, int page,
+                    int n_pages, int P, int prefix_len, float scale, int dtype, void* stream)
+{
+    const char* fn = "gdn_attn_verify";
+    gdn::KvGeom g;
+    int rc = check_attn(fn, B, K, Hq, Hkv, D, page, P, prefix_len, dtype, n_pages, g);
+    if (rc) return rc;
+    REQUIRE(scale - scale == 0.0f, GDN_EINVAL, "%s: scale is not finite", fn);
+    if (B == 0) return ok();
+    REQUIRE(q && k_pages && v_pages && lens && table && o && workspace, GDN_EINVAL, "%s: null pointer", fn);
+    const size_t es = elem_size(dtype), token = (size_t)Hq * D;
+    REQUIRE(q_stride >= (long long)token && q_stride < (1LL << 40) && q_stride * es % 16 == 0, GDN_EINVAL,
+            "%s: q_stride = %lld is below Hq*D or no multiple of 16 bytes", fn, q_stride);
+    REQUIRE(aligned16(q) && aligned16(k_pages) && aligned16(v_pages) && aligned16(o) && aligned16(workspace),
+            GDN_EINVAL, "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE(aligned4(lens) && aligned4(count) && aligned4(parent) && aligned4(table) && aligned4(lse), GDN_EINVAL,
+            "%s: lens, count, parent, table and lse must be 4-byte aligned", fn);
+    const bool bf16 = dtype == GDN_BF16;
+    const size_t need = gdn::attn_work_bytes(B, K, Hq, Hkv, D, g.page_log2, P, prefix_len, bf16);
+    REQUIRE(workspace_bytes >= need, GDN_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+    const size_t plane = (size_t)n_pages * g.page_bytes(), rows = (size_t)B * K;
+    const Span outs[] = {Span{o, rows * token * es}, Span{lse, lse ? rows * Hq * 4 : 0}, Span{workspace, need}};
+    const Span ins[] = {Span{q, ((rows - 1) * q_stride + token) * es}, Span{k_pages, plane}, Span{v_pages, plane},
+                        ints(lens, B), ints(count, B), ints(parent, rows), ints(table, (size_t)B * P)};
+    REQUIRE(!any_overlap(outs, 3, ins, 7), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const gdn::AttnArgs a{q, (size_t)q_stride, k_pages, v_pages, lens, count, parent, table, o, lse, workspace,
+                          B, K, Hq, Hkv, D, g.page_log2, n_pages, P, prefix_len, scale};
+    return launch_status(gdn::launch_attn(a, bf16, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

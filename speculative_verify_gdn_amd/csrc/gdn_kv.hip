@@ -1,0 +1,551 @@
+// gdn_kv.hip -- the paged key/value cache: pages taken (reserve), windows
+// written (append), cut back to an accepted tree path (rollback), and pages
+// freed, forked, compacted and copied (include/gdn.h states each call).
+//
+// Two kinds of kernel.  Those that decide which page goes where (reserve, fork,
+// compact) are one workgroup: their answer is a running count over all pages
+// and all sequences, a few kilobytes of int32, and one workgroup needs no
+// second launch and no cross-workgroup order; what it costs is the latency of
+// about six dependent reads.  Those that move bytes (append, rollback, page
+// copies) spread 16-byte pieces over the chip.
+#include "gdn_device.h"
+#include "gdn_kv_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kCtl = 1024;            // threads of a deciding workgroup
+constexpr int kCtlWaves = kCtl / 64;
+constexpr int kScanPer = 4;           // pages per thread and scan step
+constexpr int kScan = kCtl * kScanPer;
+
+__device__ __forceinline__ int clamp_count(const int32_t* count, int b, int K)
+{
+    return count ? min(max(count[b], 0), K) : K;
+}
+
+__device__ __forceinline__ bool held(int id, int n_pages) { return (unsigned)id < (unsigned)n_pages; }
+
+// inclusive sum over the lanes of a wave
+__device__ __forceinline__ int wave_scan(int v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// exclusive sum over the kCtl threads of a deciding workgroup; `total` gets the sum of all.
+// Every thread calls it (two barriers); `part` is kCtlWaves words of LDS.
+__device__ __forceinline__ int block_scan(int v, int* part, int& total)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int inc = wave_scan(v);
+    __syncthreads();  // part may still be read from the scan before
+    if (lane == 63) part[w] = inc;
+    __syncthreads();
+    int base = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kCtlWaves; ++i) {
+        const int p = part[i];
+        base += i < w ? p : 0;
+        sum += p;
+    }
+    total = sum;
+    return base + inc - v;
+}
+
+// pages of the ascending step [at, at + kScan) whose ref satisfies `pred`: a bit for each of this
+// thread's kScanPer consecutive pages
+template <typename F>
+__device__ __forceinline__ unsigned page_bits(const int32_t* ref, int at, int n_pages, F pred)
+{
+    unsigned bits = 0;
+    const int p0 = at + (int)threadIdx.x * kScanPer;
+#pragma unroll
+    for (int i = 0; i < kScanPer; ++i)
+        if (p0 + i < n_pages && pred(p0 + i, ref[p0 + i])) bits |= 1u << i;
+    return bits;
+}
+
+// number of free pages, at most about `enough` (counting stops once it is reached)
+__device__ __forceinline__ int count_free(const int32_t* ref, int n_pages, int enough, int* part)
+{
+    int have = 0;
+    for (int at = 0; at < n_pages && have < enough; at += kScan) {
+        int step;
+        block_scan(__popc(page_bits(ref, at, n_pages, [](int, int r) { return r == 0; })), part, step);
+        have += step;
+    }
+    return have;
+}
+
+// ---------------------------------------------------------------- reserve
+// Thread i owns a run of consecutive sequences; their wants are numbered by an
+// exclusive sum, the free pages by another, and want r takes free page r.
+__global__ __launch_bounds__(kCtl) void kv_reserve_kernel(KvReserveArgs a)
+{
+    __shared__ int part[kCtlWaves];
+    __shared__ int ids[kScan];
+    const int per = (a.B + kCtl - 1) / kCtl;
+    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+
+    // slots of sequence b's window: [s0, s1); false where it asks for nothing or passes the table
+    auto window = [&](int b, int& s0, int& s1) {
+        const long long len = max(a.lens[b], 0), add = a.add[b];
+        s0 = s1 = 0;
+        if (add <= 0 || ((len + add - 1) >> a.page_log2) >= a.P) return false;
+        s0 = (int)(len >> a.page_log2);
+        s1 = (int)((len + add - 1) >> a.page_log2) + 1;
+        return true;
+    };
+    auto need_of = [&](int b, int s0, int s1) {
+        int n = 0;
+        for (int s = s0; s < s1; ++s) n += !held(a.table[(size_t)b * a.P + s], a.n_pages);
+        return n;
+    };
+
+    int need = 0;
+    for (int b = b0; b < b1; ++b) {
+        int s0, s1;
+        // more than there are pages is as good as any larger number, and keeps the block's sum in 32 bits
+        if (window(b, s0, s1)) need = min(need + min(need_of(b, s0, s1), a.n_pages + 1), a.n_pages + 1);
+    }
+    int total;
+    const int base = block_scan(need, part, total);
+    const int have = count_free(a.ref, a.n_pages, total, part);
+
+    // grants, and where this thread's wants end: the first sequence that does not fit stops all later
+    // ones that need a page, so the granted wants are ranks base .. last-1
+    long long rank = base;
+    int last = base;
+    for (int b = b0; b < b1; ++b) {
+        int s0, s1;
+        const bool any = window(b, s0, s1);
+        const int n = any ? need_of(b, s0, s1) : 0;
+        rank += n;
+        const bool fits = any && (n == 0 || rank <= have);
+        a.granted[b] = fits ? a.add[b] : 0;
+        if (n > 0 && fits) last = (int)rank;
+    }
+
+    int b = b0, s = -1, s0 = 0, s1 = 0, next = base, seen = 0;
+    for (int at = 0; at < a.n_pages && seen < min(total, have); at += kScan) {
+        const unsigned bits = page_bits(a.ref, at, a.n_pages, [](int, int r) { return r == 0; });
+        int step, r = block_scan(__popc(bits), part, step);
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i)
+            if (bits >> i & 1) ids[r++] = at + (int)threadIdx.x * kScanPer + i;
+        __syncthreads();
+        while (next < last && next < seen + step) {
+            if (s < 0) {  // the next sequence's window
+                if (!window(b, s0, s1)) {
+                    ++b;
+                    continue;
+                }
+                s = s0;
+            }
+            for (; s < s1 && next < last && next < seen + step; ++s) {
+                int32_t* slot = a.table + (size_t)b * a.P + s;
+                if (held(*slot, a.n_pages)) continue;
+                const int id = ids[next - seen];
+                *slot = id;
+                a.ref[id] = 1;
+                ++next;
+            }
+            if (s == s1) {
+                ++b;
+                s = -1;
+            }
+        }
+        seen += step;
+    }
+}
+
+// ---------------------------------------------------------------- append
+// A thread per 16 bytes of one token and head, of both K and V.
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a)
+{
+    const int b = blockIdx.y;
+    const int per_row = a.g.row_bytes >> 4, per_token = a.g.Hkv * per_row;
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    const int t = i / per_token, c = i - t * per_token;
+    if (t >= clamp_count(a.count, b, a.K)) return;
+    const long long at = (long long)max(a.lens[b], 0) + t;
+    const long long slot = at >> a.g.page_log2;
+    if (slot >= a.P) return;
+    const int id = a.table[(size_t)b * a.P + slot];
+    if (!held(id, a.g.n_pages)) return;
+    const int h = c / per_row, x = c - h * per_row;
+    const int in_page = (int)(at & ((1 << a.g.page_log2) - 1));
+    const size_t to = ((((size_t)id * a.g.Hkv + h) << a.g.page_log2) + in_page) * a.g.row_bytes + (size_t)x * 16;
+    const size_t from = ((size_t)b * a.K + t) * a.token_bytes + (size_t)c * 16;
+    const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + from);
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + from);
+    *reinterpret_cast<uint4*>(static_cast<char*>(a.k_pages) + to) = k;
+    *reinterpret_cast<uint4*>(static_cast<char*>(a.v_pages) + to) = v;
+}
+
+// ---------------------------------------------------------------- rollback
+// The nodes on the path root..n as a bit mask: by doubling, lane i holding what
+// it has found above node i and the node to go on from.  Called by a whole wave.
+__device__ __forceinline__ unsigned long long node_path(const int32_t* parent, int N, int n)
+{
+    const int lane = threadIdx.x & 63;
+    int up = -1;
+    if (lane < N) {
+        const int p = parent ? parent[lane] : lane - 1;
+        up = p >= 0 && p < lane ? p : -1;
+    }
+    unsigned long long path = 1ull << lane;
+#pragma unroll
+    for (int d = 1; d < kKvWindowMax; d <<= 1) {
+        const int from = max(up, 0);
+        const unsigned long long more = __shfl(path, from, 64);
+        const int far = __shfl(up, from, 64);
+        if (up >= 0) {
+            path |= more;
+            up = far;
+        }
+    }
+    return __shfl(path, n, 64);
+}
+
+constexpr int kMoveBatch = 8;
+
+// A workgroup per sequence: tokens are moved in every plane, then the later
+// pages given back.  A path's i-th node has an index >= i, so a thread that
+// owns 16 bytes of a (plane, head) and moves the path in order never
+// overwrites what it has yet to read; it reads a batch before it writes it.
+__global__ __launch_bounds__(kCtl) void kv_rollback_kernel(KvRollbackArgs a)
+{
+    __shared__ int from_id[kKvWindowMax], to_id[kKvWindowMax], from_row[kKvWindowMax], to_row[kKvWindowMax];
+    const int b = blockIdx.x, lane = threadIdx.x & 63;
+    const int n_raw = a.node[b], live = clamp_count(a.count, b, a.N);
+    const long long len = max(a.lens[b], 0);
+    const bool any = n_raw >= 0 && n_raw < live;
+    const int32_t* parent = a.parent ? a.parent + (size_t)b * a.N : nullptr;
+    const unsigned long long path = any ? node_path(parent, a.N, n_raw) : 0;
+    const int kept = __popcll(path);
+    int32_t* row = a.table + (size_t)b * a.P;
+    const int mask = (1 << a.g.page_log2) - 1;
+    if (threadIdx.x < 64 && (path >> lane & 1)) {
+        const int i = __popcll(path & ((1ull << lane) - 1));
+        const long long from = len + lane, to = len + i;
+        const long long fs = from >> a.g.page_log2, ts = to >> a.g.page_log2;
+        const int f = fs < a.P ? row[fs] : -1, t = ts < a.P ? row[ts] : -1;
+        const bool move = i != lane && held(f, a.g.n_pages) && held(t, a.g.n_pages);
+        from_id[i] = move ? f : -1;
+        to_id[i] = t;
+        from_row[i] = (int)from & mask;
+        to_row[i] = (int)to & mask;
+    }
+    __syncthreads();
+
+    const int per_row = a.g.row_bytes >> 4;
+    const int pieces = a.g.planes * a.g.Hkv * per_row;
+    const size_t plane = (size_t)a.g.n_pages * ((size_t)a.g.Hkv << a.g.page_log2) * a.g.row_bytes;
+    for (int e = threadIdx.x; e < pieces; e += blockDim.x) {
+        const int x = e % per_row, ph = e / per_row;
+        const int h = ph % a.g.Hkv, pl = ph / a.g.Hkv;
+        char* at = static_cast<char*>(a.pool) + pl * plane + (size_t)x * 16;
+        auto addr = [&](int id, int r) {
+            return reinterpret_cast<uint4*>(at + ((((size_t)id * a.g.Hkv + h) << a.g.page_log2) + r) * a.g.row_bytes);
+        };
+        for (int i0 = 0; i0 < kept; i0 += kMoveBatch) {
+            uint4 u[kMoveBatch];
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j)
+                if (i0 + j < kept && from_id[i0 + j] >= 0) u[j] = *addr(from_id[i0 + j], from_row[i0 + j]);
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j)
+                if (i0 + j < kept && from_id[i0 + j] >= 0) *addr(to_id[i0 + j], to_row[i0 + j]) = u[j];
+        }
+    }
+
+    const long long after = len + kept;
+    for (long long s = ((after + mask) >> a.g.page_log2) + threadIdx.x; s < a.P; s += blockDim.x) {
+        const int id = row[s];
+        if (held(id, a.g.n_pages)) {
+            atomicSub(a.ref + id, 1);
+            row[s] = -1;
+        }
+    }
+    if (threadIdx.x == 0) a.lens_out[b] = (int32_t)after;
+}
+
+// ---------------------------------------------------------------- free
+__global__ __launch_bounds__(256) void kv_free_kernel(const int32_t* rows, int32_t* lens, int32_t* table, int32_t* ref,
+                                                      int B, int P, int n_pages)
+{
+    const int b = rows[blockIdx.x];
+    if (!held(b, B)) return;
+    for (int s = threadIdx.x; s < P; s += 256) {
+        const int id = atomicExch(table + (size_t)b * P + s, -1);  // a row named twice gives each page back once
+        if (held(id, n_pages)) atomicSub(ref + id, 1);
+    }
+    if (threadIdx.x == 0) lens[b] = 0;
+}
+
+// ---------------------------------------------------------------- page copies
+// 16-byte pieces of the pages src -> dst of every plane; a workgroup takes
+// kCopyPer pieces of a thread at a time and walks on until all are done.
+constexpr int kCopyPer = 4;
+constexpr int kCopyChunk = 256 * kCopyPer;   // pieces a workgroup moves in one go
+constexpr int kCopyGrid = 256 * 8;           // workgroups that fill the chip
+
+template <typename F>
+__device__ __forceinline__ void copy_pages(char* pool, const KvGeom& g, long long n, F pair)
+{
+    const long long pieces = (long long)(g.page_bytes() >> 4);
+    const long long chunks = (pieces + kCopyChunk - 1) / kCopyChunk, all = n * g.planes * chunks;
+    const size_t bytes = g.page_bytes();
+    for (long long w = blockIdx.x; w < all; w += gridDim.x) {
+        const long long c = w % chunks, r = w / chunks;
+        const long long pl = r % g.planes;
+        int from, to;
+        if (!pair(r / g.planes, from, to)) continue;
+        const uint4* s = reinterpret_cast<const uint4*>(pool + (pl * g.n_pages + from) * bytes);
+        uint4* d = reinterpret_cast<uint4*>(pool + (pl * g.n_pages + to) * bytes);
+        const long long e = c * kCopyChunk + threadIdx.x;
+        uint4 u[kCopyPer];
+#pragma unroll
+        for (int i = 0; i < kCopyPer; ++i)
+            if (e + i * 256 < pieces) u[i] = s[e + i * 256];
+#pragma unroll
+        for (int i = 0; i < kCopyPer; ++i)
+            if (e + i * 256 < pieces) d[e + i * 256] = u[i];
+    }
+}
+
+int copy_grid(long long n, const KvGeom& g)
+{
+    const long long chunks = ((long long)(g.page_bytes() >> 4) + kCopyChunk - 1) / kCopyChunk;
+    const long long all = n * g.planes * chunks;
+    return (int)(all < kCopyGrid ? (all > 0 ? all : 1) : kCopyGrid);
+}
+
+__global__ __launch_bounds__(256) void kv_copy_kernel(const int32_t* src, const int32_t* dst, char* pool, int n,
+                                                      KvGeom g)
+{
+    copy_pages(pool, g, n, [&](long long i, int& from, int& to) {
+        from = src[i];
+        to = dst[i];
+        return held(from, g.n_pages) && held(to, g.n_pages) && from != to;
+    });
+}
+
+// ---------------------------------------------------------------- fork
+// Which forks can be made, their new pages, and the rows.
+__global__ __launch_bounds__(kCtl) void kv_fork_kernel(KvForkArgs a)
+{
+    __shared__ int part[kCtlWaves];
+    __shared__ int ids[kScan];
+    __shared__ int page_of[kKvForkMax];          // -2 refused, -1 no new page, else its rank, then its id
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int page = 1 << a.g.page_log2;
+    auto length = [&](int i) { return max(a.lens[a.src[i]], 0); };
+
+    // can be made, but for the number of free pages: a wave looks over a fork's two rows
+    for (int i = wave; i < a.n; i += kCtlWaves) {
+        const int src = a.src[i], dst = a.dst[i];
+        bool fine = held(src, a.B) && held(dst, a.B) && src != dst;
+        bool tail = false;
+        if (fine) {
+            const long long len = length(i);
+            const long long slots = (len + page - 1) >> a.g.page_log2;
+            fine = slots <= a.P;
+            tail = (len & (page - 1)) != 0;
+            bool bad = false;
+            for (int s = lane; s < a.P; s += 64) {
+                bad |= held(a.table[(size_t)dst * a.P + s], a.g.n_pages);
+                bad |= s < slots && !held(a.table[(size_t)src * a.P + s], a.g.n_pages);
+            }
+            fine = fine && __ballot(bad) == 0;
+        }
+        if (lane == 0) page_of[i] = !fine ? -2 : (tail ? 0 : -1);
+    }
+    __syncthreads();
+    const int per = (a.n + kCtl - 1) / kCtl;
+    const int i0 = min((int)threadIdx.x * per, a.n), i1 = min(i0 + per, a.n);
+    int need = 0;
+    for (int i = i0; i < i1; ++i) need += page_of[i] == 0;
+    int total, rank = block_scan(need, part, total);
+    const int have = count_free(a.ref, a.g.n_pages, total, part);
+    for (int i = i0; i < i1; ++i)
+        if (page_of[i] == 0) {
+            page_of[i] = rank < have ? rank : -2;
+            ++rank;
+        }
+    // ranks to ids
+    int next = i0, seen = 0;
+    for (int at = 0; at < a.g.n_pages && seen < min(total, have); at += kScan) {
+        const unsigned bits = page_bits(a.ref, at, a.g.n_pages, [](int, int r) { return r == 0; });
+        int step, r = block_scan(__popc(bits), part, step);
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i)
+            if (bits >> i & 1) ids[r++] = at + (int)threadIdx.x * kScanPer + i;
+        __syncthreads();
+        for (; next < i1; ++next) {
+            if (page_of[next] < 0) continue;
+            if (page_of[next] >= seen + step) break;
+            page_of[next] = ids[page_of[next] - seen];
+        }
+        seen += step;
+    }
+    __syncthreads();
+    // the rows
+    for (int i = wave; i < a.n; i += kCtlWaves) {
+        const int id = page_of[i];
+        if (lane == 0) a.granted[i] = id != -2;
+        if (id == -2) continue;
+        const int src = a.src[i], dst = a.dst[i], len = length(i);
+        const int full = len >> a.g.page_log2;
+        for (int s = lane; s < a.P; s += 64) {
+            int to = -1;
+            if (s < full) {
+                to = a.table[(size_t)src * a.P + s];
+                if (held(to, a.g.n_pages)) atomicAdd(a.ref + to, 1);
+            } else if (s == full && id >= 0) {
+                to = id;
+                a.ref[id] = 1;
+            }
+            a.table[(size_t)dst * a.P + s] = to;
+        }
+        if (lane == 0) a.lens[dst] = len;
+    }
+}
+
+__global__ __launch_bounds__(256) void kv_fork_copy_kernel(KvForkArgs a)
+{
+    copy_pages(static_cast<char*>(a.pool), a.g, a.n, [&](long long i, int& from, int& to) {
+        if (!a.granted[i]) return false;
+        const int len = max(a.lens[a.src[i]], 0), full = len >> a.g.page_log2;
+        if ((len & ((1 << a.g.page_log2) - 1)) == 0 || full >= a.P) return false;
+        from = a.table[(size_t)a.src[i] * a.P + full];
+        to = a.table[(size_t)a.dst[i] * a.P + full];
+        return held(from, a.g.n_pages) && held(to, a.g.n_pages);
+    });
+}
+
+// ---------------------------------------------------------------- compact
+// work: [0] moves, then the moves' sources, their destinations, and the new id of every page
+__host__ __device__ inline int32_t* compact_from(int32_t* w) { return w + 4; }
+__host__ __device__ inline int32_t* compact_to(int32_t* w, int n) { return w + 4 + (n + 1) / 2; }
+__host__ __device__ inline int32_t* compact_map(int32_t* w, int n) { return w + 4 + 2 * ((n + 1) / 2); }
+
+// The holes below U and the pages in use above it, both in ascending order.
+// There are as many of one as of the other, at most n_pages / 2.
+__global__ __launch_bounds__(kCtl) void kv_compact_plan_kernel(KvCompactArgs a)
+{
+    __shared__ int part[kCtlWaves];
+    const int n = a.g.n_pages;
+    int32_t *from = compact_from(a.work), *to = compact_to(a.work, n), *map = compact_map(a.work, n);
+    int used = 0;
+    for (int at = 0; at < n; at += kScan) {
+        int step;
+        block_scan(__popc(page_bits(a.ref, at, n, [](int, int r) { return r > 0; })), part, step);
+        used += step;
+    }
+    int holes = 0, moves = 0;
+    for (int at = 0; at < n; at += kScan) {
+        // a page is a hole or a move or neither: both counts in one scan, 16 bits each (a step has 4096 pages)
+        const unsigned hole = page_bits(a.ref, at, n, [&](int p, int r) { return p < used && !(r > 0); });
+        const unsigned move = page_bits(a.ref, at, n, [&](int p, int r) { return p >= used && r > 0; });
+        int step;
+        const int both = block_scan(__popc(hole) | __popc(move) << 16, part, step);
+        int h = holes + (both & 0xffff), m = moves + (both >> 16);
+#pragma unroll
+        for (int i = 0; i < kScanPer; ++i) {
+            const int p = at + (int)threadIdx.x * kScanPer + i;
+            if (hole >> i & 1) to[h++] = p;
+            if (move >> i & 1) from[m++] = p;
+            if (p < n) {
+                map[p] = p;
+                a.ref_out[p] = p < used && !(hole >> i & 1) ? a.ref[p] : 0;
+            }
+        }
+        holes += step & 0xffff;
+        moves += step >> 16;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < moves; k += kCtl) {
+        map[from[k]] = to[k];
+        a.ref_out[to[k]] = a.ref[from[k]];
+    }
+    if (threadIdx.x == 0) a.work[0] = moves;
+}
+
+__global__ __launch_bounds__(256) void kv_compact_kernel(KvCompactArgs a)
+{
+    const int n = a.g.n_pages;
+    const int32_t *from_of = compact_from(a.work), *to_of = compact_to(a.work, n), *map = compact_map(a.work, n);
+    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < a.entries; e += (long long)gridDim.x * 256) {
+        const int id = a.table[e];
+        a.table_out[e] = held(id, n) ? map[id] : id;
+    }
+    copy_pages(static_cast<char*>(a.pool), a.g, a.work[0], [&](long long i, int& from, int& to) {
+        from = from_of[i];
+        to = to_of[i];
+        return true;
+    });
+}
+
+}  // namespace
+
+size_t kv_compact_words(int n_pages) { return 4 + 2 * (((size_t)n_pages + 1) / 2) + (size_t)n_pages; }
+
+hipError_t launch_kv_reserve(const KvReserveArgs& a, hipStream_t s)
+{
+    kv_reserve_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s)
+{
+    const long long pieces = (long long)a.K * a.g.Hkv * (a.g.row_bytes >> 4);
+    kv_append_kernel<<<dim3((unsigned)((pieces + 255) / 256), a.B), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_rollback(const KvRollbackArgs& a, hipStream_t s)
+{
+    kv_rollback_kernel<<<dim3(a.B), dim3(kCtl), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_free(const int32_t* rows, int32_t* lens, int32_t* table, int32_t* ref, int n, int B, int P,
+                          int n_pages, hipStream_t s)
+{
+    kv_free_kernel<<<dim3(n), dim3(256), 0, s>>>(rows, lens, table, ref, B, P, n_pages);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_copy(const int32_t* src, const int32_t* dst, void* pool, int n, const KvGeom& g, hipStream_t s)
+{
+    kv_copy_kernel<<<dim3(copy_grid(n, g)), dim3(256), 0, s>>>(src, dst, static_cast<char*>(pool), n, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const KvForkArgs& a, hipStream_t s)
+{
+    kv_fork_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    kv_fork_copy_kernel<<<dim3(copy_grid(a.n, a.g)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const KvCompactArgs& a, hipStream_t s)
+{
+    kv_compact_plan_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    kv_compact_kernel<<<dim3(copy_grid(a.g.n_pages / 2 + 1, a.g)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace gdn
