@@ -835,7 +835,7 @@ static int check_attn(const char* fn, int B, int K, int Hq, int Hkv, int D, int 
     REQUIRE(K <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: K = %d > %d", fn, K, gdn::kKvWindowMax);
     REQUIRE(B <= gdn::kAttnBatchMax, GDN_EUNSUPPORTED, "%s: B = %d > %d", fn, B, gdn::kAttnBatchMax);
     REQUIRE(Hq <= 1024, GDN_EUNSUPPORTED, "%s: Hq = %d > 1024", fn, Hq);
-    REQUIRE((long long)P * page < (1LL << 31), GDN_EUNSUPPORTED, "%s: %d slots of %d tokens pass 2^31", fn, P, page);
+    REQUIRE((long long)P * page <= (1LL << 30), GDN_EUNSUPPORTED, "%s: %d slots of %d tokens pass 2^30", fn, P, page);
     return GDN_OK;
 }
 

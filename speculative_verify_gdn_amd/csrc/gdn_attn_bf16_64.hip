@@ -1,0 +1,16 @@
+// gdn_attn_bf16_64.hip -- the window attention for bfloat16, head size 64.
+#include "gdn_attn_launch.h"
+
+namespace gdn {
+namespace attn {
+
+hipError_t launch_bf16_64(const AttnArgs& a, hipStream_t s)
+{
+    using M16 = Cfg<true, 64, 1, 4, 1, 1>;
+    using M32 = Cfg<true, 64, 1, 4, 1, 2>;
+    using M64 = Cfg<true, 64, 2, 2, 1, 2>;
+    return launch_all<true, 64, M16, M32, M64>(a, s);
+}
+
+}  // namespace attn
+}  // namespace gdn

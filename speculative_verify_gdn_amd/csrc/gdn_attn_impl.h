@@ -1,0 +1,898 @@
+// gdn_attn_impl.h -- the window attention over the paged cache (gdn_attn_verify),
+// instantiated per type and head size in gdn_attn_{bf16,f32}_{64,128,256}.hip.
+//
+// Mathematics.  Over any set of keys a row keeps m (a reference for its
+// exponents), l = sum e^{x-m} and the vector a = sum e^{x-m} v; sets are joined
+// by scaling both to a common m.  So a row's keys can be cut anywhere: the
+// pages that all sequences share are read once for the rows of all of them, and
+// what is left is cut evenly over the chip.
+//
+// Work list.  A unit is one tile of N keys against the M rows of one
+// key/value head.  Two lists: the shared units (head, row tile, key tile), whose
+// row tiles run through the window tokens of every sequence that holds the
+// prefix, and the sequences' own units (sequence, head, row tile, key tile).
+// Part i of n has the units [i U / n, (i+1) U / n); the workgroups take a part of each
+// list, the shared ones in their order and the own ones from the last workgroup
+// down, so that lists that are shorter than the grid meet as little as may be.  The load is
+// even whatever the lengths are, and no host knowledge of them is needed: each
+// workgroup sums the lists' lengths over the sequences by itself.  A run of
+// consecutive units of one row tile is a piece; a piece leaves (m, l, a) in the
+// workspace and a second kernel joins the pieces of each row, except where one
+// piece is all there is.  Consecutive workgroups sit on one XCD, so row tiles
+// that read the same keys at the same time share its L2.
+//
+// A tile.  K and V rows go from memory straight into LDS (16 bytes a lane), one
+// tile ahead of the one being worked on.  S^T = K Q^T leaves a query row in the
+// lanes with the same lane & 15, 4 keys a register group; e^{x-m} of that layout
+// is already the operand of O^T = V^T P^T, and V^T comes out of LDS by the
+// transposing 8-byte read.  The 16-byte chunks of a row are permuted by the key's
+// low bits so that both kinds of read meet every bank once.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_kv_internal.h"
+
+namespace gdn {
+namespace attn {
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short bf16x4_t;
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
+
+constexpr int kThreads = 256;
+constexpr float kNoMax = -1e37f;   // the reference of a row that has seen no key: finite, so differences are
+constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// M rows by N keys over the 4 waves: RW groups of rows x KW groups of keys x DW parts of the output's columns;
+// a wave has MW times 16 rows
+template <bool BF16_, int D_, int RW_, int KW_, int DW_, int MW_>
+struct Cfg {
+    static constexpr bool BF16 = BF16_;
+    static constexpr int D = D_, RW = RW_, KW = KW_, DW = DW_, MW = MW_;
+    static_assert(RW * KW * DW == 4, "four waves");
+    static constexpr int M = 16 * MW * RW;
+    static constexpr int ES = BF16 ? 2 : 4, ROW = D * ES, CH = ROW / 16;
+    static constexpr int N = 8192 / D;             // keys a tile: K and V are 32 KB in bf16, 64 KB in fp32
+    static constexpr int KF = N / KW / 16;         // 16-key groups of a wave
+    static constexpr int DB = D / 16 / DW;         // 16-column groups of a wave's output
+    static constexpr int MAT = N * ROW, STAGE = 2 * MAT;
+    static constexpr int QC = BF16 ? D / 32 : D / 16;  // registers groups of a row's q
+};
+
+// where each 16-byte chunk of a key's row sits: chunk ^ swizzle(key)
+template <class C>
+__device__ __forceinline__ constexpr int k_swizzle(int key) { return C::CH >= 16 ? (key & 15) : ((key >> 1) & 7); }
+template <class C>
+__device__ __forceinline__ constexpr int v_swizzle(int key)
+{
+    if constexpr (!C::BF16) return ((key >> 2) & 3) << 2;
+    else return C::CH >= 16 ? (key & 7) << 1 : ((key >> 1) & 3) << 1;
+}
+
+// what a sequence asks for
+struct Seq {
+    int cnt, len, end, start, tiles, rts;
+    bool part;
+    long long units;
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
+{
+    Seq s;
+    const int cap = a.P << a.page_log2;
+    s.cnt = a.count ? min(max(a.count[b], 0), a.K) : a.K;
+    s.len = min(max(a.lens[b], 0), cap);
+    s.end = (int)min((long long)s.len + s.cnt, (long long)cap);
+    s.part = a.prefix > 0 && s.len >= a.prefix && s.cnt > 0;
+    s.start = s.part ? a.prefix : 0;
+    s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) / N : 0;
+    s.rts = (s.cnt * (a.Hq / a.Hkv) + M - 1) / M;
+    s.units = (long long)a.Hkv * s.rts * s.tiles;
+    return s;
+}
+
+// the lists' lengths, for the joining kernel
+struct Head {
+    long long shared_units, own_units;
+    int shared_parts, own_parts;
+};
+struct PlanSeq {
+    long long own_base;  // own units of the sequences before
+    int tok_base, pad;   // window tokens of the prefix-holding sequences before (-1: not one of them)
+};
+
+// workspace: Head | PlanSeq[B] | (m, l) of shared rows | of own rows | a of shared rows | of own rows
+struct Layout {
+    size_t plan, ml_s, ml_o, o_s, o_o, bytes;
+};
+__host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+__host__ __device__ inline Layout layout(const AttnArgs& a, int nb, int MS, int MO)
+{
+    const size_t G = a.Hq / a.Hkv;
+    const size_t slots_s = MS ? nb + a.Hkv * (((size_t)a.B * a.K * G + MS - 1) / MS) : 0;
+    const size_t slots_o = nb + (size_t)a.B * a.Hkv * ((a.K * G + MO - 1) / MO);
+    Layout w;
+    w.plan = up256(sizeof(Head));
+    w.ml_s = up256(w.plan + a.B * sizeof(PlanSeq));
+    w.ml_o = up256(w.ml_s + slots_s * MS * 8);
+    w.o_s = up256(w.ml_o + slots_o * MO * 8);
+    w.o_o = w.o_s + slots_s * MS * a.D * 4;
+    w.bytes = w.o_o + slots_o * MO * a.D * 4;
+    return w;
+}
+
+// first unit of part i of n, and the part of a unit
+__device__ __forceinline__ long long first_unit(long long units, int n, int i) { return units * i / n; }
+__device__ __forceinline__ int block_of(long long units, int n, long long u) { return (int)(((u + 1) * n - 1) / units); }
+// (a list is cut in no more parts than it has units, so that none is empty)
+__device__ __forceinline__ int parts_for(int nb, long long units) { return units < nb ? (int)units : nb; }
+
+// ---------------------------------------------------------------- pieces of a tile
+// 1 KB of global memory to LDS: lane l's 16 bytes go to lds + 16 l.  Written as assembly because the
+// compiler would otherwise wait for the tile on its way before it reads the tile that is there; nothing
+// is returned in registers, and load_wait() below waits for all of them.  (m0 takes the LDS address; one
+// wait state between writing it and the load.)
+__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t voff, const char* base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(voff), "s"(base)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ void load_wait()
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+__device__ __forceinline__ void block_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 lds_read16(uint32_t at)
+{
+    typedef __attribute__((address_space(3))) const f32x4_t lds_f4;
+    return __builtin_bit_cast(uint4, *(lds_f4*)(lds_char*)(uintptr_t)at);
+}
+
+__device__ __forceinline__ float lds_read4(uint32_t at)
+{
+    typedef __attribute__((address_space(3))) const float lds_f1;
+    return *(lds_f1*)(lds_char*)(uintptr_t)at;
+}
+
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ long long uni64(long long v)
+{
+    return (long long)((unsigned long long)(unsigned)uni((int)(v >> 32)) << 32 | (unsigned)uni((int)v));
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// two floats to bf16 (to nearest), packed
+__device__ __forceinline__ uint32_t pack2(float x, float y)
+{
+    const bf16x2_t h = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+// nodes on the path from a root to each node: lane i returns those of node i (called by a whole wave, K <= 64)
+__device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, int K)
+{
+    const int lane = threadIdx.x & 63;
+    int up = -1;
+    if (lane < K) {
+        const int p = parent ? parent[lane] : lane - 1;
+        up = p >= 0 && p < lane ? p : -1;
+    }
+    unsigned long long path = 1ull << lane;
+#pragma unroll
+    for (int d = 1; d < kKvWindowMax; d <<= 1) {
+        const int from = max(up, 0);
+        const unsigned long long more = __shfl(path, from, 64);
+        const int far = __shfl(up, from, 64);
+        if (up >= 0) {
+            path |= more;
+            up = far;
+        }
+    }
+    return path;
+}
+
+// LDS beside the tiles
+struct Small {
+    int part[4];
+    long long lpart[4];
+    int found_b;
+    long long found_off;
+    int bad_value;
+    int tok[132];             // window tokens (b * K + t) of a shared row tile
+    float2 ml[4][64];         // (m, l) of the waves' rows, to be joined
+};
+
+struct PieceIn {
+    const int32_t* row;       // table row
+    const int32_t* parent;    // of the sequence, or nullptr
+    int h, p0, tiles;         // key/value head, first position, tiles
+    int len, end;             // window's first position and the end of what is there
+    bool window;              // keys at len.. are seen by their descendants only
+};
+
+struct PieceOut {
+    bool direct;              // the whole row: o and lse at once
+    float* o;                 // [M][D]
+    float2* ml;               // [M]
+};
+
+// a row of the tile: token b * K + t, t, and the query head of its group; false for a row that is not there
+struct RowId {
+    int tok, t, g;
+    bool live;
+};
+
+template <class C, class RowFn>
+__device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s, const PieceIn& in,
+                                          const PieceOut& out, RowFn row_of)
+{
+    constexpr int MW = C::MW, KF = C::KF, DB = C::DB, QC = C::QC, N = C::N;
+    const int lane = threadIdx.x & 63, w = uni(threadIdx.x >> 6);
+    const int rw = w % C::RW, kw = (w / C::RW) % C::KW, dw = w / (C::RW * C::KW);
+    const int n16 = lane & 15, grp = lane >> 4;
+    const int page_mask = (1 << a.page_log2) - 1;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)sm;
+    const int G = a.Hq / a.Hkv;
+
+    // ---- the pages: lane i holds slot first + i (a missing one as page 0, flagged), and the 64 slots after
+    auto slot_id = [&](int sl, bool& bad) {
+        int id = sl < a.P ? in.row[sl] : -1;
+        bad = (unsigned)id >= (unsigned)a.n_pages;
+        return bad ? 0 : id;
+    };
+    int first = in.p0 >> a.page_log2;
+    bool bad_lane, bad_lane2;
+    int ids = slot_id(first + lane, bad_lane), ids2 = slot_id(first + 64 + lane, bad_lane2);
+    unsigned long long bad = __ballot(bad_lane), bad2 = __ballot(bad_lane2);
+
+    // ---- tile loads: wave w brings the keys w N/4 .. of K and V
+    constexpr int KPI = 1024 / C::ROW, NI = N / 4 / KPI;
+    const size_t page_bytes = ((size_t)a.Hkv << a.page_log2) * C::ROW;
+    const size_t head_off = ((size_t)in.h << a.page_log2) * C::ROW;
+    const int lkey = lane / C::CH, lch = lane % C::CH;
+    auto issue = [&](int j, int buf) {
+        const int pt = in.p0 + j * N;
+        int s0 = (pt >> a.page_log2) - first;
+        if (s0 >= 64) {
+            ids = ids2;
+            bad = bad2;
+            first += 64;
+            s0 -= 64;
+            ids2 = slot_id(first + 64 + lane, bad_lane2);
+            bad2 = __ballot(bad_lane2);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int key = w * (N / 4) + i * KPI;
+            const int id = __builtin_amdgcn_readlane(ids, s0 + (key >> a.page_log2));
+            const size_t off = (size_t)id * page_bytes + head_off + (size_t)((pt + key) & page_mask) * C::ROW;
+            const uint32_t vk = lkey * C::ROW + ((lch ^ k_swizzle<C>(key + lkey)) << 4);
+            const uint32_t vv = lkey * C::ROW + ((lch ^ v_swizzle<C>(key + lkey)) << 4);
+            const uint32_t to = lds0 + buf * C::STAGE + key * C::ROW;
+            load_lds(to, vk, static_cast<const char*>(a.k_pages) + off);
+            load_lds(to + C::MAT, vv, static_cast<const char*>(a.v_pages) + off);
+        }
+        const int slots = max(N >> a.page_log2, 1);
+        return (unsigned)(bad >> s0) & ((1u << slots) - 1);   // missing pages of the tile
+    };
+    unsigned miss_next = issue(0, 0);
+
+    // ---- the rows
+    float m[MW], l[MW];
+    unsigned long long sees[MW];
+    RowId id[MW];
+    uint4 q[MW][QC];
+    const float c = fabsf(a.scale) * kLog2e;
+    const uint32_t flip = a.scale < 0.f ? (C::BF16 ? 0x80008000u : 0x80000000u) : 0u;  // the sign goes into q
+    const unsigned long long path = in.window ? ancestors(in.parent, a.K) : 0;
+#pragma unroll
+    for (int r = 0; r < MW; ++r) {
+        id[r] = row_of((rw * MW + r) * 16 + n16);
+        m[r] = kNoMax;
+        l[r] = 0.f;
+        sees[r] = __shfl(path, id[r].t & 63, 64);
+        const char* qp = static_cast<const char*>(a.q) +
+                         ((size_t)id[r].tok * a.q_stride + (size_t)(in.h * G + id[r].g) * C::D) * C::ES + grp * 16;
+#pragma unroll
+        for (int e = 0; e < QC; ++e) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (id[r].live) u = *reinterpret_cast<const uint4*>(qp + e * 64);
+            q[r][e] = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+        }
+    }
+    f32x4_t o[DB][MW];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < MW; ++r) o[d][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    // LDS addresses of this lane within a tile: chunk c of a row sits at its lane's chunk with the low bits of c
+    // flipped in, and further chunks, keys and 16-key groups lie at constant distances
+    const int kbase = kw * (N / C::KW);
+    const int vkey = C::BF16 ? 4 * grp + (n16 >> 2) : 4 * grp;   // (fp32 adds the register's index)
+    const uint32_t k_lane = lds0 + (kbase + n16) * C::ROW + ((grp ^ k_swizzle<C>(n16)) << 4);
+    const uint32_t v_lane =
+        lds0 + C::MAT + (kbase + vkey) * C::ROW + dw * (DB * 16 * C::ES) +
+        (C::BF16 ? ((((n16 >> 1) & 1) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 1) * 8
+                 : (((n16 >> 2) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 3) * 4);
+    static_assert(C::DW == 1 || (DB * 16 * C::ES) % 256 == 0, "a part's columns start on whole swizzle groups");
+
+    for (int j = 0; j < in.tiles; ++j) {
+        const unsigned miss = miss_next;
+        load_wait();
+        block_barrier();   // every wave's part of this tile is there, and nobody reads the other buffer any more
+        if (j + 1 < in.tiles) miss_next = issue(j + 1, (j + 1) & 1);
+        char* kt = sm + (j & 1) * C::STAGE;
+        char* vt = kt + C::MAT;
+        const int pt = in.p0 + j * N;
+        const bool masked = miss != 0 || (in.window && pt + N > in.len) || pt + N > in.end;
+
+        // Values nobody may see are cleared where they lie (0 times NaN is NaN), and a window value that some
+        // row sees but is not finite is noted: rows that do not see it must not meet it either.
+        bool poison = false;
+        if (masked) {
+            if (threadIdx.x == 0) s.bad_value = 0;
+            block_barrier();
+            for (int e = threadIdx.x; e < N * C::CH; e += kThreads) {
+                const int key = e / C::CH, pos = pt + key;
+                uint4* v = reinterpret_cast<uint4*>(vt + e * 16);
+                if (pos >= in.end || (miss >> (key >> a.page_log2) & 1)) *v = make_uint4(0, 0, 0, 0);
+                else if (in.window && pos >= in.len) {
+                    const uint4 u = *v;
+                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        odd |= (x[i] & 0x7f800000u) == 0x7f800000u;
+                        if (C::BF16) odd |= (x[i] & 0x7f80u) == 0x7f80u;
+                    }
+                    if (odd) s.bad_value = 1;
+                }
+            }
+            block_barrier();
+            poison = uni(s.bad_value) != 0;
+        }
+
+        // opaque, so that the addresses are formed from them in the loop and not kept in dozens of registers
+        uint32_t k_at = k_lane + (j & 1) * C::STAGE, v_at = v_lane + (j & 1) * C::STAGE;
+        asm volatile("" : "+v"(k_at), "+v"(v_at));
+
+        // ---- S^T = K Q^T
+        f32x4_t x[KF][MW];
+#pragma unroll
+        for (int k = 0; k < KF; ++k)
+#pragma unroll
+            for (int r = 0; r < MW; ++r) x[k][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < QC; ++e)
+#pragma unroll
+            for (int k = 0; k < KF; ++k) {
+                const uint4 u = lds_read16((k_at ^ (uint32_t)(((4 * e) & (C::CH - 1) & 15) << 4)) +
+                                           (4 * e / 16) * 256 + 16 * k * C::ROW);
+#pragma unroll
+                for (int r = 0; r < MW; ++r) {
+                    if constexpr (C::BF16) {
+                        x[k][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u),
+                                                                          __builtin_bit_cast(bf16x8_t, q[r][e]),
+                                                                          x[k][r], 0, 0, 0);
+                    } else {
+                        const uint32_t ua[4] = {u.x, u.y, u.z, u.w};
+                        const uint32_t qa[4] = {q[r][e].x, q[r][e].y, q[r][e].z, q[r][e].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[k][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ua[i]),
+                                                                           __uint_as_float(qa[i]), x[k][r], 0, 0, 0);
+                    }
+                }
+            }
+
+        // ---- weights e^{x-m}
+        unsigned seen[MW];   // of a masked tile: a bit for each of this lane's keys
+        if (masked) {
+#pragma unroll
+            for (int r = 0; r < MW; ++r) {
+                seen[r] = 0;
+#pragma unroll
+                for (int k = 0; k < KF; ++k) {
+                    const int key = kbase + 16 * k + 4 * grp;
+                    // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
+                    // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
+                    const int rel = pt + key - in.len, left = in.end - (pt + key);
+                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees[r] >> (max(rel, 0) & 63));
+                    const int old = min(max(-rel, 0), 4);
+                    unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
+                    bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
+                    seen[r] |= bits << (4 * k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[k][r][i] = (bits >> i & 1) ? x[k][r][i] : -INFINITY;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < MW; ++r) {
+            float t = x[0][r][0];
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t = fmaxf(t, x[k][r][i]);
+            if (__any(t * c > m[r] + kSlack)) {
+                t = fmaxf(t, __shfl_xor(t, 16, 64));
+                t = fmaxf(t, __shfl_xor(t, 32, 64));
+                // a row moves its reference by its own keys alone, so its bits depend on no other row
+                const float mn = t * c > m[r] + kSlack ? t * c : m[r], f = exp2_(m[r] - mn);
+                m[r] = mn;
+                l[r] *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d][r] *= f;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float p = exp2_(__builtin_fmaf(x[k][r][i], c, -m[r]));
+                    if (masked) p = (seen[r] >> (4 * k + i) & 1) ? p : 0.f;
+                    x[k][r][i] = p;
+                    sum += p;
+                }
+            l[r] += sum;
+        }
+
+        if (poison) {
+            // what is not finite reaches the rows that see it by itself, then leaves the tile
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma nounroll
+                for (int kk = 0; kk < 16; ++kk) {
+                    const int key = kbase + 16 * k + kk;
+                    if (pt + key < in.len || pt + key >= in.end) continue;
+                    const int from = (kk >> 2) * 16 + n16;
+                    float p[MW];
+                    bool v[MW];
+#pragma unroll
+                    for (int r = 0; r < MW; ++r) {
+                        const float p0 = __shfl(x[k][r][0], from, 64), p1 = __shfl(x[k][r][1], from, 64);
+                        const float p2 = __shfl(x[k][r][2], from, 64), p3 = __shfl(x[k][r][3], from, 64);
+                        p[r] = kk & 2 ? (kk & 1 ? p3 : p2) : (kk & 1 ? p1 : p0);
+                        v[r] = __shfl((int)seen[r], from, 64) >> (4 * k + (kk & 3)) & 1;
+                    }
+                    const char* vrow = vt + key * C::ROW;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const int col = (dw * DB + d) * 16 + 4 * grp;   // 4 columns of one chunk
+                        const int at = ((col * C::ES / 16) ^ v_swizzle<C>(key)) * 16 + col * C::ES % 16;
+                        const float4 y = load4<C::BF16>(vrow + at, 0);
+                        const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int r = 0; r < MW; ++r)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (v[r] && !(fabsf(ya[i]) < INFINITY)) o[d][r][i] += p[r] * ya[i];
+                        asm volatile("" ::: "memory");   // one group's loads at a time: this path is rare
+                    }
+                }
+            block_barrier();
+            for (int e = threadIdx.x; e < N * C::CH; e += kThreads) {
+                const int pos = pt + e / C::CH;
+                if (pos < in.len || pos >= in.end) continue;
+                uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t u = v[i];
+                    if ((u & 0x7f800000u) == 0x7f800000u) u &= C::BF16 ? 0xffffu : 0u;
+                    if (C::BF16 && (u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+                    v[i] = u;
+                }
+            }
+            block_barrier();
+        }
+
+        // ---- O^T += V^T P^T
+        if constexpr (C::BF16) {
+            // the weights enter the product in bf16, as v is: half a step of 2^-8 each, unbiased
+            auto v_frag = [&](int k, int d) {
+                lds_char* at = (lds_char*)(uintptr_t)((v_at ^ (uint32_t)((d & (C::CH / 2 - 1) & 7) << 5)) +
+                                                      (d / 8) * 256 + 16 * k * C::ROW);
+                return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at));
+            };
+            if constexpr (KF == 1) {
+                uint2 p[MW];
+#pragma unroll
+                for (int r = 0; r < MW; ++r)
+                    p[r] = make_uint2(pack2(x[0][r][0], x[0][r][1]), pack2(x[0][r][2], x[0][r][3]));
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const bf16x4_t v = __builtin_bit_cast(bf16x4_t, v_frag(0, d));
+#pragma unroll
+                    for (int r = 0; r < MW; ++r)
+                        o[d][r] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, __builtin_bit_cast(bf16x4_t, p[r]),
+                                                                            o[d][r], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KF; k += 2) {
+                    uint4 p[MW];
+#pragma unroll
+                    for (int r = 0; r < MW; ++r)
+                        p[r] = make_uint4(pack2(x[k][r][0], x[k][r][1]), pack2(x[k][r][2], x[k][r][3]),
+                                          pack2(x[k + 1][r][0], x[k + 1][r][1]), pack2(x[k + 1][r][2], x[k + 1][r][3]));
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const uint2 v0 = v_frag(k, d), v1 = v_frag(k + 1, d);
+                        const bf16x8_t v = __builtin_bit_cast(bf16x8_t, make_uint4(v0.x, v0.y, v1.x, v1.y));
+#pragma unroll
+                        for (int r = 0; r < MW; ++r)
+                            o[d][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, p[r]),
+                                                                              o[d][r], 0, 0, 0);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = lds_read4((v_at ^ (uint32_t)((d & 3) << 6)) + (d / 4) * 256 +
+                                                  (16 * k + i) * C::ROW);
+#pragma unroll
+                        for (int r = 0; r < MW; ++r)
+                            o[d][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, x[k][r][i], o[d][r], 0, 0, 0);
+                    }
+        }
+    }
+
+    // ---- the four lane groups' sums, then the waves of other keys, in a fixed order
+#pragma unroll
+    for (int r = 0; r < MW; ++r) {
+        l[r] += __shfl_xor(l[r], 16, 64);
+        l[r] += __shfl_xor(l[r], 32, 64);
+    }
+    block_barrier();   // the tiles are done with
+    if constexpr (C::KW > 1) {
+        constexpr int F = DB * MW;
+        float* box = reinterpret_cast<float*>(sm);
+        auto at = [&](int k, int f) {
+            return reinterpret_cast<f32x4_t*>(box + ((((k - 1) * C::DW + dw) * C::RW + rw) * F + f) * 256 + lane * 4);
+        };
+        if (kw > 0) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < MW; ++r) *at(kw, d * MW + r) = o[d][r];
+            if (grp == 0)
+#pragma unroll
+                for (int r = 0; r < MW; ++r) s.ml[w][r * 16 + n16] = make_float2(m[r], l[r]);
+        }
+        block_barrier();
+        if (kw == 0) {
+            for (int k = 1; k < C::KW; ++k) {
+#pragma unroll
+                for (int r = 0; r < MW; ++r) {
+                    const float2 v = s.ml[w + k * C::RW][r * 16 + n16];
+                    const float mn = fmaxf(m[r], v.x), f = exp2_(m[r] - mn), g = exp2_(v.x - mn);
+                    m[r] = mn;
+                    l[r] = l[r] * f + v.y * g;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[d][r] = o[d][r] * f + *at(k, d * MW + r) * g;
+                }
+            }
+        }
+        block_barrier();   // the next piece's tiles may come
+        if (kw > 0) return;
+    }
+#pragma unroll
+    for (int r = 0; r < MW; ++r) {
+        if (!id[r].live) continue;
+        const int row = (rw * MW + r) * 16 + n16;
+        if (out.direct) {
+            const size_t at = (size_t)id[r].tok * a.Hq + in.h * G + id[r].g;
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const f32x4_t y = o[d][r] * inv;
+                const size_t e = at * C::D + (dw * DB + d) * 16 + 4 * grp;
+                if constexpr (C::BF16) {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
+                        make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+                } else {
+                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.o) + e) = y;
+                }
+            }
+            if (a.lse && dw == 0 && grp == 0) a.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + __log2f(l[r])) * kLn2;
+        } else {
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                *reinterpret_cast<f32x4_t*>(out.o + (size_t)row * C::D + (dw * DB + d) * 16 + 4 * grp) = o[d][r];
+            if (dw == 0 && grp == 0) out.ml[row] = make_float2(m[r], l[r]);
+        }
+    }
+}
+
+// exclusive sums over the workgroup's threads (256), and the totals
+__device__ __forceinline__ int scan_int(int v, Small& s, int& total)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += u;
+    }
+    __syncthreads();
+    if (lane == 63) s.part[w] = inc;
+    __syncthreads();
+    int base = 0;
+    total = 0;
+    for (int i = 0; i < 4; ++i) {
+        base += i < w ? s.part[i] : 0;
+        total += s.part[i];
+    }
+    return base + inc - v;
+}
+
+__device__ __forceinline__ long long scan_long(long long v, Small& s, long long& total)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    long long inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long long u = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += u;
+    }
+    __syncthreads();
+    if (lane == 63) s.lpart[w] = inc;
+    __syncthreads();
+    long long base = 0;
+    total = 0;
+    for (int i = 0; i < 4; ++i) {
+        base += i < w ? s.lpart[i] : 0;
+        total += s.lpart[i];
+    }
+    return base + inc - v;
+}
+
+// SH: the shared list's configuration, or void
+template <class OW, class SH>
+__global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnArgs a, int nb)
+{
+    // all of LDS is asked for at the launch and starts at 0: the swizzled addresses flip bits below 256
+    extern __shared__ __attribute__((aligned(1024))) char sm[];
+    Small& s = *reinterpret_cast<Small*>(sm + 2 * OW::STAGE);
+    constexpr bool kShared = !__is_same(SH, void);
+    const int G = a.Hq / a.Hkv;
+    int MS = 0;
+    if constexpr (kShared) MS = SH::M;
+    const Layout wk = layout(a, nb, MS, OW::M);
+    char* work = static_cast<char*>(a.work);
+
+    // ---- the lists' lengths: thread i sums the sequences [b0, b1)
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+    long long mine = 0;
+    int toks = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Seq q = seq_of(a, b, OW::N, OW::M);
+        mine += q.units;
+        if (q.part) toks += q.cnt;
+    }
+    long long own;
+    const long long own_base = scan_long(mine, s, own);
+    own = uni64(own);
+    int tok_total = 0, tok_base = 0;
+    long long shared = 0;
+    int row_tiles = 0, key_tiles = 0;
+    if constexpr (kShared) {
+        tok_base = scan_int(toks, s, tok_total);
+        tok_total = uni(tok_total);
+        row_tiles = (int)(((long long)tok_total * G + SH::M - 1) / SH::M);
+        key_tiles = (a.prefix + SH::N - 1) / SH::N;
+        shared = (long long)a.Hkv * row_tiles * key_tiles;
+    }
+    const int shared_parts = parts_for(nb, shared), own_parts = parts_for(nb, own);
+    const int blocks = parts_for(nb, shared + own);
+    // consecutive workgroups of the lists on one XCD (workgroups are dealt to the 8 XCDs in turn)
+    const int per_xcd = (blocks + 7) / 8;
+    const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{shared, own, shared_parts, own_parts};
+        PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + wk.plan);
+        long long base = own_base;
+        int tok = tok_base;
+        for (int b = b0; b < b1; ++b) {
+            const Seq q = seq_of(a, b, OW::N, OW::M);
+            plan[b] = PlanSeq{base, q.part ? tok : -1, 0};
+            base += q.units;
+            tok += q.part ? q.cnt : 0;
+        }
+    }
+    if ((int)(blockIdx.x >> 3) >= per_xcd || lb >= blocks) return;
+
+    if constexpr (kShared) {
+        long long u = lb < shared_parts ? first_unit(shared, shared_parts, lb) : 0;
+        const long long u1 = lb < shared_parts ? first_unit(shared, shared_parts, lb + 1) : 0;
+        while (u < u1) {
+            const int seg = (int)(u / key_tiles), k0 = (int)(u - (long long)seg * key_tiles);
+            const int nt = (int)min((long long)(key_tiles - k0), u1 - u);
+            const int h = seg / row_tiles, rt = seg - h * row_tiles;
+            // the tile's tokens
+            const int r0 = rt * SH::M, t0 = r0 / G;
+            const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
+            __syncthreads();
+            int tok = tok_base;
+            for (int b = b0; b < b1 && tok < t1; ++b) {
+                const Seq q = seq_of(a, b, OW::N, OW::M);
+                if (!q.part) continue;
+                for (int t = max(0, t0 - tok); t < q.cnt && tok + t < t1; ++t) s.tok[tok + t - t0] = b * a.K + t;
+                tok += q.cnt;
+            }
+            __syncthreads();
+            const int lead = uni(s.tok[0] / a.K);
+            PieceIn in{a.table + (size_t)lead * a.P, nullptr, h, k0 * SH::N, nt, a.prefix, a.prefix, false};
+            const size_t slot = (size_t)lb + seg;
+            PieceOut out{false, reinterpret_cast<float*>(work + wk.o_s) + slot * SH::M * SH::D,
+                         reinterpret_cast<float2*>(work + wk.ml_s) + slot * SH::M};
+            run_piece<SH>(a, sm, s, in, out, [&](int r) {
+                RowId id{0, 0, 0, false};
+                const int t = (r0 + r) / G;
+                id.live = t < t1;
+                if (id.live) {
+                    id.tok = s.tok[t - t0];
+                    id.t = id.tok % a.K;
+                    id.g = (r0 + r) - t * G;
+                }
+                return id;
+            });
+            u += nt;
+        }
+    }
+
+    const int part = blocks - 1 - lb;
+    if (part >= own_parts) return;
+    long long u = first_unit(own, own_parts, part);
+    const long long u1 = first_unit(own, own_parts, part + 1);
+    // the sequence of the first unit
+    __syncthreads();
+    if (own_base <= u && u < own_base + mine) {
+        long long base = own_base;
+        for (int b = b0; b < b1; ++b) {
+            const Seq q = seq_of(a, b, OW::N, OW::M);
+            if (u < base + q.units) {
+                s.found_b = b;
+                s.found_off = u - base;
+                break;
+            }
+            base += q.units;
+        }
+    }
+    __syncthreads();
+    int b = uni(s.found_b);
+    long long off = uni64(s.found_off);
+    while (u < u1) {
+        const Seq q = seq_of(a, b, OW::N, OW::M);
+        const int tiles = uni(q.tiles), rts = uni(q.rts);
+        if (off >= (long long)a.Hkv * rts * tiles) {
+            off = 0;
+            ++b;
+            continue;
+        }
+        const int seg = (int)(off / tiles), k0 = (int)(off - (long long)seg * tiles);
+        const int nt = (int)min((long long)(tiles - k0), u1 - u);
+        const int h = seg / rts, rt = seg - h * rts;
+        const int RT = (a.K * G + OW::M - 1) / OW::M;
+        const size_t slot = (size_t)part + ((size_t)b * a.Hkv + h) * RT + rt;
+        PieceIn in{a.table + (size_t)b * a.P, a.parent ? a.parent + (size_t)b * a.K : nullptr, h,
+                   uni(q.start) + k0 * OW::N, nt, uni(q.len), uni(q.end), true};
+        PieceOut out{uni(q.part) == 0 && nt == tiles, reinterpret_cast<float*>(work + wk.o_o) + slot * OW::M * OW::D,
+                     reinterpret_cast<float2*>(work + wk.ml_o) + slot * OW::M};
+        const int r0 = rt * OW::M, cnt = uni(q.cnt);
+        run_piece<OW>(a, sm, s, in, out, [&](int r) {
+            RowId id{0, 0, 0, false};
+            const int t = (r0 + r) / G;
+            id.live = t < cnt;
+            if (id.live) {
+                id.tok = b * a.K + t;
+                id.t = t;
+                id.g = (r0 + r) - t * G;
+            }
+            return id;
+        });
+        u += nt;
+        off += nt;
+    }
+}
+
+// ---------------------------------------------------------------- joining
+// A wave per row: lanes hold the pieces' (m, l) first, then the columns.
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int nb, int MS, int MO, int N)
+{
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const long long row = (long long)blockIdx.x * 4 + uni(threadIdx.x >> 6);
+    if (row >= (long long)a.B * a.K * a.Hq) return;
+    const int G = a.Hq / a.Hkv;
+    const int tok = (int)(row / a.Hq), hq = (int)(row - (long long)tok * a.Hq);
+    const int b = tok / a.K, t = tok - b * a.K, h = hq / G, g = hq - h * G;
+    const Seq q = seq_of(a, b, N, MO);
+    if (t >= q.cnt) return;
+    const Layout wk = layout(a, nb, MS, MO);
+    const char* work = static_cast<const char*>(a.work);
+    const Head head = *reinterpret_cast<const Head*>(work);
+    const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + wk.plan)[b];
+
+    int n_s = 0, n_o = 0;
+    size_t at_s = 0, at_o = 0, step_s = MS, step_o = MO;   // first row in the workspace, rows to the next piece
+    if (plan.tok_base >= 0 && head.shared_units > 0) {
+        const int r = (plan.tok_base + t) * G + g, rt = r / MS;
+        const int key_tiles = (a.prefix + N - 1) / N;
+        const int row_tiles = (int)(head.shared_units / ((long long)a.Hkv * key_tiles));
+        const long long seg = (long long)h * row_tiles + rt;
+        const int l0 = block_of(head.shared_units, head.shared_parts, seg * key_tiles);
+        const int l1 = block_of(head.shared_units, head.shared_parts, (seg + 1) * key_tiles - 1);
+        n_s = l1 - l0 + 1;
+        at_s = (size_t)(l0 + seg) * MS + (r - rt * MS);
+    }
+    if (q.tiles > 0) {
+        const int r = t * G + g, rt = r / MO, RT = (a.K * G + MO - 1) / MO;
+        const long long u = plan.own_base + ((long long)h * q.rts + rt) * q.tiles;
+        const int l0 = block_of(head.own_units, head.own_parts, u);
+        const int l1 = block_of(head.own_units, head.own_parts, u + q.tiles - 1);
+        n_o = l1 - l0 + 1;
+        at_o = ((size_t)l0 + ((size_t)b * a.Hkv + h) * RT + rt) * MO + (r - rt * MO);
+        if (n_o == 1 && !q.part) return;   // written by its one piece
+    }
+    const float2* ml_s = reinterpret_cast<const float2*>(work + wk.ml_s);
+    const float2* ml_o = reinterpret_cast<const float2*>(work + wk.ml_o);
+    const float* o_s = reinterpret_cast<const float*>(work + wk.o_s);
+    const float* o_o = reinterpret_cast<const float*>(work + wk.o_o);
+    const int n = n_s + n_o;
+    float M = kNoMax, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const int i = i0 + lane;
+        float2 v = make_float2(kNoMax, 0.f);
+        if (i < n) v = i < n_s ? ml_s[at_s + i * step_s] : ml_o[at_o + (i - n_s) * step_o];
+        float mx = v.x;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
+        const float mn = fmaxf(M, mx), f = exp2_(M - mn), wgt = exp2_(v.x - mn);
+        float sum = v.y * wgt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        M = mn;
+        L = L * f + sum;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+        const int last = min(64, n - i0);
+#pragma unroll 4
+        for (int k = 0; k < last; ++k) {
+            const int p = i0 + k;
+            const float* src = p < n_s ? o_s + (at_s + p * step_s) * D : o_o + (at_o + (p - n_s) * step_o) * D;
+            const float wk_ = __shfl(wgt, k, 64);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(src[lane * E + e], wk_, acc[e]);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int e = 0; e < E; ++e) store1<BF16>(a.o, (size_t)row * D + lane * E + e, acc[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -1,0 +1,80 @@
+// gdn_attn_launch.h -- the instances of the window attention and the rule that
+// picks among them.
+#pragma once
+
+#include "gdn_attn_impl.h"
+
+namespace gdn {
+namespace attn {
+
+struct Pick {
+    int blocks, MS, MO;  // workgroups, rows of a shared tile (0: no shared list), rows of an own tile
+};
+
+// A tile of M rows reads its keys once for up to M rows of a key/value head; rows that are not there cost
+// matrix work only.
+inline Pick pick(const AttnArgs& a, bool bf16)
+{
+    Pick p;
+    const int G = a.Hq / a.Hkv, R = a.K * G;
+    p.blocks = bf16 ? 512 : 256;   // two workgroups fit a CU (64 KB of tiles each), one in fp32
+    p.MO = R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    p.MS = a.prefix == 0 ? 0 : 64;
+    return p;
+}
+
+hipError_t launch_bf16_64(const AttnArgs& a, hipStream_t s);
+hipError_t launch_bf16_128(const AttnArgs& a, hipStream_t s);
+hipError_t launch_bf16_256(const AttnArgs& a, hipStream_t s);
+hipError_t launch_f32_64(const AttnArgs& a, hipStream_t s);
+hipError_t launch_f32_128(const AttnArgs& a, hipStream_t s);
+hipError_t launch_f32_256(const AttnArgs& a, hipStream_t s);
+
+// more than the default 64 KB of LDS a workgroup has to be asked for, once for each kernel and device
+template <typename K>
+hipError_t allow_lds(K kernel, int bytes, unsigned long long& done)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
+    return e;
+}
+
+template <class OW, class SH>
+hipError_t launch_one(const AttnArgs& a, const Pick& p, hipStream_t s)
+{
+    static unsigned long long done = 0;
+    constexpr int lds = 2 * OW::STAGE + (int)sizeof(Small);
+    auto* kernel = attn_kernel<OW, SH>;
+    const hipError_t e = allow_lds(kernel, lds, done);
+    if (e != hipSuccess) return e;
+    kernel<<<dim3(p.blocks), dim3(kThreads), lds, s>>>(a, p.blocks);
+    return hipGetLastError();
+}
+
+template <bool BF16, int D, class M16, class M32, class M64>
+hipError_t launch_all(const AttnArgs& a, hipStream_t s)
+{
+    const Pick p = pick(a, BF16);
+    hipError_t e;
+    if (p.MS == 0)
+        e = p.MO == 16   ? launch_one<M16, void>(a, p, s)
+            : p.MO == 32 ? launch_one<M32, void>(a, p, s)
+                         : launch_one<M64, void>(a, p, s);
+    else
+        e = p.MO == 16   ? launch_one<M16, M64>(a, p, s)
+            : p.MO == 32 ? launch_one<M32, M64>(a, p, s)
+                         : launch_one<M64, M64>(a, p, s);
+    if (e != hipSuccess) return e;
+    const long long rows = (long long)a.B * a.K * a.Hq;
+    attn_join_kernel<BF16, D><<<dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s>>>(a, p.blocks, p.MS, p.MO,
+                                                                                        M16::N);
+    return hipGetLastError();
+}
+
+}  // namespace attn
+}  // namespace gdn
