@@ -846,7 +846,9 @@ int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, in
     int rc = check_attn(fn, B, K, Hq, Hkv, D, page, P, prefix_len, dtype, 1, g);
     if (rc) return rc;
     REQUIRE(bytes, GDN_EINVAL, "%s: null bytes", fn);
-    *bytes = gdn::attn_work_bytes(B, K, Hq, Hkv, D, g.page_log2, P, prefix_len, dtype == GDN_BF16);
+    const size_t need = gdn::attn_work_bytes(B, K, Hq, Hkv, D, g.page_log2, P, prefix_len, dtype == GDN_BF16);
+    REQUIRE(need > 0, GDN_EUNSUPPORTED, "%s: %d tables of %d slots pass 2^31 units of work", fn, B, P);
+    *bytes = need;
     return ok();
 }
 
@@ -871,6 +873,7 @@ int gdn_attn_verify(const void* q, long long q_stride, const void* k_pages, cons
             "%s: lens, count, parent, table and lse must be 4-byte aligned", fn);
     const bool bf16 = dtype == GDN_BF16;
     const size_t need = gdn::attn_work_bytes(B, K, Hq, Hkv, D, g.page_log2, P, prefix_len, bf16);
+    REQUIRE(need > 0, GDN_EUNSUPPORTED, "%s: %d tables of %d slots pass 2^31 units of work", fn, B, P);
     REQUIRE(workspace_bytes >= need, GDN_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
     const size_t plane = (size_t)n_pages * g.page_bytes(), rows = (size_t)B * K;
     const Span outs[] = {Span{o, rows * token * es}, Span{lse, lse ? rows * Hq * 4 : 0}, Span{workspace, need}};

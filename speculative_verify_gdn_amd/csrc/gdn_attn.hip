@@ -4,6 +4,7 @@
 
 namespace gdn {
 
+// 0 where the work lists would have more units than 32 bits count
 size_t attn_work_bytes(int B, int K, int Hq, int Hkv, int D, int page_log2, int P, int prefix, bool bf16)
 {
     AttnArgs a{};
@@ -16,7 +17,7 @@ size_t attn_work_bytes(int B, int K, int Hq, int Hkv, int D, int page_log2, int 
     a.P = P;
     a.prefix = prefix;
     const attn::Pick p = attn::pick(a, bf16);
-    return attn::layout(a, p.blocks, p.MS, p.MO).bytes;
+    return attn::countable(a, p, 8192 / D) ? attn::layout(a, p.blocks, p.MS, p.MO).bytes : 0;
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool bf16, hipStream_t s)

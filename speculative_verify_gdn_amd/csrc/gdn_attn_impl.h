@@ -75,7 +75,7 @@ __device__ __forceinline__ constexpr int v_swizzle(int key)
 struct Seq {
     int cnt, len, end, start, tiles, rts;
     bool part;
-    long long units;
+    int units;
 };
 
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
@@ -89,18 +89,18 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
     s.start = s.part ? a.prefix : 0;
     s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) / N : 0;
     s.rts = (s.cnt * (a.Hq / a.Hkv) + M - 1) / M;
-    s.units = (long long)a.Hkv * s.rts * s.tiles;
+    s.units = a.Hkv * s.rts * s.tiles;
     return s;
 }
 
-// the lists' lengths, for the joining kernel
+// the lists' lengths and cuts, for the joining kernel
 struct Head {
-    long long shared_units, own_units;
+    int shared_units, own_units;
     int shared_parts, own_parts;
 };
 struct PlanSeq {
-    long long own_base;  // own units of the sequences before
-    int tok_base, pad;   // window tokens of the prefix-holding sequences before (-1: not one of them)
+    int own_base;   // own units of the sequences before
+    int tok_base;   // window tokens of the prefix-holding sequences before (-1: not one of them)
 };
 
 // workspace: Head | PlanSeq[B] | (m, l) of shared rows | of own rows | a of shared rows | of own rows
@@ -123,11 +123,20 @@ __host__ __device__ inline Layout layout(const AttnArgs& a, int nb, int MS, int 
     return w;
 }
 
-// first unit of part i of n, and the part of a unit
-__device__ __forceinline__ long long first_unit(long long units, int n, int i) { return units * i / n; }
-__device__ __forceinline__ int block_of(long long units, int n, long long u) { return (int)(((u + 1) * n - 1) / units); }
+// Part i of n parts of U units has the units floor(U i / n) .. floor(U (i+1) / n) - 1, so unit u is in part
+// floor(((u + 1) n - 1) / U).  Both quotients by doubles (an integer division of 64 bits takes ten times as
+// long): their numerators are below 2^40 and exact, and half a unit added keeps the rounding of the quotient
+// (below 2^31 parts in 2^53) on the right side of every integer.
+__device__ __forceinline__ int first_unit(int units, int n, int i)
+{
+    return (int)(((double)units * i + 0.5) / n);
+}
+__device__ __forceinline__ int part_of(int units, int n, int u)
+{
+    return (int)(((double)(u + 1) * n - 0.5) / units);
+}
 // (a list is cut in no more parts than it has units, so that none is empty)
-__device__ __forceinline__ int parts_for(int nb, long long units) { return units < nb ? (int)units : nb; }
+__device__ __forceinline__ int parts_for(int nb, int units) { return units < nb ? units : nb; }
 
 // ---------------------------------------------------------------- pieces of a tile
 // 1 KB of global memory to LDS: lane l's 16 bytes go to lds + 16 l.  Written as assembly because the
@@ -166,11 +175,6 @@ __device__ __forceinline__ float lds_read4(uint32_t at)
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ long long uni64(long long v)
-{
-    return (long long)((unsigned long long)(unsigned)uni((int)(v >> 32)) << 32 | (unsigned)uni((int)v));
-}
-
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // two floats to bf16 (to nearest), packed
@@ -206,9 +210,7 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, i
 // LDS beside the tiles
 struct Small {
     int part[4];
-    long long lpart[4];
-    int found_b;
-    long long found_off;
+    int found_b, found_off;
     int bad_value;
     int tok[132];             // window tokens (b * K + t) of a shared row tile
     float2 ml[4][64];         // (m, l) of the waves' rows, to be joined
@@ -622,7 +624,7 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     }
 }
 
-// exclusive sums over the workgroup's threads (256), and the totals
+// exclusive sum over the workgroup's threads (256), and the total
 __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -644,27 +646,6 @@ __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
     return base + inc - v;
 }
 
-__device__ __forceinline__ long long scan_long(long long v, Small& s, long long& total)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    long long inc = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const long long u = __shfl_up(inc, d, 64);
-        if (lane >= d) inc += u;
-    }
-    __syncthreads();
-    if (lane == 63) s.lpart[w] = inc;
-    __syncthreads();
-    long long base = 0;
-    total = 0;
-    for (int i = 0; i < 4; ++i) {
-        base += i < w ? s.lpart[i] : 0;
-        total += s.lpart[i];
-    }
-    return base + inc - v;
-}
-
 // SH: the shared list's configuration, or void
 template <class OW, class SH>
 __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnArgs a, int nb)
@@ -682,39 +663,36 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
     // ---- the lists' lengths: thread i sums the sequences [b0, b1)
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
-    long long mine = 0;
-    int toks = 0;
+    int mine = 0, toks = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq q = seq_of(a, b, OW::N, OW::M);
         mine += q.units;
         if (q.part) toks += q.cnt;
     }
-    long long own;
-    const long long own_base = scan_long(mine, s, own);
-    own = uni64(own);
+    int own;
+    const int own_base = scan_int(mine, s, own);
+    own = uni(own);
     int tok_total = 0, tok_base = 0;
-    long long shared = 0;
-    int row_tiles = 0, key_tiles = 0;
+    int shared = 0, row_tiles = 0, key_tiles = 0;
     if constexpr (kShared) {
         tok_base = scan_int(toks, s, tok_total);
         tok_total = uni(tok_total);
-        row_tiles = (int)(((long long)tok_total * G + SH::M - 1) / SH::M);
+        row_tiles = (tok_total * G + SH::M - 1) / SH::M;
         key_tiles = (a.prefix + SH::N - 1) / SH::N;
-        shared = (long long)a.Hkv * row_tiles * key_tiles;
+        shared = a.Hkv * row_tiles * key_tiles;
     }
     const int shared_parts = parts_for(nb, shared), own_parts = parts_for(nb, own);
-    const int blocks = parts_for(nb, shared + own);
+    const int blocks = min(nb, shared_parts + own_parts);
     // consecutive workgroups of the lists on one XCD (workgroups are dealt to the 8 XCDs in turn)
     const int per_xcd = (blocks + 7) / 8;
     const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{shared, own, shared_parts, own_parts};
         PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + wk.plan);
-        long long base = own_base;
-        int tok = tok_base;
+        int base = own_base, tok = tok_base;
         for (int b = b0; b < b1; ++b) {
             const Seq q = seq_of(a, b, OW::N, OW::M);
-            plan[b] = PlanSeq{base, q.part ? tok : -1, 0};
+            plan[b] = PlanSeq{base, q.part ? tok : -1};
             base += q.units;
             tok += q.part ? q.cnt : 0;
         }
@@ -722,11 +700,11 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
     if ((int)(blockIdx.x >> 3) >= per_xcd || lb >= blocks) return;
 
     if constexpr (kShared) {
-        long long u = lb < shared_parts ? first_unit(shared, shared_parts, lb) : 0;
-        const long long u1 = lb < shared_parts ? first_unit(shared, shared_parts, lb + 1) : 0;
+        int u = lb < shared_parts ? first_unit(shared, shared_parts, lb) : 0;
+        const int u1 = lb < shared_parts ? first_unit(shared, shared_parts, lb + 1) : 0;
         while (u < u1) {
-            const int seg = (int)(u / key_tiles), k0 = (int)(u - (long long)seg * key_tiles);
-            const int nt = (int)min((long long)(key_tiles - k0), u1 - u);
+            const int seg = u / key_tiles, k0 = u - seg * key_tiles;
+            const int nt = min(key_tiles - k0, u1 - u);
             const int h = seg / row_tiles, rt = seg - h * row_tiles;
             // the tile's tokens
             const int r0 = rt * SH::M, t0 = r0 / G;
@@ -762,12 +740,12 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
 
     const int part = blocks - 1 - lb;
     if (part >= own_parts) return;
-    long long u = first_unit(own, own_parts, part);
-    const long long u1 = first_unit(own, own_parts, part + 1);
+    int u = first_unit(own, own_parts, part);
+    const int u1 = first_unit(own, own_parts, part + 1);
     // the sequence of the first unit
     __syncthreads();
     if (own_base <= u && u < own_base + mine) {
-        long long base = own_base;
+        int base = own_base;
         for (int b = b0; b < b1; ++b) {
             const Seq q = seq_of(a, b, OW::N, OW::M);
             if (u < base + q.units) {
@@ -779,18 +757,17 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
         }
     }
     __syncthreads();
-    int b = uni(s.found_b);
-    long long off = uni64(s.found_off);
+    int b = uni(s.found_b), off = uni(s.found_off);
     while (u < u1) {
         const Seq q = seq_of(a, b, OW::N, OW::M);
         const int tiles = uni(q.tiles), rts = uni(q.rts);
-        if (off >= (long long)a.Hkv * rts * tiles) {
+        if (off >= a.Hkv * rts * tiles) {
             off = 0;
             ++b;
             continue;
         }
-        const int seg = (int)(off / tiles), k0 = (int)(off - (long long)seg * tiles);
-        const int nt = (int)min((long long)(tiles - k0), u1 - u);
+        const int seg = off / tiles, k0 = off - seg * tiles;
+        const int nt = min(tiles - k0, u1 - u);
         const int h = seg / rts, rt = seg - h * rts;
         const int RT = (a.K * G + OW::M - 1) / OW::M;
         const size_t slot = (size_t)part + ((size_t)b * a.Hkv + h) * RT + rt;
@@ -816,82 +793,104 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
 }
 
 // ---------------------------------------------------------------- joining
-// A wave per row: lanes hold the pieces' (m, l) first, then the columns.
-template <bool BF16, int D>
+// A thread has 4 columns of a row; SPLIT threads share them, each taking every SPLIT-th piece (few rows have
+// many pieces, and then it is the chain of reads that costs), and are joined in LDS in a fixed order.
+template <bool BF16, int D, int SPLIT>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int nb, int MS, int MO, int N)
 {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63;
-    const long long row = (long long)blockIdx.x * 4 + uni(threadIdx.x >> 6);
-    if (row >= (long long)a.B * a.K * a.Hq) return;
-    const int G = a.Hq / a.Hkv;
-    const int tok = (int)(row / a.Hq), hq = (int)(row - (long long)tok * a.Hq);
-    const int b = tok / a.K, t = tok - b * a.K, h = hq / G, g = hq - h * G;
-    const Seq q = seq_of(a, b, N, MO);
-    if (t >= q.cnt) return;
+    constexpr int C4 = D / 4, PER = kThreads / SPLIT, AHEAD = 4;
+    __shared__ f32x4_t box[SPLIT > 1 ? kThreads : 1];
+    __shared__ float2 box_ml[SPLIT > 1 ? kThreads : 1];
+    const int sub = threadIdx.x / PER;
+    const long long unit = (long long)blockIdx.x * PER + threadIdx.x % PER;
+    const long long row = unit / C4;
+    const int c4 = (int)(unit % C4);
+    int n_s = 0, n_o = 0;
+    size_t at_s = 0, at_o = 0;   // first rows in the workspace
     const Layout wk = layout(a, nb, MS, MO);
     const char* work = static_cast<const char*>(a.work);
-    const Head head = *reinterpret_cast<const Head*>(work);
-    const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + wk.plan)[b];
-
-    int n_s = 0, n_o = 0;
-    size_t at_s = 0, at_o = 0, step_s = MS, step_o = MO;   // first row in the workspace, rows to the next piece
-    if (plan.tok_base >= 0 && head.shared_units > 0) {
-        const int r = (plan.tok_base + t) * G + g, rt = r / MS;
-        const int key_tiles = (a.prefix + N - 1) / N;
-        const int row_tiles = (int)(head.shared_units / ((long long)a.Hkv * key_tiles));
-        const long long seg = (long long)h * row_tiles + rt;
-        const int l0 = block_of(head.shared_units, head.shared_parts, seg * key_tiles);
-        const int l1 = block_of(head.shared_units, head.shared_parts, (seg + 1) * key_tiles - 1);
-        n_s = l1 - l0 + 1;
-        at_s = (size_t)(l0 + seg) * MS + (r - rt * MS);
-    }
-    if (q.tiles > 0) {
-        const int r = t * G + g, rt = r / MO, RT = (a.K * G + MO - 1) / MO;
-        const long long u = plan.own_base + ((long long)h * q.rts + rt) * q.tiles;
-        const int l0 = block_of(head.own_units, head.own_parts, u);
-        const int l1 = block_of(head.own_units, head.own_parts, u + q.tiles - 1);
-        n_o = l1 - l0 + 1;
-        at_o = ((size_t)l0 + ((size_t)b * a.Hkv + h) * RT + rt) * MO + (r - rt * MO);
-        if (n_o == 1 && !q.part) return;   // written by its one piece
-    }
-    const float2* ml_s = reinterpret_cast<const float2*>(work + wk.ml_s);
-    const float2* ml_o = reinterpret_cast<const float2*>(work + wk.ml_o);
-    const float* o_s = reinterpret_cast<const float*>(work + wk.o_s);
-    const float* o_o = reinterpret_cast<const float*>(work + wk.o_o);
-    const int n = n_s + n_o;
-    float M = kNoMax, L = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        const int i = i0 + lane;
-        float2 v = make_float2(kNoMax, 0.f);
-        if (i < n) v = i < n_s ? ml_s[at_s + i * step_s] : ml_o[at_o + (i - n_s) * step_o];
-        float mx = v.x;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
-        const float mn = fmaxf(M, mx), f = exp2_(M - mn), wgt = exp2_(v.x - mn);
-        float sum = v.y * wgt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-        M = mn;
-        L = L * f + sum;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= f;
-        const int last = min(64, n - i0);
-#pragma unroll 4
-        for (int k = 0; k < last; ++k) {
-            const int p = i0 + k;
-            const float* src = p < n_s ? o_s + (at_s + p * step_s) * D : o_o + (at_o + (p - n_s) * step_o) * D;
-            const float wk_ = __shfl(wgt, k, 64);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(src[lane * E + e], wk_, acc[e]);
+    bool mine = row < (long long)a.B * a.K * a.Hq;
+    if (mine) {
+        const int G = a.Hq / a.Hkv;
+        const int tok = (int)(row / a.Hq), hq = (int)(row - (long long)tok * a.Hq);
+        const int b = tok / a.K, t = tok - b * a.K, h = hq / G, g = hq - h * G;
+        const Head head = *reinterpret_cast<const Head*>(work);
+        const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + wk.plan)[b];
+        const Seq q = seq_of(a, b, N, MO);
+        mine = t < q.cnt;
+        if (mine && plan.tok_base >= 0 && head.shared_units > 0) {
+            const int r = (plan.tok_base + t) * G + g, rt = r / MS;
+            const int key_tiles = (a.prefix + N - 1) / N;
+            const int seg = head.shared_units / key_tiles / a.Hkv * h + rt;
+            const int p0 = part_of(head.shared_units, head.shared_parts, seg * key_tiles);
+            n_s = part_of(head.shared_units, head.shared_parts, (seg + 1) * key_tiles - 1) - p0 + 1;
+            at_s = (size_t)(p0 + seg) * MS + (r - rt * MS);
+        }
+        if (mine && q.tiles > 0) {
+            const int r = t * G + g, rt = r / MO, RT = (a.K * G + MO - 1) / MO;
+            const int u = plan.own_base + (h * q.rts + rt) * q.tiles;
+            const int p0 = part_of(head.own_units, head.own_parts, u);
+            n_o = part_of(head.own_units, head.own_parts, u + q.tiles - 1) - p0 + 1;
+            at_o = ((size_t)p0 + ((size_t)b * a.Hkv + h) * RT + rt) * MO + (r - rt * MO);
+            if (n_o == 1 && !q.part) mine = false;   // written by its one piece
         }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float2* ml_s = reinterpret_cast<const float2*>(work + wk.ml_s) + at_s;
+    const float2* ml_o = reinterpret_cast<const float2*>(work + wk.ml_o) + at_o;
+    const f32x4_t* o_s = reinterpret_cast<const f32x4_t*>(work + wk.o_s) + at_s * C4 + c4;
+    const f32x4_t* o_o = reinterpret_cast<const f32x4_t*>(work + wk.o_o) + at_o * C4 + c4;
+    const int n = mine ? n_s + n_o : 0;
+    float M = kNoMax, L = 0.f;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int i = sub; i < n; i += SPLIT * AHEAD) {
+        float2 v[AHEAD];
+        f32x4_t x[AHEAD];
 #pragma unroll
-    for (int e = 0; e < E; ++e) store1<BF16>(a.o, (size_t)row * D + lane * E + e, acc[e] * inv);
-    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+        for (int k = 0; k < AHEAD; ++k) {
+            const int p = i + k * SPLIT;
+            v[k] = make_float2(kNoMax, 0.f);
+            x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (p < n) {
+                const bool sh = p < n_s;
+                const size_t j = sh ? (size_t)p * MS : (size_t)(p - n_s) * MO;
+                v[k] = (sh ? ml_s : ml_o)[j];
+                x[k] = (sh ? o_s : o_o)[j * C4];
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) mn = fmaxf(mn, v[k].x);
+        const float f = exp2_(M - mn);
+        M = mn;
+        L *= f;
+        acc *= f;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const float w = exp2_(v[k].x - mn);
+            L = __builtin_fmaf(v[k].y, w, L);
+            acc += x[k] * w;
+        }
+    }
+    if constexpr (SPLIT > 1) {
+        box[threadIdx.x] = acc;
+        box_ml[threadIdx.x] = make_float2(M, L);
+        __syncthreads();
+        if (sub > 0) return;
+        for (int k = 1; k < SPLIT; ++k) {
+            const float2 v = box_ml[k * PER + threadIdx.x];
+            const float mn = fmaxf(M, v.x), f = exp2_(M - mn), w = exp2_(v.x - mn);
+            M = mn;
+            L = L * f + v.y * w;
+            acc = acc * f + box[k * PER + threadIdx.x] * w;
+        }
+    }
+    if (!mine) return;
+    const f32x4_t y = acc * (L == 0.f ? 0.f : 1.f / L);
+    if constexpr (BF16)
+        reinterpret_cast<uint2*>(a.o)[unit] = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+    else
+        reinterpret_cast<f32x4_t*>(a.o)[unit] = y;
+    if (a.lse && c4 == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
 }  // namespace attn

@@ -23,6 +23,16 @@ inline Pick pick(const AttnArgs& a, bool bf16)
     return p;
 }
 
+// units of the two lists at most: they are counted in 32 bits
+inline bool countable(const AttnArgs& a, const Pick& p, int N)
+{
+    const long long G = a.Hq / a.Hkv, most = (1ll << 31) - 1;
+    const long long own = (long long)a.B * a.Hkv * ((a.K * G + p.MO - 1) / p.MO);
+    const long long tiles = (((long long)a.P << a.page_log2) + N - 1) / N;
+    const long long shared = p.MS ? a.Hkv * ((a.B * a.K * G + p.MS - 1) / p.MS) : 0;
+    return own <= most / tiles && shared <= most / tiles;
+}
+
 hipError_t launch_bf16_64(const AttnArgs& a, hipStream_t s);
 hipError_t launch_bf16_128(const AttnArgs& a, hipStream_t s);
 hipError_t launch_bf16_256(const AttnArgs& a, hipStream_t s);
@@ -70,9 +80,13 @@ hipError_t launch_all(const AttnArgs& a, hipStream_t s)
             : p.MO == 32 ? launch_one<M32, M64>(a, p, s)
                          : launch_one<M64, M64>(a, p, s);
     if (e != hipSuccess) return e;
-    const long long rows = (long long)a.B * a.K * a.Hq;
-    attn_join_kernel<BF16, D><<<dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s>>>(a, p.blocks, p.MS, p.MO,
-                                                                                        M16::N);
+    // 4 columns a thread; where that fills less than half the chip or a sixteenth of it, 4 or 16 threads share them
+    const long long units = (long long)a.B * a.K * a.Hq * (D / 4);
+    const int split = units <= 16384 ? 16 : units <= 131072 ? 4 : 1;
+    const dim3 grid((unsigned)((units * split + kThreads - 1) / kThreads));
+    auto* join = split == 16 ? attn_join_kernel<BF16, D, 16> : split == 4 ? attn_join_kernel<BF16, D, 4>
+                                                                          : attn_join_kernel<BF16, D, 1>;
+    join<<<grid, dim3(kThreads), 0, s>>>(a, p.blocks, p.MS, p.MO, M16::N);
     return hipGetLastError();
 }
 
