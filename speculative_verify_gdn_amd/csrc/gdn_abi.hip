@@ -94,6 +94,8 @@ int check_kv(const char* fn, int planes, int n_pages, int Hkv, int page, int D, 
             "%s: page = %d is not a power of two in 16..1024", fn, page);
     REQUIRE(n_pages <= gdn::kKvPagesMax, GDN_EUNSUPPORTED, "%s: n_pages = %d > %d", fn, n_pages, gdn::kKvPagesMax);
     REQUIRE(Hkv <= 1024, GDN_EUNSUPPORTED, "%s: Hkv = %d > 1024", fn, Hkv);
+    REQUIRE((long long)Hkv * page * D <= (1 << 28), GDN_EUNSUPPORTED, "%s: a page of %d x %d x %d passes 2^28 elements",
+            fn, Hkv, page, D);
     REQUIRE(planes <= 65535, GDN_EUNSUPPORTED, "%s: planes = %d > 65535", fn, planes);
     g.planes = planes;
     g.n_pages = n_pages;

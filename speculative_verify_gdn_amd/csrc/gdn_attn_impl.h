@@ -139,16 +139,31 @@ __device__ __forceinline__ int part_of(int units, int n, int u)
 __device__ __forceinline__ int parts_for(int nb, int units) { return units < nb ? units : nb; }
 
 // ---------------------------------------------------------------- pieces of a tile
-// 1 KB of global memory to LDS: lane l's 16 bytes go to lds + 16 l.  Written as assembly because the
+// COUNT KB of global memory to LDS: in the i-th, lane l's 16 bytes at base + 1024 i + voff[i] go to
+// lds + 1024 i + 16 l (the instruction's offset counts on both sides).  Written as assembly because the
 // compiler would otherwise wait for the tile on its way before it reads the tile that is there; nothing
 // is returned in registers, and load_wait() below waits for all of them.  (m0 takes the LDS address; one
 // wait state between writing it and the load.)
-__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t voff, const char* base)
+template <int COUNT>
+__device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, const char* base)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(lds), "v"(voff), "s"(base)
-                 : "memory", "m0");
+    static_assert(COUNT == 2 || COUNT == 4, "2 or 4 KB");
+    if constexpr (COUNT == 2)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %1, %3\n\t"
+                     "global_load_lds_dwordx4 %2, %3 offset:1024"
+                     :
+                     : "s"(lds), "v"(voff[0]), "v"(voff[1]), "s"(base)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %1, %5\n\t"
+                     "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+                     "global_load_lds_dwordx4 %4, %5 offset:3072"
+                     :
+                     : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(base)
+                     : "memory", "m0");
 }
 
 __device__ __forceinline__ void load_wait()
@@ -259,11 +274,19 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     int ids = slot_id(first + lane, bad_lane), ids2 = slot_id(first + 64 + lane, bad_lane2);
     unsigned long long bad = __ballot(bad_lane), bad2 = __ballot(bad_lane2);
 
-    // ---- tile loads: wave w brings the keys w N/4 .. of K and V
-    constexpr int KPI = 1024 / C::ROW, NI = N / 4 / KPI;
-    const size_t page_bytes = ((size_t)a.Hkv << a.page_log2) * C::ROW;
-    const size_t head_off = ((size_t)in.h << a.page_log2) * C::ROW;
+    // ---- tile loads: wave w brings the keys w N/4 .. of K and V, in groups of up to 16 keys (of one page, as a
+    // page has 16 at least), a group in runs of CNT KB
+    constexpr int WK = N / 4, GK = WK < 16 ? WK : 16, KPI = 1024 / C::ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
+    const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_log2) * C::ROW;
+    const uint32_t head_off = ((uint32_t)in.h << a.page_log2) * C::ROW;
     const int lkey = lane / C::CH, lch = lane % C::CH;
+    uint32_t k_off[NI], v_off[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int key = (w * WK + i * KPI + lkey) & 15;   // (a group's further 16s do not change the swizzle)
+        k_off[i] = lkey * C::ROW + ((lch ^ k_swizzle<C>(key)) << 4);
+        v_off[i] = lkey * C::ROW + ((lch ^ v_swizzle<C>(key)) << 4);
+    }
     auto issue = [&](int j, int buf) {
         const int pt = in.p0 + j * N;
         int s0 = (pt >> a.page_log2) - first;
@@ -276,15 +299,17 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
             bad2 = __ballot(bad_lane2);
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int key = w * (N / 4) + i * KPI;
-            const int id = __builtin_amdgcn_readlane(ids, s0 + (key >> a.page_log2));
-            const size_t off = (size_t)id * page_bytes + head_off + (size_t)((pt + key) & page_mask) * C::ROW;
-            const uint32_t vk = lkey * C::ROW + ((lch ^ k_swizzle<C>(key + lkey)) << 4);
-            const uint32_t vv = lkey * C::ROW + ((lch ^ v_swizzle<C>(key + lkey)) << 4);
+        for (int g = 0; g < WK / GK; ++g) {
+            const int key = w * WK + g * GK;
+            const uint32_t id = __builtin_amdgcn_readlane(ids, s0 + (key >> a.page_log2));
+            const uint64_t off = (uint64_t)id * page_bytes + (head_off + ((pt + key) & page_mask) * C::ROW);
             const uint32_t to = lds0 + buf * C::STAGE + key * C::ROW;
-            load_lds(to, vk, static_cast<const char*>(a.k_pages) + off);
-            load_lds(to + C::MAT, vv, static_cast<const char*>(a.v_pages) + off);
+#pragma unroll
+            for (int i = 0; i < NI; i += CNT) {
+                load_lds<CNT>(to + i * 1024, k_off + i, static_cast<const char*>(a.k_pages) + off + i * 1024);
+                load_lds<CNT>(to + C::MAT + i * 1024, v_off + i,
+                              static_cast<const char*>(a.v_pages) + off + i * 1024);
+            }
         }
         const int slots = max(N >> a.page_log2, 1);
         return (unsigned)(bad >> s0) & ((1u << slots) - 1);   // missing pages of the tile
