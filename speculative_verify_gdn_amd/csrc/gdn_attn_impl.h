@@ -40,18 +40,18 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr float kNoMax = -1e37f;   // the reference of a row that has seen no key: finite, so differences are
 constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// M rows by N keys over the 4 waves: RW groups of rows x KW groups of keys x DW parts of the output's columns;
+// M rows by N keys over the 8 waves: RW groups of rows x KW groups of keys x DW parts of the output's columns;
 // a wave has MW times 16 rows
 template <bool BF16_, int D_, int RW_, int KW_, int DW_, int MW_>
 struct Cfg {
     static constexpr bool BF16 = BF16_;
     static constexpr int D = D_, RW = RW_, KW = KW_, DW = DW_, MW = MW_;
-    static_assert(RW * KW * DW == 4, "four waves");
+    static_assert(RW * KW * DW == kWaves, "every wave has a part");
     static constexpr int M = 16 * MW * RW;
     static constexpr int ES = BF16 ? 2 : 4, ROW = D * ES, CH = ROW / 16;
     static constexpr int N = 8192 / D;             // keys a tile: K and V are 32 KB in bf16, 64 KB in fp32
@@ -224,11 +224,11 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, i
 
 // LDS beside the tiles
 struct Small {
-    int part[4];
+    int part[kWaves];
     int found_b, found_off;
     int bad_value;
     int tok[132];             // window tokens (b * K + t) of a shared row tile
-    float2 ml[4][64];         // (m, l) of the waves' rows, to be joined
+    float2 ml[kWaves][32];    // (m, l) of the waves' rows, to be joined
 };
 
 struct PieceIn {
@@ -274,9 +274,9 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     int ids = slot_id(first + lane, bad_lane), ids2 = slot_id(first + 64 + lane, bad_lane2);
     unsigned long long bad = __ballot(bad_lane), bad2 = __ballot(bad_lane2);
 
-    // ---- tile loads: wave w brings the keys w N/4 .. of K and V, in groups of up to 16 keys (of one page, as a
+    // ---- tile loads: wave w brings the keys w N/8 .. of K and V, in groups of up to 16 keys (of one page, as a
     // page has 16 at least), a group in runs of CNT KB
-    constexpr int WK = N / 4, GK = WK < 16 ? WK : 16, KPI = 1024 / C::ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
+    constexpr int WK = N / kWaves, GK = WK < 16 ? WK : 16, KPI = 1024 / C::ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
     const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_log2) * C::ROW;
     const uint32_t head_off = ((uint32_t)in.h << a.page_log2) * C::ROW;
     const int lkey = lane / C::CH, lch = lane % C::CH;
@@ -314,6 +314,7 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
         const int slots = max(N >> a.page_log2, 1);
         return (unsigned)(bad >> s0) & ((1u << slots) - 1);   // missing pages of the tile
     };
+    if (threadIdx.x == 0) s.bad_value = 0;   // (before the first barrier of the loop)
     unsigned miss_next = issue(0, 0);
 
     // ---- the rows
@@ -339,6 +340,10 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
             q[r][e] = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
         }
     }
+    bool any = false;
+#pragma unroll
+    for (int r = 0; r < MW; ++r) any |= id[r].live;
+    const bool alive = __any(any);   // a wave without rows only loads
     f32x4_t o[DB][MW];
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -351,10 +356,10 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     const int vkey = C::BF16 ? 4 * grp + (n16 >> 2) : 4 * grp;   // (fp32 adds the register's index)
     const uint32_t k_lane = lds0 + (kbase + n16) * C::ROW + ((grp ^ k_swizzle<C>(n16)) << 4);
     const uint32_t v_lane =
-        lds0 + C::MAT + (kbase + vkey) * C::ROW + dw * (DB * 16 * C::ES) +
-        (C::BF16 ? ((((n16 >> 1) & 1) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 1) * 8
+        lds0 + C::MAT + (kbase + vkey) * C::ROW + (dw * DB * 16 * C::ES & ~255) +
+        (C::BF16 ? ((((n16 >> 1) & 1) ^ v_swizzle<C>(vkey) ^ (2 * dw * DB & 15)) << 4) + (n16 & 1) * 8
                  : (((n16 >> 2) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 3) * 4);
-    static_assert(C::DW == 1 || (DB * 16 * C::ES) % 256 == 0, "a part's columns start on whole swizzle groups");
+    static_assert(C::DW == 1 || DB * 16 * C::ES >= 128, "a part starts on a half or whole swizzle group");
 
     for (int j = 0; j < in.tiles; ++j) {
         const unsigned miss = miss_next;
@@ -366,31 +371,31 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
         const int pt = in.p0 + j * N;
         const bool masked = miss != 0 || (in.window && pt + N > in.len) || pt + N > in.end;
 
-        // Values nobody may see are cleared where they lie (0 times NaN is NaN), and a window value that some
-        // row sees but is not finite is noted: rows that do not see it must not meet it either.
-        bool poison = false;
+        // Values nobody may see are cleared where they lie (0 times NaN is NaN), and so are the window's that are
+        // not finite: only some rows see them, and get them at the end.
         if (masked) {
-            if (threadIdx.x == 0) s.bad_value = 0;
-            block_barrier();
             for (int e = threadIdx.x; e < N * C::CH; e += kThreads) {
                 const int key = e / C::CH, pos = pt + key;
-                uint4* v = reinterpret_cast<uint4*>(vt + e * 16);
-                if (pos >= in.end || (miss >> (key >> a.page_log2) & 1)) *v = make_uint4(0, 0, 0, 0);
-                else if (in.window && pos >= in.len) {
-                    const uint4 u = *v;
-                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                    bool odd = false;
+                uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
+                if (pos >= in.end || (miss >> (key >> a.page_log2) & 1)) {
+                    *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
+                } else if (in.window && pos >= in.len) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        odd |= (x[i] & 0x7f800000u) == 0x7f800000u;
-                        if (C::BF16) odd |= (x[i] & 0x7f80u) == 0x7f80u;
+                        const uint32_t u = v[i];
+                        uint32_t keep = u;
+                        if ((u & 0x7f800000u) == 0x7f800000u) keep &= C::BF16 ? 0xffffu : 0u;
+                        if (C::BF16 && (u & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                        if (keep != u) {
+                            v[i] = keep;
+                            s.bad_value = 1;
+                        }
                     }
-                    if (odd) s.bad_value = 1;
                 }
             }
             block_barrier();
-            poison = uni(s.bad_value) != 0;
         }
+        if (!alive) continue;
 
         // opaque, so that the addresses are formed from them in the loop and not kept in dozens of registers
         uint32_t k_at = k_lane + (j & 1) * C::STAGE, v_at = v_lane + (j & 1) * C::STAGE;
@@ -477,55 +482,6 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
             l[r] += sum;
         }
 
-        if (poison) {
-            // what is not finite reaches the rows that see it by itself, then leaves the tile
-#pragma unroll
-            for (int k = 0; k < KF; ++k)
-#pragma nounroll
-                for (int kk = 0; kk < 16; ++kk) {
-                    const int key = kbase + 16 * k + kk;
-                    if (pt + key < in.len || pt + key >= in.end) continue;
-                    const int from = (kk >> 2) * 16 + n16;
-                    float p[MW];
-                    bool v[MW];
-#pragma unroll
-                    for (int r = 0; r < MW; ++r) {
-                        const float p0 = __shfl(x[k][r][0], from, 64), p1 = __shfl(x[k][r][1], from, 64);
-                        const float p2 = __shfl(x[k][r][2], from, 64), p3 = __shfl(x[k][r][3], from, 64);
-                        p[r] = kk & 2 ? (kk & 1 ? p3 : p2) : (kk & 1 ? p1 : p0);
-                        v[r] = __shfl((int)seen[r], from, 64) >> (4 * k + (kk & 3)) & 1;
-                    }
-                    const char* vrow = vt + key * C::ROW;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const int col = (dw * DB + d) * 16 + 4 * grp;   // 4 columns of one chunk
-                        const int at = ((col * C::ES / 16) ^ v_swizzle<C>(key)) * 16 + col * C::ES % 16;
-                        const float4 y = load4<C::BF16>(vrow + at, 0);
-                        const float ya[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int r = 0; r < MW; ++r)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (v[r] && !(fabsf(ya[i]) < INFINITY)) o[d][r][i] += p[r] * ya[i];
-                        asm volatile("" ::: "memory");   // one group's loads at a time: this path is rare
-                    }
-                }
-            block_barrier();
-            for (int e = threadIdx.x; e < N * C::CH; e += kThreads) {
-                const int pos = pt + e / C::CH;
-                if (pos < in.len || pos >= in.end) continue;
-                uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t u = v[i];
-                    if ((u & 0x7f800000u) == 0x7f800000u) u &= C::BF16 ? 0xffffu : 0u;
-                    if (C::BF16 && (u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-                    v[i] = u;
-                }
-            }
-            block_barrier();
-        }
-
         // ---- O^T += V^T P^T
         if constexpr (C::BF16) {
             // the weights enter the product in bf16, as v is: half a step of 2^-8 each, unbiased
@@ -588,7 +544,28 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
         l[r] += __shfl_xor(l[r], 16, 64);
         l[r] += __shfl_xor(l[r], 32, 64);
     }
+    const bool bad_value = uni(s.bad_value) != 0;
     block_barrier();   // the tiles are done with
+    if (bad_value && alive) {
+        // a window value that is not finite makes what it makes of the rows that see it
+        for (int pos = max(in.p0, in.len); pos < min(in.end, in.p0 + in.tiles * N); ++pos) {
+            if (((pos - in.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
+            bool missing;
+            const int page = slot_id(pos >> a.page_log2, missing);
+            if (missing) continue;
+            const size_t at = ((((size_t)page * a.Hkv + in.h) << a.page_log2) + (pos & page_mask)) * C::D;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const float4 y = load4<C::BF16>(a.v_pages, at + (dw * DB + d) * 16 + 4 * grp);
+                const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int r = 0; r < MW; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((sees[r] >> (pos - in.len) & 1) && !(fabsf(ya[i]) < INFINITY)) o[d][r][i] += ya[i];
+            }
+        }
+    }
     if constexpr (C::KW > 1) {
         constexpr int F = DB * MW;
         float* box = reinterpret_cast<float*>(sm);
@@ -606,6 +583,7 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
         }
         block_barrier();
         if (kw == 0) {
+#pragma nounroll
             for (int k = 1; k < C::KW; ++k) {
 #pragma unroll
                 for (int r = 0; r < MW; ++r) {
@@ -649,7 +627,7 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     }
 }
 
-// exclusive sum over the workgroup's threads (256), and the total
+// exclusive sum over the workgroup's threads, and the total
 __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -664,7 +642,7 @@ __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
     __syncthreads();
     int base = 0;
     total = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWaves; ++i) {
         base += i < w ? s.part[i] : 0;
         total += s.part[i];
     }
@@ -673,7 +651,7 @@ __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
 
 // SH: the shared list's configuration, or void
 template <class OW, class SH>
-__global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnArgs a, int nb)
+__global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnArgs a, int nb)
 {
     // all of LDS is asked for at the launch and starts at 0: the swizzled addresses flip bits below 256
     extern __shared__ __attribute__((aligned(1024))) char sm[];
@@ -820,12 +798,14 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 2 : 1) void attn_kernel(AttnAr
 // ---------------------------------------------------------------- joining
 // A thread has 4 columns of a row; SPLIT threads share them, each taking every SPLIT-th piece (few rows have
 // many pieces, and then it is the chain of reads that costs), and are joined in LDS in a fixed order.
+constexpr int kJoin = 256;
+
 template <bool BF16, int D, int SPLIT>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int nb, int MS, int MO, int N)
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, int MS, int MO, int N)
 {
-    constexpr int C4 = D / 4, PER = kThreads / SPLIT, AHEAD = 4;
-    __shared__ f32x4_t box[SPLIT > 1 ? kThreads : 1];
-    __shared__ float2 box_ml[SPLIT > 1 ? kThreads : 1];
+    constexpr int C4 = D / 4, PER = kJoin / SPLIT, AHEAD = 4;
+    __shared__ f32x4_t box[SPLIT > 1 ? kJoin : 1];
+    __shared__ float2 box_ml[SPLIT > 1 ? kJoin : 1];
     const int sub = threadIdx.x / PER;
     const long long unit = (long long)blockIdx.x * PER + threadIdx.x % PER;
     const long long row = unit / C4;

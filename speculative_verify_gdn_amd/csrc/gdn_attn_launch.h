@@ -18,8 +18,9 @@ inline Pick pick(const AttnArgs& a, bool bf16)
     Pick p;
     const int G = a.Hq / a.Hkv, R = a.K * G;
     p.blocks = bf16 ? 512 : 256;   // two workgroups fit a CU (64 KB of tiles each), one in fp32
-    p.MO = R <= 16 ? 16 : R <= 32 ? 32 : 64;
-    p.MS = a.prefix == 0 ? 0 : 64;
+    const int most = bf16 && a.D == 256 ? 64 : 128;   // 128 rows of 256 columns do not fit the registers of 4 waves a SIMD
+    p.MO = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : most;
+    p.MS = a.prefix == 0 ? 0 : a.B * R <= 64 ? 64 : most;
     return p;
 }
 
@@ -66,27 +67,38 @@ hipError_t launch_one(const AttnArgs& a, const Pick& p, hipStream_t s)
     return hipGetLastError();
 }
 
-template <bool BF16, int D, class M16, class M32, class M64>
+template <class SH, class M16, class M32, class M64, class M128>
+hipError_t launch_with(const AttnArgs& a, const Pick& p, hipStream_t s)
+{
+    if (p.MO == 16) return launch_one<M16, SH>(a, p, s);
+    if (p.MO == 32) return launch_one<M32, SH>(a, p, s);
+    if constexpr (!__is_same(M128, void))
+        if (p.MO == 128) return launch_one<M128, SH>(a, p, s);
+    return launch_one<M64, SH>(a, p, s);
+}
+
+template <bool BF16, int D, class M16, class M32, class M64, class M128>
 hipError_t launch_all(const AttnArgs& a, hipStream_t s)
 {
     const Pick p = pick(a, BF16);
     hipError_t e;
-    if (p.MS == 0)
-        e = p.MO == 16   ? launch_one<M16, void>(a, p, s)
-            : p.MO == 32 ? launch_one<M32, void>(a, p, s)
-                         : launch_one<M64, void>(a, p, s);
-    else
-        e = p.MO == 16   ? launch_one<M16, M64>(a, p, s)
-            : p.MO == 32 ? launch_one<M32, M64>(a, p, s)
-                         : launch_one<M64, M64>(a, p, s);
+    if (p.MS == 0) {
+        e = launch_with<void, M16, M32, M64, M128>(a, p, s);
+    } else {
+        if constexpr (!__is_same(M128, void))
+            e = p.MS == 128 ? launch_with<M128, M16, M32, M64, M128>(a, p, s)
+                            : launch_with<M64, M16, M32, M64, M128>(a, p, s);
+        else
+            e = launch_with<M64, M16, M32, M64, M128>(a, p, s);
+    }
     if (e != hipSuccess) return e;
     // 4 columns a thread; where that fills less than half the chip or a sixteenth of it, 4 or 16 threads share them
     const long long units = (long long)a.B * a.K * a.Hq * (D / 4);
     const int split = units <= 16384 ? 16 : units <= 131072 ? 4 : 1;
-    const dim3 grid((unsigned)((units * split + kThreads - 1) / kThreads));
+    const dim3 grid((unsigned)((units * split + kJoin - 1) / kJoin));
     auto* join = split == 16 ? attn_join_kernel<BF16, D, 16> : split == 4 ? attn_join_kernel<BF16, D, 4>
                                                                           : attn_join_kernel<BF16, D, 1>;
-    join<<<grid, dim3(kThreads), 0, s>>>(a, p.blocks, p.MS, p.MO, M16::N);
+    join<<<grid, dim3(kJoin), 0, s>>>(a, p.blocks, p.MS, p.MO, M16::N);
     return hipGetLastError();
 }
 
