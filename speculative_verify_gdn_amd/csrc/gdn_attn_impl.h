@@ -7,19 +7,22 @@
 // pages that all sequences share are read once for the rows of all of them, and
 // what is left is cut evenly over the chip.
 //
-// Work list.  A unit is one tile of N keys against the M rows of one
-// key/value head.  Two lists: the shared units (head, row tile, key tile), whose
-// row tiles run through the window tokens of every sequence that holds the
-// prefix, and the sequences' own units (sequence, head, row tile, key tile).
-// Part i of n has the units [i U / n, (i+1) U / n); the workgroups take a part of each
-// list, the shared ones in their order and the own ones from the last workgroup
-// down, so that lists that are shorter than the grid meet as little as may be.  The load is
-// even whatever the lengths are, and no host knowledge of them is needed: each
-// workgroup sums the lists' lengths over the sequences by itself.  A run of
-// consecutive units of one row tile is a piece; a piece leaves (m, l, a) in the
-// workspace and a second kernel joins the pieces of each row, except where one
-// piece is all there is.  Consecutive workgroups sit on one XCD, so row tiles
-// that read the same keys at the same time share its L2.
+// Work lists.  A unit is one tile of N keys against the M rows of one
+// key/value head.  The shared list has an item for each (head, split of the prefix,
+// row tile), whose row tiles run through the window tokens of every sequence that
+// holds the prefix; the splits are as many as make the items fill the grid best.
+// The own list has the units (sequence, head, key tile) in this order, and part i of
+// n has the units [i U / n, (i+1) U / n), so the load is even whatever the lengths are;
+// a part's row tiles go to neighbouring workgroups (with windows of unequal length
+// the row tiles are units of the list instead).  No host knowledge of lengths is
+// needed: each workgroup sums them over the sequences by itself.  The workgroups
+// take the shared items in their order and the own parts from the last workgroup
+// down, so that short lists meet as little as may be.  A run of units of
+// one row tile is a piece; a piece leaves (m, l, a) in the workspace and a second
+// kernel joins the pieces of each row, except where one piece is all there is.
+// Consecutive workgroups sit on one XCD, so that row tiles that read the same keys
+// at the same time share its L2: before the row tiles of a key range were
+// neighbours, four of five reads of a shared prefix missed it.
 //
 // A tile.  K and V rows go from memory straight into LDS (16 bytes a lane), one
 // tile ahead of the one being worked on.  S^T = K Q^T leaves a query row in the
@@ -89,14 +92,14 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
     s.start = s.part ? a.prefix : 0;
     s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) / N : 0;
     s.rts = (s.cnt * (a.Hq / a.Hkv) + M - 1) / M;
-    s.units = a.Hkv * s.rts * s.tiles;
+    s.units = a.Hkv * s.tiles * (a.count ? s.rts : 1);
     return s;
 }
 
 // the lists' lengths and cuts, for the joining kernel
 struct Head {
-    int shared_units, own_units;
-    int shared_parts, own_parts;
+    int row_tiles, splits;       // of the shared list
+    int own_units, own_parts;
 };
 struct PlanSeq {
     int own_base;   // own units of the sequences before
@@ -111,7 +114,8 @@ __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)
 __host__ __device__ inline Layout layout(const AttnArgs& a, int nb, int MS, int MO)
 {
     const size_t G = a.Hq / a.Hkv;
-    const size_t slots_s = MS ? nb + a.Hkv * (((size_t)a.B * a.K * G + MS - 1) / MS) : 0;
+    const size_t segs = MS ? a.Hkv * (((size_t)a.B * a.K * G + MS - 1) / MS) : 0;
+    const size_t slots_s = MS ? (segs > 2 * (size_t)nb ? segs : 2 * (size_t)nb) : 0;
     const size_t slots_o = nb + (size_t)a.B * a.Hkv * ((a.K * G + MO - 1) / MO);
     Layout w;
     w.plan = up256(sizeof(Head));
@@ -135,8 +139,38 @@ __device__ __forceinline__ int part_of(int units, int n, int u)
 {
     return (int)(((double)(u + 1) * n - 0.5) / units);
 }
+// Into how many splits the prefix goes: for s of them, `segs` heads and row tiles take ceil(segs s / nb) rounds of
+// ceil(tiles / s) tiles and about kStartup tiles' time for a piece's first reads and its end.  A lane tries each s;
+// there are at most max(segs, 2 nb) items.
+constexpr int kStartup = 6;
+__device__ __forceinline__ int splits_for(int segs, int tiles, int nb)
+{
+    const int n = (threadIdx.x & 63) + 1;
+    int cost = (segs * n + nb - 1) / nb * ((tiles + n - 1) / n + kStartup);
+    if (n > 1 && (n > tiles || segs * n > 2 * nb)) cost = 0x7fffffff;
+    int best = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int c = __shfl_xor(cost, d, 64), m = __shfl_xor(best, d, 64);
+        const bool less = c < cost || (c == cost && m < best);
+        cost = less ? c : cost;
+        best = less ? m : best;
+    }
+    return __builtin_amdgcn_readfirstlane(best);
+}
+
+// how the own list counts row tiles: with equal windows a unit stands for all RT of them, taken by RT
+// neighbouring workgroups; otherwise each is a unit of its own
+struct RowTiles {
+    int in_list, grouped;
+};
+__host__ __device__ inline RowTiles row_tiles_of(const AttnArgs& a, int M)
+{
+    const int rt = (a.K * (a.Hq / a.Hkv) + M - 1) / M;
+    return a.count ? RowTiles{rt, 1} : RowTiles{1, rt};
+}
 // (a list is cut in no more parts than it has units, so that none is empty)
-__device__ __forceinline__ int parts_for(int nb, int units) { return units < nb ? units : nb; }
+__device__ __forceinline__ int parts_for(int nb, int grouped, int units) { return min(max(nb / grouped, 1), units); }
 
 // ---------------------------------------------------------------- pieces of a tile
 // COUNT KB of global memory to LDS: in the i-th, lane l's 16 bytes at base + 1024 i + voff[i] go to
@@ -676,21 +710,23 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     const int own_base = scan_int(mine, s, own);
     own = uni(own);
     int tok_total = 0, tok_base = 0;
-    int shared = 0, row_tiles = 0, key_tiles = 0;
+    int items = 0, row_tiles = 0, key_tiles = 0, splits = 0;
     if constexpr (kShared) {
         tok_base = scan_int(toks, s, tok_total);
         tok_total = uni(tok_total);
         row_tiles = (tok_total * G + SH::M - 1) / SH::M;
         key_tiles = (a.prefix + SH::N - 1) / SH::N;
-        shared = a.Hkv * row_tiles * key_tiles;
+        splits = splits_for(a.Hkv * row_tiles, key_tiles, nb);
+        items = a.Hkv * row_tiles * splits;
     }
-    const int shared_parts = parts_for(nb, shared), own_parts = parts_for(nb, own);
-    const int blocks = min(nb, shared_parts + own_parts);
+    const RowTiles rts_of = row_tiles_of(a, OW::M);
+    const int own_parts = parts_for(nb, rts_of.grouped, own);
+    const int blocks = min(nb, items + own_parts * rts_of.grouped);
     // consecutive workgroups of the lists on one XCD (workgroups are dealt to the 8 XCDs in turn)
     const int per_xcd = (blocks + 7) / 8;
     const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{shared, own, shared_parts, own_parts};
+        if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{row_tiles, splits, own, own_parts};
         PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + wk.plan);
         int base = own_base, tok = tok_base;
         for (int b = b0; b < b1; ++b) {
@@ -703,12 +739,9 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     if ((int)(blockIdx.x >> 3) >= per_xcd || lb >= blocks) return;
 
     if constexpr (kShared) {
-        int u = lb < shared_parts ? first_unit(shared, shared_parts, lb) : 0;
-        const int u1 = lb < shared_parts ? first_unit(shared, shared_parts, lb + 1) : 0;
-        while (u < u1) {
-            const int seg = u / key_tiles, k0 = u - seg * key_tiles;
-            const int nt = min(key_tiles - k0, u1 - u);
-            const int h = seg / row_tiles, rt = seg - h * row_tiles;
+        for (int it = lb; it < items; it += blocks) {
+            const int hs = it / row_tiles, rt = it - hs * row_tiles, h = hs / splits, sp = hs - h * splits;
+            const int k0 = (int)((unsigned)key_tiles * sp / splits), k1 = (int)((unsigned)key_tiles * (sp + 1) / splits);
             // the tile's tokens
             const int r0 = rt * SH::M, t0 = r0 / G;
             const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
@@ -722,8 +755,8 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             }
             __syncthreads();
             const int lead = uni(s.tok[0] / a.K);
-            PieceIn in{a.table + (size_t)lead * a.P, nullptr, h, k0 * SH::N, nt, a.prefix, a.prefix, false};
-            const size_t slot = (size_t)lb + seg;
+            PieceIn in{a.table + (size_t)lead * a.P, nullptr, h, k0 * SH::N, k1 - k0, a.prefix, a.prefix, false};
+            const size_t slot = it;
             PieceOut out{false, reinterpret_cast<float*>(work + wk.o_s) + slot * SH::M * SH::D,
                          reinterpret_cast<float2*>(work + wk.ml_s) + slot * SH::M};
             run_piece<SH>(a, sm, s, in, out, [&](int r) {
@@ -737,12 +770,12 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
                 }
                 return id;
             });
-            u += nt;
         }
     }
 
-    const int part = blocks - 1 - lb;
-    if (part >= own_parts) return;
+    const int own_block = blocks - 1 - lb;
+    if (own_block >= own_parts * rts_of.grouped) return;
+    const int part = own_block / rts_of.grouped, rt_block = own_block - part * rts_of.grouped;
     int u = first_unit(own, own_parts, part);
     const int u1 = first_unit(own, own_parts, part + 1);
     // the sequence of the first unit
@@ -763,7 +796,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     int b = uni(s.found_b), off = uni(s.found_off);
     while (u < u1) {
         const Seq q = seq_of(a, b, OW::N, OW::M);
-        const int tiles = uni(q.tiles), rts = uni(q.rts);
+        const int tiles = uni(q.tiles), rts = a.count ? uni(q.rts) : 1;
         if (off >= a.Hkv * rts * tiles) {
             off = 0;
             ++b;
@@ -771,9 +804,8 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
         }
         const int seg = off / tiles, k0 = off - seg * tiles;
         const int nt = min(tiles - k0, u1 - u);
-        const int h = seg / rts, rt = seg - h * rts;
-        const int RT = (a.K * G + OW::M - 1) / OW::M;
-        const size_t slot = (size_t)part + ((size_t)b * a.Hkv + h) * RT + rt;
+        const int h = seg / rts, rt_list = seg - h * rts, rt = rt_list + rt_block;
+        const size_t slot = ((size_t)part + ((size_t)b * a.Hkv + h) * rts_of.in_list + rt_list) * rts_of.grouped + rt_block;
         PieceIn in{a.table + (size_t)b * a.P, a.parent ? a.parent + (size_t)b * a.K : nullptr, h,
                    uni(q.start) + k0 * OW::N, nt, uni(q.len), uni(q.end), true};
         PieceOut out{uni(q.part) == 0 && nt == tiles, reinterpret_cast<float*>(work + wk.o_o) + slot * OW::M * OW::D,
@@ -811,7 +843,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
     const long long row = unit / C4;
     const int c4 = (int)(unit % C4);
     int n_s = 0, n_o = 0;
-    size_t at_s = 0, at_o = 0;   // first rows in the workspace
+    size_t at_s = 0, at_o = 0, step_s = 0, step_o = 0;   // first rows in the workspace, rows to the next piece
     const Layout wk = layout(a, nb, MS, MO);
     const char* work = static_cast<const char*>(a.work);
     bool mine = row < (long long)a.B * a.K * a.Hq;
@@ -823,20 +855,23 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
         const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + wk.plan)[b];
         const Seq q = seq_of(a, b, N, MO);
         mine = t < q.cnt;
-        if (mine && plan.tok_base >= 0 && head.shared_units > 0) {
+        if (mine && plan.tok_base >= 0) {
             const int r = (plan.tok_base + t) * G + g, rt = r / MS;
-            const int key_tiles = (a.prefix + N - 1) / N;
-            const int seg = head.shared_units / key_tiles / a.Hkv * h + rt;
-            const int p0 = part_of(head.shared_units, head.shared_parts, seg * key_tiles);
-            n_s = part_of(head.shared_units, head.shared_parts, (seg + 1) * key_tiles - 1) - p0 + 1;
-            at_s = (size_t)(p0 + seg) * MS + (r - rt * MS);
+            n_s = head.splits;
+            at_s = ((size_t)h * head.splits * head.row_tiles + rt) * MS + (r - rt * MS);
+            step_s = (size_t)head.row_tiles * MS;
         }
         if (mine && q.tiles > 0) {
-            const int r = t * G + g, rt = r / MO, RT = (a.K * G + MO - 1) / MO;
-            const int u = plan.own_base + (h * q.rts + rt) * q.tiles;
+            const RowTiles rts_of = row_tiles_of(a, MO);
+            const int r = t * G + g, rt = r / MO;
+            const int rt_list = a.count ? rt : 0, rt_block = a.count ? 0 : rt;
+            const int u = plan.own_base + (h * (a.count ? q.rts : 1) + rt_list) * q.tiles;
             const int p0 = part_of(head.own_units, head.own_parts, u);
             n_o = part_of(head.own_units, head.own_parts, u + q.tiles - 1) - p0 + 1;
-            at_o = ((size_t)p0 + ((size_t)b * a.Hkv + h) * RT + rt) * MO + (r - rt * MO);
+            const size_t slot =
+                ((size_t)p0 + ((size_t)b * a.Hkv + h) * rts_of.in_list + rt_list) * rts_of.grouped + rt_block;
+            at_o = slot * MO + (r - rt * MO);
+            step_o = (size_t)rts_of.grouped * MO;
             if (n_o == 1 && !q.part) mine = false;   // written by its one piece
         }
     }
@@ -857,7 +892,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
             x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             if (p < n) {
                 const bool sh = p < n_s;
-                const size_t j = sh ? (size_t)p * MS : (size_t)(p - n_s) * MO;
+                const size_t j = sh ? p * step_s : (p - n_s) * step_o;
                 v[k] = (sh ? ml_s : ml_o)[j];
                 x[k] = (sh ? o_s : o_o)[j * C4];
             }
