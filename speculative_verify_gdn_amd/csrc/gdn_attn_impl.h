@@ -260,7 +260,9 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, i
 struct Small {
     int part[kWaves];
     int found_b, found_off;
+    int tok_base[kThreads];   // window tokens of the prefix-holding sequences before a thread's own
     int bad_value;
+    unsigned long long path[64];
     int tok[132];             // window tokens (b * K + t) of a shared row tile
     float2 ml[kWaves][32];    // (m, l) of the waves' rows, to be joined
 };
@@ -314,13 +316,10 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_log2) * C::ROW;
     const uint32_t head_off = ((uint32_t)in.h << a.page_log2) * C::ROW;
     const int lkey = lane / C::CH, lch = lane % C::CH;
-    uint32_t k_off[NI], v_off[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int key = (w * WK + i * KPI + lkey) & 15;   // (a group's further 16s do not change the swizzle)
-        k_off[i] = lkey * C::ROW + ((lch ^ k_swizzle<C>(key)) << 4);
-        v_off[i] = lkey * C::ROW + ((lch ^ v_swizzle<C>(key)) << 4);
-    }
+    // (the i-th KB of a group is i KPI keys on: bits of the key that no other part of it has, so they flip in)
+    const int key0 = w * WK + lkey;
+    const uint32_t k_off = lkey * C::ROW + ((lch ^ k_swizzle<C>(key0 & 15)) << 4);
+    const uint32_t v_off = lkey * C::ROW + ((lch ^ v_swizzle<C>(key0 & 15)) << 4);
     auto issue = [&](int j, int buf) {
         const int pt = in.p0 + j * N;
         int s0 = (pt >> a.page_log2) - first;
@@ -340,9 +339,14 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
             const uint32_t to = lds0 + buf * C::STAGE + key * C::ROW;
 #pragma unroll
             for (int i = 0; i < NI; i += CNT) {
-                load_lds<CNT>(to + i * 1024, k_off + i, static_cast<const char*>(a.k_pages) + off + i * 1024);
-                load_lds<CNT>(to + C::MAT + i * 1024, v_off + i,
-                              static_cast<const char*>(a.v_pages) + off + i * 1024);
+                uint32_t ko[CNT], vo[CNT];
+#pragma unroll
+                for (int e = 0; e < CNT; ++e) {
+                    ko[e] = k_off ^ (k_swizzle<C>((i + e) * KPI) << 4);
+                    vo[e] = v_off ^ (v_swizzle<C>((i + e) * KPI) << 4);
+                }
+                load_lds<CNT>(to + i * 1024, ko, static_cast<const char*>(a.k_pages) + off + i * 1024);
+                load_lds<CNT>(to + C::MAT + i * 1024, vo, static_cast<const char*>(a.v_pages) + off + i * 1024);
             }
         }
         const int slots = max(N >> a.page_log2, 1);
@@ -352,31 +356,36 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     unsigned miss_next = issue(0, 0);
 
     // ---- the rows
+    // Row r of this lane, formed anew wherever it is asked for: kept, it would take registers through the loop.
+    auto row_id = [&](int r) {
+        int row = (rw * MW + r) * 16 + (threadIdx.x & 15);
+        asm volatile("" : "+v"(row));
+        return row_of(row);
+    };
+    // the window's nodes on the path to each node, for the tiles that need them
+    if (in.window && w == 0) s.path[lane] = ancestors(in.parent, a.K);
     float m[MW], l[MW];
-    unsigned long long sees[MW];
-    RowId id[MW];
     uint4 q[MW][QC];
     const float c = fabsf(a.scale) * kLog2e;
-    const uint32_t flip = a.scale < 0.f ? (C::BF16 ? 0x80008000u : 0x80000000u) : 0u;  // the sign goes into q
-    const unsigned long long path = in.window ? ancestors(in.parent, a.K) : 0;
+    bool any = false;
+    {
+        const uint32_t flip = a.scale < 0.f ? (C::BF16 ? 0x80008000u : 0x80000000u) : 0u;  // the sign goes into q
 #pragma unroll
-    for (int r = 0; r < MW; ++r) {
-        id[r] = row_of((rw * MW + r) * 16 + n16);
-        m[r] = kNoMax;
-        l[r] = 0.f;
-        sees[r] = __shfl(path, id[r].t & 63, 64);
-        const char* qp = static_cast<const char*>(a.q) +
-                         ((size_t)id[r].tok * a.q_stride + (size_t)(in.h * G + id[r].g) * C::D) * C::ES + grp * 16;
+        for (int r = 0; r < MW; ++r) {
+            const RowId id = row_id(r);
+            any |= id.live;
+            m[r] = kNoMax;
+            l[r] = 0.f;
+            const char* qp = static_cast<const char*>(a.q) +
+                             ((size_t)id.tok * a.q_stride + (size_t)(in.h * G + id.g) * C::D) * C::ES + grp * 16;
 #pragma unroll
-        for (int e = 0; e < QC; ++e) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (id[r].live) u = *reinterpret_cast<const uint4*>(qp + e * 64);
-            q[r][e] = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+            for (int e = 0; e < QC; ++e) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (id.live) u = *reinterpret_cast<const uint4*>(qp + e * 64);
+                q[r][e] = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
+            }
         }
     }
-    bool any = false;
-#pragma unroll
-    for (int r = 0; r < MW; ++r) any |= id[r].live;
     const bool alive = __any(any);   // a wave without rows only loads
     f32x4_t o[DB][MW];
 #pragma unroll
@@ -470,13 +479,14 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
 #pragma unroll
             for (int r = 0; r < MW; ++r) {
                 seen[r] = 0;
+                const unsigned long long sees = in.window ? s.path[row_id(r).t & 63] : 0;
 #pragma unroll
                 for (int k = 0; k < KF; ++k) {
                     const int key = kbase + 16 * k + 4 * grp;
                     // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
                     // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
                     const int rel = pt + key - in.len, left = in.end - (pt + key);
-                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees[r] >> (max(rel, 0) & 63));
+                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees >> (max(rel, 0) & 63));
                     const int old = min(max(-rel, 0), 4);
                     unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
                     bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
@@ -579,8 +589,10 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
         l[r] += __shfl_xor(l[r], 32, 64);
     }
     const bool bad_value = uni(s.bad_value) != 0;
-    block_barrier();   // the tiles are done with
     if (bad_value && alive) {
+        unsigned long long sees[MW];
+#pragma unroll
+        for (int r = 0; r < MW; ++r) sees[r] = s.path[row_id(r).t & 63];
         // a window value that is not finite makes what it makes of the rows that see it
         for (int pos = max(in.p0, in.len); pos < min(in.end, in.p0 + in.tiles * N); ++pos) {
             if (((pos - in.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
@@ -600,6 +612,7 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
             }
         }
     }
+    block_barrier();   // the tiles, and what this piece kept beside them, are done with
     if constexpr (C::KW > 1) {
         constexpr int F = DB * MW;
         float* box = reinterpret_cast<float*>(sm);
@@ -635,10 +648,11 @@ __device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s,
     }
 #pragma unroll
     for (int r = 0; r < MW; ++r) {
-        if (!id[r].live) continue;
+        const RowId id = row_id(r);
+        if (!id.live) continue;
         const int row = (rw * MW + r) * 16 + n16;
         if (out.direct) {
-            const size_t at = (size_t)id[r].tok * a.Hq + in.h * G + id[r].g;
+            const size_t at = (size_t)id.tok * a.Hq + in.h * G + id.g;
             const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
@@ -713,6 +727,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     int items = 0, row_tiles = 0, key_tiles = 0, splits = 0;
     if constexpr (kShared) {
         tok_base = scan_int(toks, s, tok_total);
+        s.tok_base[threadIdx.x] = tok_base;
         tok_total = uni(tok_total);
         row_tiles = (tok_total * G + SH::M - 1) / SH::M;
         key_tiles = (a.prefix + SH::N - 1) / SH::N;
@@ -738,6 +753,27 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     }
     if ((int)(blockIdx.x >> 3) >= per_xcd || lb >= blocks) return;
 
+    // the own part: its units [own_u, own_u1), the first in sequence own_b, own_off units into it
+    const int own_block = blocks - 1 - lb;
+    const bool has_own = own_block < own_parts * rts_of.grouped;
+    const int part = own_block / rts_of.grouped, rt_block = own_block - part * rts_of.grouped;
+    const int own_u = has_own ? first_unit(own, own_parts, part) : 0;
+    const int own_u1 = has_own ? first_unit(own, own_parts, part + 1) : 0;
+    if (own_base <= own_u && own_u < own_base + mine) {
+        int base = own_base;
+        for (int b = b0; b < b1; ++b) {
+            const Seq q = seq_of(a, b, OW::N, OW::M);
+            if (own_u < base + q.units) {
+                s.found_b = b;
+                s.found_off = own_u - base;
+                break;
+            }
+            base += q.units;
+        }
+    }
+    __syncthreads();
+    const int own_b = uni(s.found_b), own_off = uni(s.found_off);
+
     if constexpr (kShared) {
         for (int it = lb; it < items; it += blocks) {
             const int hs = it / row_tiles, rt = it - hs * row_tiles, h = hs / splits, sp = hs - h * splits;
@@ -746,8 +782,9 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             const int r0 = rt * SH::M, t0 = r0 / G;
             const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
             __syncthreads();
-            int tok = tok_base;
-            for (int b = b0; b < b1 && tok < t1; ++b) {
+            int tok = s.tok_base[threadIdx.x];
+            const int f0 = min((int)threadIdx.x * per, a.B), f1 = min(f0 + per, a.B);
+            for (int b = f0; b < f1 && tok < t1; ++b) {
                 const Seq q = seq_of(a, b, OW::N, OW::M);
                 if (!q.part) continue;
                 for (int t = max(0, t0 - tok); t < q.cnt && tok + t < t1; ++t) s.tok[tok + t - t0] = b * a.K + t;
@@ -773,28 +810,8 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
         }
     }
 
-    const int own_block = blocks - 1 - lb;
-    if (own_block >= own_parts * rts_of.grouped) return;
-    const int part = own_block / rts_of.grouped, rt_block = own_block - part * rts_of.grouped;
-    int u = first_unit(own, own_parts, part);
-    const int u1 = first_unit(own, own_parts, part + 1);
-    // the sequence of the first unit
-    __syncthreads();
-    if (own_base <= u && u < own_base + mine) {
-        int base = own_base;
-        for (int b = b0; b < b1; ++b) {
-            const Seq q = seq_of(a, b, OW::N, OW::M);
-            if (u < base + q.units) {
-                s.found_b = b;
-                s.found_off = u - base;
-                break;
-            }
-            base += q.units;
-        }
-    }
-    __syncthreads();
-    int b = uni(s.found_b), off = uni(s.found_off);
-    while (u < u1) {
+    int b = own_b, off = own_off, u = own_u;
+    while (u < own_u1) {
         const Seq q = seq_of(a, b, OW::N, OW::M);
         const int tiles = uni(q.tiles), rts = a.count ? uni(q.rts) : 1;
         if (off >= a.Hkv * rts * tiles) {
@@ -803,7 +820,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             continue;
         }
         const int seg = off / tiles, k0 = off - seg * tiles;
-        const int nt = min(tiles - k0, u1 - u);
+        const int nt = min(tiles - k0, own_u1 - u);
         const int h = seg / rts, rt_list = seg - h * rts, rt = rt_list + rt_block;
         const size_t slot = ((size_t)part + ((size_t)b * a.Hkv + h) * rts_of.in_list + rt_list) * rts_of.grouped + rt_block;
         PieceIn in{a.table + (size_t)b * a.P, a.parent ? a.parent + (size_t)b * a.K : nullptr, h,
