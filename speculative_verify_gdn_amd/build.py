@@ -11,7 +11,8 @@ same library with the count of clamped accept lengths of csrc/gdn_debug.h,
 read by gdn_debug_clamped_accepts.
 
 Each .hip file under csrc/ is compiled to an object in _build/ (in parallel),
-then linked into speculative_verify_gdn_amd/libgdn.so.  Flags:
+then linked into speculative_verify_gdn_amd/libgdn.so; the Python extension
+_gdn_binding.so (csrc/gdn_binding.cpp) is compiled beside it.  Flags:
   --offload-arch=gfx950          MI355X only
   -ffp-contract=off              every fused multiply-add is written out
   -fhip-fp32-correctly-rounded-divide-sqrt, -fno-gpu-flush-denormals-to-zero
@@ -68,6 +69,28 @@ def _compile(src: str, build_dir: str = BUILD, extra=()) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """Compile the Python extension that marshals the cache and attention calls (csrc/gdn_binding.cpp) with the
+    host compiler, against torch's headers; returns its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(PKG, "_gdn_binding.so")
+    tmp = lib + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *("-isystem" + d for d in cpp_extension.include_paths()), "-I" + sysconfig.get_paths()["include"],
+           "-o", tmp, os.path.join(CSRC, "gdn_binding.cpp"),
+           "-L" + cpp_extension.TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the binding failed to compile:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, lib)
+    return lib
+
+
 def build(verbose: bool = False, timeline: bool = False, debug: bool = False) -> str:
     """Compile every HIP source and link libgdn.so (with timeline libgdn_timeline.so, with debug
     libgdn_debug.so); returns its path."""
@@ -86,6 +109,10 @@ def build(verbose: bool = False, timeline: bool = False, debug: bool = False) ->
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, lib)
+    if not variant:
+        binding = build_binding()
+        if verbose:
+            print("built", binding)
     if verbose:
         print("built", lib)
     return lib

@@ -1,4 +1,5 @@
-"""ctypes binding of libgdn.so (include/gdn.h) for torch device tensors.
+"""Binding of libgdn.so (include/gdn.h) for torch device tensors, by ctypes (the
+cache and attention calls by a compiled extension, csrc/gdn_binding.cpp).
 
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  Each function takes torch tensors that already live on the GPU,
@@ -329,104 +330,55 @@ def verify_tree_step(x, w, parent, beta_raw, alpha, dt_bias, A_log, H, o, y, Hk,
 
 
 # ---------------------------------------------------------------- paged cache and window attention
-def _i32(**ts):
-    """The int32 device arrays of a cache call: name = (tensor or None, its shape)."""
-    for name, (t, shape) in ts.items():
-        if t is None:
-            continue
-        _dev(t)
-        if t.dtype != torch.int32:
-            raise TypeError("%s must be int32, not %s" % (name, t.dtype))
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+# These calls take a few microseconds on the GPU and many tensors, so their checks and conversions are compiled
+# (csrc/gdn_binding.cpp); there is no other path: a missing extension raises on the first call.
+_ext = None
 
 
-def _pool(pool):
-    """(planes, n_pages, Hkv, page, D, dtype) of a pool [planes][n_pages][Hkv][page][D]."""
-    _dev(pool)
-    if pool.dim() != 5:
-        raise ValueError("pool has shape %s, not [planes][n_pages][Hkv][page][D]" % (tuple(pool.shape),))
-    return (*pool.shape, _dtype(pool))
+def _B():
+    global _ext
+    if _ext is None:
+        try:
+            from . import _gdn_binding
+        except ImportError as e:
+            raise FileNotFoundError("libgdn's binding is not built (%s); run python -m speculative_verify_gdn_amd.build"
+                                    % e) from e
+        _ext = _gdn_binding
+    return _ext
 
 
-def _plane_pair(k_pages, v_pages):
-    _dev(k_pages, v_pages)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
-        raise ValueError("k_pages and v_pages must be planes [n_pages][Hkv][page][D] of one shape and type")
-    return (*k_pages.shape, _dtype(k_pages))
-
-
-def _tokens(name, x, shape, dtype):
-    """Elements between the tokens of x [B][K][heads][D], which may be a slice of wider rows (dense heads)."""
-    if not x.is_cuda:
-        raise ValueError("libgdn takes device tensors")
-    if tuple(x.shape) != tuple(shape) or _dtype(x) != dtype:
-        raise ValueError("%s must be %s of the cache's type" % (name, list(shape)))
-    B, K, H, D = x.shape
-    if x.numel() == 0 or x.is_contiguous():
-        return H * D
-    st = x.stride()
-    stride = st[1] if K > 1 else st[0]
-    if (D > 1 and st[3] != 1) or (H > 1 and st[2] != D) or (B > 1 and st[0] != K * stride) or stride < H * D:
-        raise ValueError("%s must have dense heads and evenly spaced tokens" % name)
-    return stride
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kv_reserve(lens, add, table, ref, page, granted, stream=None):
     """gdn_kv_reserve: lowest free pages for the next add [B] tokens behind lens [B]; table [B][P] and ref
     [n_pages] are updated, granted [B] <- add or 0.  All int32."""
-    B, P = table.shape
-    _i32(lens=(lens, (B,)), add=(add, (B,)), table=(table, (B, P)), ref=(ref, (ref.numel(),)), granted=(granted, (B,)))
-    _check(_L().gdn_kv_reserve(_p(lens), _p(add), _p(table), _p(ref), _p(granted), B, P, ref.numel(), int(page),
-                               _stream(stream)))
+    _check(_B().kv_reserve(_L()._handle, _raw(stream), lens, add, table, ref, granted, page))
 
 
 def kv_append(k, v, k_pages, v_pages, lens, table, count=None, stream=None):
     """gdn_kv_append: k, v [B][K][Hkv][D] (dense heads; tokens may be slices of wider rows) to the positions
     lens[b]+t, t < count[b] (None: K), of the planes k_pages, v_pages [n_pages][Hkv][page][D]."""
-    n_pages, Hkv, page, D, dt = _plane_pair(k_pages, v_pages)
-    B, P = table.shape
-    K = k.shape[1]
-    stride = _tokens("k", k, (B, K, Hkv, D), dt)
-    if _tokens("v", v, (B, K, Hkv, D), dt) != stride:
-        raise ValueError("k and v must have the same token stride")
-    _i32(lens=(lens, (B,)), table=(table, (B, P)), count=(count, (B,)))
-    _check(_L().gdn_kv_append(_p(k), _p(v), stride, _p(k_pages), _p(v_pages), _p(lens), _p(count), _p(table), B, K, Hkv,
-                              D, page, n_pages, P, dt, _stream(stream)))
+    _check(_B().kv_append(_L()._handle, _raw(stream), k, v, k_pages, v_pages, lens, count, table))
 
 
 def kv_rollback_tree(node, parent, lens, table, ref, pool, lens_out, count=None, N=None, stream=None):
     """gdn_kv_rollback_tree: sequence b keeps the path to node[b] of its window (parent [B][N]; None: a chain of N
     tokens, node = accepted - 1): its tokens move to lens[b].. in every plane of pool, lens_out <- the new
     lengths (lens_out may be lens), later pages are given back."""
-    planes, n_pages, Hkv, page, D, dt = _pool(pool)
-    B, P = table.shape
-    if parent is None and N is None:
-        raise ValueError("a chain (parent=None) needs its window length N")
-    N = parent.shape[1] if parent is not None else int(N)
-    _i32(node=(node, (B,)), parent=(parent, (B, N)), lens=(lens, (B,)), table=(table, (B, P)), ref=(ref, (n_pages,)),
-         lens_out=(lens_out, (B,)), count=(count, (B,)))
-    _check(_L().gdn_kv_rollback_tree(_p(node), _p(parent), _p(lens), _p(count), _p(table), _p(ref), _p(pool),
-                                     _p(lens_out), B, N, P, planes, n_pages, Hkv, page, D, dt, _stream(stream)))
+    _check(_B().kv_rollback_tree(_L()._handle, _raw(stream), node, parent, lens, count, table, ref, pool, lens_out, N))
 
 
 def kv_free(rows, lens, table, ref, stream=None):
     """gdn_kv_free: the rows [n] of table [B][P] give back their pages (ref [n_pages]); their lens become 0."""
-    B, P = table.shape
-    _i32(rows=(rows, (rows.numel(),)), lens=(lens, (B,)), table=(table, (B, P)), ref=(ref, (ref.numel(),)))
-    _check(_L().gdn_kv_free(_p(rows), _p(lens), _p(table), _p(ref), rows.numel(), B, P, ref.numel(), _stream(stream)))
+    _check(_B().kv_free(_L()._handle, _raw(stream), rows, lens, table, ref))
 
 
 def kv_fork(src, dst, lens, table, ref, pool, granted, stream=None):
     """gdn_kv_fork: the empty rows dst [n] become copies of the rows src [n]: full pages shared, a partial last
     page copied in every plane of pool; granted [n] <- 1 or 0."""
-    planes, n_pages, Hkv, page, D, dt = _pool(pool)
-    B, P = table.shape
-    n = src.numel()
-    _i32(src=(src, (n,)), dst=(dst, (n,)), lens=(lens, (B,)), table=(table, (B, P)), ref=(ref, (n_pages,)),
-         granted=(granted, (n,)))
-    _check(_L().gdn_kv_fork(_p(src), _p(dst), _p(lens), _p(table), _p(ref), _p(pool), _p(granted), n, B, P, planes,
-                            n_pages, Hkv, page, D, dt, _stream(stream)))
+    _check(_B().kv_fork(_L()._handle, _raw(stream), src, dst, lens, table, ref, pool, granted))
 
 
 def _bytes(fn, *sizes):
@@ -443,20 +395,12 @@ def kv_compact_workspace(ref):
 def kv_compact(table, ref, pool, table_out, ref_out, workspace, stream=None):
     """gdn_kv_compact: the pages in use move to the lowest ids of pool; table_out and ref_out receive table (any
     shape) and ref [n_pages] under the new ids."""
-    planes, n_pages, Hkv, page, D, dt = _pool(pool)
-    _i32(table=(table, table.shape), ref=(ref, (n_pages,)), table_out=(table_out, table.shape), ref_out=(ref_out, (n_pages,)))
-    _dev(workspace)
-    _check(_L().gdn_kv_compact(_p(table), _p(ref), _p(pool), _p(table_out), _p(ref_out), _p(workspace),
-                               workspace.numel() * workspace.element_size(), table.numel(), planes, n_pages, Hkv, page,
-                               D, dt, _stream(stream)))
+    _check(_B().kv_compact(_L()._handle, _raw(stream), table, ref, pool, table_out, ref_out, workspace))
 
 
 def kv_copy(src, dst, pool, stream=None):
     """gdn_kv_copy: page src[i] to page dst[i] in every plane of pool."""
-    planes, n_pages, Hkv, page, D, dt = _pool(pool)
-    n = src.numel()
-    _i32(src=(src, (n,)), dst=(dst, (n,)))
-    _check(_L().gdn_kv_copy(_p(src), _p(dst), _p(pool), n, planes, n_pages, Hkv, page, D, dt, _stream(stream)))
+    _check(_B().kv_copy(_L()._handle, _raw(stream), src, dst, pool))
 
 
 def attn_workspace(q, k_pages, table, prefix_len=0):
@@ -473,19 +417,5 @@ def attn_verify(q, k_pages, v_pages, lens, table, o, prefix_len=0, count=None, p
     committed keys 0..lens[b]-1 and the window's own (already appended at lens[b]..): causal, or the ancestors
     of parent [B][K].  o [B][K][Hq][D], lse [B][K][Hq] f32 or None; count [B]: tokens per window; prefix_len: tokens
     whose pages every sequence that long shares; scale None: D ** -0.5; workspace: attn_workspace(...)."""
-    n_pages, Hkv, page, D, dt = _plane_pair(k_pages, v_pages)
-    B, P = table.shape
-    K, Hq = q.shape[1], q.shape[2]
-    stride = _tokens("q", q, (B, K, Hq, D), dt)
-    _dev(o, lse, workspace)
-    if workspace is None:
-        raise ValueError("attn_verify needs a workspace (attn_workspace)")
-    if o.shape != q.shape or o.dtype != q.dtype:
-        raise ValueError("o must have q's shape and type")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, K, Hq)):
-        raise ValueError("lse must be float32 [B][K][Hq]")
-    _i32(lens=(lens, (B,)), table=(table, (B, P)), count=(count, (B,)), parent=(parent, (B, K)))
-    _check(_L().gdn_attn_verify(_p(q), stride, _p(k_pages), _p(v_pages), _p(lens), _p(count), _p(parent), _p(table),
-                                _p(o), _p(lse), _p(workspace), workspace.numel() * workspace.element_size(), B, K, Hq,
-                                Hkv, D, page, n_pages, P, int(prefix_len), float(D ** -0.5 if scale is None else scale),
-                                dt, _stream(stream)))
+    _check(_B().attn_verify(_L()._handle, _raw(stream), q, k_pages, v_pages, lens, count, parent, table, o, lse,
+                            workspace, prefix_len, scale))
