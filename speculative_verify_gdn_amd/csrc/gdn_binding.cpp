@@ -18,6 +18,8 @@
 
 #include <cmath>
 #include <cstdarg>
+#include <deque>
+#include <exception>
 #include <initializer_list>
 
 #include <ATen/core/Tensor.h>
@@ -52,8 +54,8 @@ struct Lib {
     void* handle = nullptr;
 };
 
-// the release and the debug build at most are open at once (a library is never closed)
-Lib g_libs[8];
+// the builds seen so far (a library is never closed, and a deque's elements stay where they are)
+std::deque<Lib> g_libs;
 
 template <typename F>
 void symbol(void* handle, F& f, const char* name)
@@ -69,24 +71,20 @@ const Lib& lib_of(PyObject* o)
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "libgdn handle is null");
         throw Raised{};
     }
-    for (Lib& l : g_libs) {
+    for (const Lib& l : g_libs)
         if (l.handle == h) return l;
-        if (!l.handle) {
-            Lib n;
-            symbol(h, n.kv_reserve, "gdn_kv_reserve");
-            symbol(h, n.kv_append, "gdn_kv_append");
-            symbol(h, n.kv_rollback_tree, "gdn_kv_rollback_tree");
-            symbol(h, n.kv_free, "gdn_kv_free");
-            symbol(h, n.kv_fork, "gdn_kv_fork");
-            symbol(h, n.kv_compact, "gdn_kv_compact");
-            symbol(h, n.kv_copy, "gdn_kv_copy");
-            symbol(h, n.attn_verify, "gdn_attn_verify");
-            n.handle = h;
-            l = n;
-            return l;
-        }
-    }
-    raise(PyExc_RuntimeError, "more builds of libgdn are loaded than are expected");
+    Lib n;
+    symbol(h, n.kv_reserve, "gdn_kv_reserve");
+    symbol(h, n.kv_append, "gdn_kv_append");
+    symbol(h, n.kv_rollback_tree, "gdn_kv_rollback_tree");
+    symbol(h, n.kv_free, "gdn_kv_free");
+    symbol(h, n.kv_fork, "gdn_kv_fork");
+    symbol(h, n.kv_compact, "gdn_kv_compact");
+    symbol(h, n.kv_copy, "gdn_kv_copy");
+    symbol(h, n.attn_verify, "gdn_attn_verify");
+    n.handle = h;
+    g_libs.push_back(n);
+    return g_libs.back();
 }
 
 PyObject* g_raw_stream;  // torch's current stream of a device, as an integer
