@@ -11,9 +11,9 @@
 // key/value head.  The shared list has an item for each (head, split of the prefix,
 // row tile), whose row tiles run through the window tokens of every sequence that
 // holds the prefix; the splits are as many as make the items fill the grid best.
-// The own list has the units (sequence, head, key tile) in this order, and part i of
-// n has the units [i U / n, (i+1) U / n), so the load is even whatever the lengths are;
-// a part's row tiles go to neighbouring workgroups (with windows of unequal length
+// The own list has the units (sequence, head, key tile) in this order, with
+// kStartup empty ones before each head's tiles, and part i of n has the units
+// [i U / n, (i+1) U / n), so the load is even whatever the lengths are; a part's row tiles go to neighbouring workgroups (with windows of unequal length
 // the row tiles are units of the list instead).  No host knowledge of lengths is
 // needed: each workgroup sums them over the sequences by itself.  The workgroups
 // take the shared items in their order and the own parts from the last workgroup
@@ -48,20 +48,20 @@ constexpr float kNoMax = -1e37f;   // the reference of a row that has seen no ke
 constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// M rows by N keys over the 8 waves: RW groups of rows x KW groups of keys x DW parts of the output's columns;
-// a wave has MW times 16 rows
-template <bool BF16_, int D_, int RW_, int KW_, int DW_, int MW_>
+// M rows by N keys over the 8 waves: RW groups of 16 rows x KW groups of keys x DW parts of the output's columns
+template <bool BF16_, int D_, int RW_, int KW_, int DW_>
 struct Cfg {
     static constexpr bool BF16 = BF16_;
-    static constexpr int D = D_, RW = RW_, KW = KW_, DW = DW_, MW = MW_;
+    static constexpr int D = D_, RW = RW_, KW = KW_, DW = DW_;
     static_assert(RW * KW * DW == kWaves, "every wave has a part");
-    static constexpr int M = 16 * MW * RW;
+    static constexpr int M = 16 * RW;
     static constexpr int ES = BF16 ? 2 : 4, ROW = D * ES, CH = ROW / 16;
     static constexpr int N = 8192 / D;             // keys a tile: K and V are 32 KB in bf16, 64 KB in fp32
     static constexpr int KF = N / KW / 16;         // 16-key groups of a wave
     static constexpr int DB = D / 16 / DW;         // 16-column groups of a wave's output
     static constexpr int MAT = N * ROW, STAGE = 2 * MAT;
-    static constexpr int QC = BF16 ? D / 32 : D / 16;  // registers groups of a row's q
+    static constexpr int QC = BF16 ? D / 32 : D / 16;  // 16-byte pieces a lane holds of a row's q
+    static_assert((KW - 1) * DW * RW * DB * 1024 <= STAGE, "what the waves of other keys leave fits one buffer");
 };
 
 // where each 16-byte chunk of a key's row sits: chunk ^ swizzle(key)
@@ -74,32 +74,49 @@ __device__ __forceinline__ constexpr int v_swizzle(int key)
     else return C::CH >= 16 ? (key & 7) << 1 : ((key >> 1) & 3) << 1;
 }
 
+// What a piece costs beside its tiles (its first reads, its end), in tiles: cutting by tiles alone left the workgroups
+// with many short sequences at work twice as long as the others.
+constexpr int kStartup = 6;
+
 // what a sequence asks for
 struct Seq {
     int cnt, len, end, start, tiles, rts;
     bool part;
-    int units;
+    int segs;        // runs of tiles: (head, row tile) pairs
 };
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
+__device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int count, int N, int M)
 {
     Seq s;
     const int cap = a.P << a.page_log2;
-    s.cnt = a.count ? min(max(a.count[b], 0), a.K) : a.K;
-    s.len = min(max(a.lens[b], 0), cap);
+    s.cnt = min(max(count, 0), a.K);
+    s.len = min(max(len, 0), cap);
     s.end = (int)min((long long)s.len + s.cnt, (long long)cap);
     s.part = a.prefix > 0 && s.len >= a.prefix && s.cnt > 0;
     s.start = s.part ? a.prefix : 0;
     s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) / N : 0;
     s.rts = (s.cnt * (a.Hq / a.Hkv) + M - 1) / M;
-    s.units = a.Hkv * s.tiles * (a.count ? s.rts : 1);
+    s.segs = s.tiles > 0 ? a.Hkv * (a.count ? s.rts : 1) : 0;
     return s;
+}
+
+// (by values: a conditional of two lvalues would put the arguments in memory)
+__device__ __forceinline__ int count_of(const AttnArgs& a, int b)
+{
+    int n = a.K;
+    if (a.count) n = a.count[b];
+    return n;
+}
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b, int N, int M)
+{
+    return seq_from(a, a.lens[b], count_of(a, b), N, M);
 }
 
 // the lists' lengths and cuts, for the joining kernel
 struct Head {
     int row_tiles, splits;       // of the shared list
-    int own_units, own_parts;
+    int own_units, own_parts, own_extra;
 };
 struct PlanSeq {
     int own_base;   // own units of the sequences before
@@ -142,7 +159,6 @@ __device__ __forceinline__ int part_of(int units, int n, int u)
 // Into how many splits the prefix goes: for s of them, `segs` heads and row tiles take ceil(segs s / nb) rounds of
 // ceil(tiles / s) tiles and about kStartup tiles' time for a piece's first reads and its end.  A lane tries each s;
 // there are at most max(segs, 2 nb) items.
-constexpr int kStartup = 6;
 __device__ __forceinline__ int splits_for(int segs, int tiles, int nb)
 {
     const int n = (threadIdx.x & 63) + 1;
@@ -188,7 +204,7 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, con
                      "global_load_lds_dwordx4 %2, %3 offset:1024"
                      :
                      : "s"(lds), "v"(voff[0]), "v"(voff[1]), "s"(base)
-                     : "memory", "m0");
+                     : "memory");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %1, %5\n\t"
@@ -197,7 +213,7 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, con
                      "global_load_lds_dwordx4 %4, %5 offset:3072"
                      :
                      : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(base)
-                     : "memory", "m0");
+                     : "memory");
 }
 
 __device__ __forceinline__ void load_wait()
@@ -233,15 +249,12 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
     return __builtin_bit_cast(uint32_t, h);
 }
 
-// nodes on the path from a root to each node: lane i returns those of node i (called by a whole wave, K <= 64)
-__device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, int K)
+// nodes on the path from a root to each node: lane i has the parent of node i (one that is not below it: a root) and
+// gets those of node i (called by a whole wave)
+__device__ __forceinline__ unsigned long long ancestors(int parent)
 {
     const int lane = threadIdx.x & 63;
-    int up = -1;
-    if (lane < K) {
-        const int p = parent ? parent[lane] : lane - 1;
-        up = p >= 0 && p < lane ? p : -1;
-    }
+    int up = parent >= 0 && parent < lane ? parent : -1;
     unsigned long long path = 1ull << lane;
 #pragma unroll
     for (int d = 1; d < kKvWindowMax; d <<= 1) {
@@ -260,431 +273,59 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t* parent, i
 struct Small {
     int part[kWaves];
     int found_b, found_off;
-    int tok_base[kThreads];   // window tokens of the prefix-holding sequences before a thread's own
-    int bad_value;
-    unsigned long long path[64];
-    int tok[132];             // window tokens (b * K + t) of a shared row tile
-    float2 ml[kWaves][32];    // (m, l) of the waves' rows, to be joined
+    // what pieces are described from: uniform values, read again where they are needed (in scalar registers they
+    // would be spilled to vector registers all through the loop)
+    int own_part, rt_block, own_u1, extra;
+    int row_tiles, key_tiles, splits, tok_total;
+    const char* base[4];                // in the workspace: a of shared and of own rows, their (m, l)
+    int bad_value;                      // the number of the last piece that had a window value that is not finite
+    int tok_base[kThreads];             // window tokens of the prefix-holding sequences before a thread's own
+    int len[kThreads], count[kThreads]; // lengths and windows of the first sequences (all of them, mostly)
+    unsigned long long path[2][64];     // the window's nodes on the path to each node, by the piece's number
+    int tok[132];                       // window tokens (b * K + t) of a shared row tile
+    float2 ml[kWaves][16];              // (m, l) of the waves' rows, to be joined
 };
 
-struct PieceIn {
-    const int32_t* row;       // table row
-    const int32_t* parent;    // of the sequence, or nullptr
-    int h, p0, tiles;         // key/value head, first position, tiles
-    int len, end;             // window's first position and the end of what is there
-    bool window;              // keys at len.. are seen by their descendants only
+// where a piece starts: own: sequence b, `off` units into it, unit u of the list; shared: item it
+struct Ref {
+    int b, off, u, it;
 };
 
-struct PieceOut {
-    bool direct;              // the whole row: o and lse at once
-    float* o;                 // [M][D]
-    float2* ml;               // [M]
+// a run of tiles of one row tile
+struct Piece {
+    int b;                  // whose table row it reads
+    int h, p0, tiles;       // key/value head, first position, tiles
+    int len, end;           // the window's first position and the end of what is there
+    int r0, tok0, tok1;     // rows r0.. of the tokens tok0 .. tok1-1 (row r is of token r / G)
+    int slot;               // workspace slot; -1: the rows are whole, o and lse are written at once
 };
 
-// a row of the tile: token b * K + t, t, and the query head of its group; false for a row that is not there
-struct RowId {
-    int tok, t, g;
-    bool live;
-};
-
-template <class C, class RowFn>
-__device__ __forceinline__ void run_piece(const AttnArgs& a, char* sm, Small& s, const PieceIn& in,
-                                          const PieceOut& out, RowFn row_of)
+// The kernel's arguments, loaded anew (the first argument is at the start of their segment): used where the time of
+// a scalar load does not count, to keep them out of the registers of the loop.
+__device__ __forceinline__ const AttnArgs& args_again()
 {
-    constexpr int MW = C::MW, KF = C::KF, DB = C::DB, QC = C::QC, N = C::N;
-    const int lane = threadIdx.x & 63, w = uni(threadIdx.x >> 6);
-    const int rw = w % C::RW, kw = (w / C::RW) % C::KW, dw = w / (C::RW * C::KW);
-    const int n16 = lane & 15, grp = lane >> 4;
-    const int page_mask = (1 << a.page_log2) - 1;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)sm;
-    const int G = a.Hq / a.Hkv;
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttnArgs*)p;
+}
 
-    // ---- the pages: lane i holds slot first + i (a missing one as page 0, flagged), and the 64 slots after
-    auto slot_id = [&](int sl, bool& bad) {
-        int id = sl < a.P ? in.row[sl] : -1;
-        bad = (unsigned)id >= (unsigned)a.n_pages;
-        return bad ? 0 : id;
-    };
-    int first = in.p0 >> a.page_log2;
-    bool bad_lane, bad_lane2;
-    int ids = slot_id(first + lane, bad_lane), ids2 = slot_id(first + 64 + lane, bad_lane2);
-    unsigned long long bad = __ballot(bad_lane), bad2 = __ballot(bad_lane2);
-
-    // ---- tile loads: wave w brings the keys w N/8 .. of K and V, in groups of up to 16 keys (of one page, as a
-    // page has 16 at least), a group in runs of CNT KB
-    constexpr int WK = N / kWaves, GK = WK < 16 ? WK : 16, KPI = 1024 / C::ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
-    const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_log2) * C::ROW;
-    const uint32_t head_off = ((uint32_t)in.h << a.page_log2) * C::ROW;
-    const int lkey = lane / C::CH, lch = lane % C::CH;
-    // (the i-th KB of a group is i KPI keys on: bits of the key that no other part of it has, so they flip in)
-    const int key0 = w * WK + lkey;
-    const uint32_t k_off = lkey * C::ROW + ((lch ^ k_swizzle<C>(key0 & 15)) << 4);
-    const uint32_t v_off = lkey * C::ROW + ((lch ^ v_swizzle<C>(key0 & 15)) << 4);
-    auto issue = [&](int j, int buf) {
-        const int pt = in.p0 + j * N;
-        int s0 = (pt >> a.page_log2) - first;
-        if (s0 >= 64) {
-            ids = ids2;
-            bad = bad2;
-            first += 64;
-            s0 -= 64;
-            ids2 = slot_id(first + 64 + lane, bad_lane2);
-            bad2 = __ballot(bad_lane2);
-        }
-#pragma unroll
-        for (int g = 0; g < WK / GK; ++g) {
-            const int key = w * WK + g * GK;
-            const uint32_t id = __builtin_amdgcn_readlane(ids, s0 + (key >> a.page_log2));
-            const uint64_t off = (uint64_t)id * page_bytes + (head_off + ((pt + key) & page_mask) * C::ROW);
-            const uint32_t to = lds0 + buf * C::STAGE + key * C::ROW;
-#pragma unroll
-            for (int i = 0; i < NI; i += CNT) {
-                uint32_t ko[CNT], vo[CNT];
-#pragma unroll
-                for (int e = 0; e < CNT; ++e) {
-                    ko[e] = k_off ^ (k_swizzle<C>((i + e) * KPI) << 4);
-                    vo[e] = v_off ^ (v_swizzle<C>((i + e) * KPI) << 4);
-                }
-                load_lds<CNT>(to + i * 1024, ko, static_cast<const char*>(a.k_pages) + off + i * 1024);
-                load_lds<CNT>(to + C::MAT + i * 1024, vo, static_cast<const char*>(a.v_pages) + off + i * 1024);
-            }
-        }
-        const int slots = max(N >> a.page_log2, 1);
-        return (unsigned)(bad >> s0) & ((1u << slots) - 1);   // missing pages of the tile
-    };
-    if (threadIdx.x == 0) s.bad_value = 0;   // (before the first barrier of the loop)
-    unsigned miss_next = issue(0, 0);
-
-    // ---- the rows
-    // Row r of this lane, formed anew wherever it is asked for: kept, it would take registers through the loop.
-    auto row_id = [&](int r) {
-        int row = (rw * MW + r) * 16 + (threadIdx.x & 15);
-        asm volatile("" : "+v"(row));
-        return row_of(row);
-    };
-    // the window's nodes on the path to each node, for the tiles that need them
-    if (in.window && w == 0) s.path[lane] = ancestors(in.parent, a.K);
-    float m[MW], l[MW];
-    uint4 q[MW][QC];
-    const float c = fabsf(a.scale) * kLog2e;
-    bool any = false;
-    {
-        const uint32_t flip = a.scale < 0.f ? (C::BF16 ? 0x80008000u : 0x80000000u) : 0u;  // the sign goes into q
-#pragma unroll
-        for (int r = 0; r < MW; ++r) {
-            const RowId id = row_id(r);
-            any |= id.live;
-            m[r] = kNoMax;
-            l[r] = 0.f;
-            const char* qp = static_cast<const char*>(a.q) +
-                             ((size_t)id.tok * a.q_stride + (size_t)(in.h * G + id.g) * C::D) * C::ES + grp * 16;
-#pragma unroll
-            for (int e = 0; e < QC; ++e) {
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (id.live) u = *reinterpret_cast<const uint4*>(qp + e * 64);
-                q[r][e] = make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip);
-            }
-        }
-    }
-    const bool alive = __any(any);   // a wave without rows only loads
-    f32x4_t o[DB][MW];
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int r = 0; r < MW; ++r) o[d][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    // LDS addresses of this lane within a tile: chunk c of a row sits at its lane's chunk with the low bits of c
-    // flipped in, and further chunks, keys and 16-key groups lie at constant distances
-    const int kbase = kw * (N / C::KW);
-    const int vkey = C::BF16 ? 4 * grp + (n16 >> 2) : 4 * grp;   // (fp32 adds the register's index)
-    const uint32_t k_lane = lds0 + (kbase + n16) * C::ROW + ((grp ^ k_swizzle<C>(n16)) << 4);
-    const uint32_t v_lane =
-        lds0 + C::MAT + (kbase + vkey) * C::ROW + (dw * DB * 16 * C::ES & ~255) +
-        (C::BF16 ? ((((n16 >> 1) & 1) ^ v_swizzle<C>(vkey) ^ (2 * dw * DB & 15)) << 4) + (n16 & 1) * 8
-                 : (((n16 >> 2) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 3) * 4);
-    static_assert(C::DW == 1 || DB * 16 * C::ES >= 128, "a part starts on a half or whole swizzle group");
-
-    for (int j = 0; j < in.tiles; ++j) {
-        const unsigned miss = miss_next;
-        load_wait();
-        block_barrier();   // every wave's part of this tile is there, and nobody reads the other buffer any more
-        if (j + 1 < in.tiles) miss_next = issue(j + 1, (j + 1) & 1);
-        char* kt = sm + (j & 1) * C::STAGE;
-        char* vt = kt + C::MAT;
-        const int pt = in.p0 + j * N;
-        const bool masked = miss != 0 || (in.window && pt + N > in.len) || pt + N > in.end;
-
-        // Values nobody may see are cleared where they lie (0 times NaN is NaN), and so are the window's that are
-        // not finite: only some rows see them, and get them at the end.
-        if (masked) {
-            for (int e = threadIdx.x; e < N * C::CH; e += kThreads) {
-                const int key = e / C::CH, pos = pt + key;
-                uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
-                if (pos >= in.end || (miss >> (key >> a.page_log2) & 1)) {
-                    *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
-                } else if (in.window && pos >= in.len) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t u = v[i];
-                        uint32_t keep = u;
-                        if ((u & 0x7f800000u) == 0x7f800000u) keep &= C::BF16 ? 0xffffu : 0u;
-                        if (C::BF16 && (u & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
-                        if (keep != u) {
-                            v[i] = keep;
-                            s.bad_value = 1;
-                        }
-                    }
-                }
-            }
-            block_barrier();
-        }
-        if (!alive) continue;
-
-        // opaque, so that the addresses are formed from them in the loop and not kept in dozens of registers
-        uint32_t k_at = k_lane + (j & 1) * C::STAGE, v_at = v_lane + (j & 1) * C::STAGE;
-        asm volatile("" : "+v"(k_at), "+v"(v_at));
-
-        // ---- S^T = K Q^T
-        f32x4_t x[KF][MW];
-#pragma unroll
-        for (int k = 0; k < KF; ++k)
-#pragma unroll
-            for (int r = 0; r < MW; ++r) x[k][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < QC; ++e)
-#pragma unroll
-            for (int k = 0; k < KF; ++k) {
-                const uint4 u = lds_read16((k_at ^ (uint32_t)(((4 * e) & (C::CH - 1) & 15) << 4)) +
-                                           (4 * e / 16) * 256 + 16 * k * C::ROW);
-#pragma unroll
-                for (int r = 0; r < MW; ++r) {
-                    if constexpr (C::BF16) {
-                        x[k][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u),
-                                                                          __builtin_bit_cast(bf16x8_t, q[r][e]),
-                                                                          x[k][r], 0, 0, 0);
-                    } else {
-                        const uint32_t ua[4] = {u.x, u.y, u.z, u.w};
-                        const uint32_t qa[4] = {q[r][e].x, q[r][e].y, q[r][e].z, q[r][e].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[k][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ua[i]),
-                                                                           __uint_as_float(qa[i]), x[k][r], 0, 0, 0);
-                    }
-                }
-            }
-
-        // ---- weights e^{x-m}
-        unsigned seen[MW];   // of a masked tile: a bit for each of this lane's keys
-        if (masked) {
-#pragma unroll
-            for (int r = 0; r < MW; ++r) {
-                seen[r] = 0;
-                const unsigned long long sees = in.window ? s.path[row_id(r).t & 63] : 0;
-#pragma unroll
-                for (int k = 0; k < KF; ++k) {
-                    const int key = kbase + 16 * k + 4 * grp;
-                    // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
-                    // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
-                    const int rel = pt + key - in.len, left = in.end - (pt + key);
-                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees >> (max(rel, 0) & 63));
-                    const int old = min(max(-rel, 0), 4);
-                    unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
-                    bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
-                    seen[r] |= bits << (4 * k);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[k][r][i] = (bits >> i & 1) ? x[k][r][i] : -INFINITY;
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < MW; ++r) {
-            float t = x[0][r][0];
-#pragma unroll
-            for (int k = 0; k < KF; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) t = fmaxf(t, x[k][r][i]);
-            if (__any(t * c > m[r] + kSlack)) {
-                t = fmaxf(t, __shfl_xor(t, 16, 64));
-                t = fmaxf(t, __shfl_xor(t, 32, 64));
-                // a row moves its reference by its own keys alone, so its bits depend on no other row
-                const float mn = t * c > m[r] + kSlack ? t * c : m[r], f = exp2_(m[r] - mn);
-                m[r] = mn;
-                l[r] *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[d][r] *= f;
-            }
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < KF; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p = exp2_(__builtin_fmaf(x[k][r][i], c, -m[r]));
-                    if (masked) p = (seen[r] >> (4 * k + i) & 1) ? p : 0.f;
-                    x[k][r][i] = p;
-                    sum += p;
-                }
-            l[r] += sum;
-        }
-
-        // ---- O^T += V^T P^T
-        if constexpr (C::BF16) {
-            // the weights enter the product in bf16, as v is: half a step of 2^-8 each, unbiased
-            auto v_frag = [&](int k, int d) {
-                lds_char* at = (lds_char*)(uintptr_t)((v_at ^ (uint32_t)((d & (C::CH / 2 - 1) & 7) << 5)) +
-                                                      (d / 8) * 256 + 16 * k * C::ROW);
-                return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at));
-            };
-            if constexpr (KF == 1) {
-                uint2 p[MW];
-#pragma unroll
-                for (int r = 0; r < MW; ++r)
-                    p[r] = make_uint2(pack2(x[0][r][0], x[0][r][1]), pack2(x[0][r][2], x[0][r][3]));
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const bf16x4_t v = __builtin_bit_cast(bf16x4_t, v_frag(0, d));
-#pragma unroll
-                    for (int r = 0; r < MW; ++r)
-                        o[d][r] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, __builtin_bit_cast(bf16x4_t, p[r]),
-                                                                            o[d][r], 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < KF; k += 2) {
-                    uint4 p[MW];
-#pragma unroll
-                    for (int r = 0; r < MW; ++r)
-                        p[r] = make_uint4(pack2(x[k][r][0], x[k][r][1]), pack2(x[k][r][2], x[k][r][3]),
-                                          pack2(x[k + 1][r][0], x[k + 1][r][1]), pack2(x[k + 1][r][2], x[k + 1][r][3]));
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const uint2 v0 = v_frag(k, d), v1 = v_frag(k + 1, d);
-                        const bf16x8_t v = __builtin_bit_cast(bf16x8_t, make_uint4(v0.x, v0.y, v1.x, v1.y));
-#pragma unroll
-                        for (int r = 0; r < MW; ++r)
-                            o[d][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, p[r]),
-                                                                              o[d][r], 0, 0, 0);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < KF; ++k)
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = lds_read4((v_at ^ (uint32_t)((d & 3) << 6)) + (d / 4) * 256 +
-                                                  (16 * k + i) * C::ROW);
-#pragma unroll
-                        for (int r = 0; r < MW; ++r)
-                            o[d][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, x[k][r][i], o[d][r], 0, 0, 0);
-                    }
-        }
-    }
-
-    // ---- the four lane groups' sums, then the waves of other keys, in a fixed order
-#pragma unroll
-    for (int r = 0; r < MW; ++r) {
-        l[r] += __shfl_xor(l[r], 16, 64);
-        l[r] += __shfl_xor(l[r], 32, 64);
-    }
-    const bool bad_value = uni(s.bad_value) != 0;
-    if (bad_value && alive) {
-        unsigned long long sees[MW];
-#pragma unroll
-        for (int r = 0; r < MW; ++r) sees[r] = s.path[row_id(r).t & 63];
-        // a window value that is not finite makes what it makes of the rows that see it
-        for (int pos = max(in.p0, in.len); pos < min(in.end, in.p0 + in.tiles * N); ++pos) {
-            if (((pos - in.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
-            bool missing;
-            const int page = slot_id(pos >> a.page_log2, missing);
-            if (missing) continue;
-            const size_t at = ((((size_t)page * a.Hkv + in.h) << a.page_log2) + (pos & page_mask)) * C::D;
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const float4 y = load4<C::BF16>(a.v_pages, at + (dw * DB + d) * 16 + 4 * grp);
-                const float ya[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int r = 0; r < MW; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if ((sees[r] >> (pos - in.len) & 1) && !(fabsf(ya[i]) < INFINITY)) o[d][r][i] += ya[i];
-            }
-        }
-    }
-    block_barrier();   // the tiles, and what this piece kept beside them, are done with
-    if constexpr (C::KW > 1) {
-        constexpr int F = DB * MW;
-        float* box = reinterpret_cast<float*>(sm);
-        auto at = [&](int k, int f) {
-            return reinterpret_cast<f32x4_t*>(box + ((((k - 1) * C::DW + dw) * C::RW + rw) * F + f) * 256 + lane * 4);
-        };
-        if (kw > 0) {
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int r = 0; r < MW; ++r) *at(kw, d * MW + r) = o[d][r];
-            if (grp == 0)
-#pragma unroll
-                for (int r = 0; r < MW; ++r) s.ml[w][r * 16 + n16] = make_float2(m[r], l[r]);
-        }
-        block_barrier();
-        if (kw == 0) {
-#pragma nounroll
-            for (int k = 1; k < C::KW; ++k) {
-#pragma unroll
-                for (int r = 0; r < MW; ++r) {
-                    const float2 v = s.ml[w + k * C::RW][r * 16 + n16];
-                    const float mn = fmaxf(m[r], v.x), f = exp2_(m[r] - mn), g = exp2_(v.x - mn);
-                    m[r] = mn;
-                    l[r] = l[r] * f + v.y * g;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[d][r] = o[d][r] * f + *at(k, d * MW + r) * g;
-                }
-            }
-        }
-        block_barrier();   // the next piece's tiles may come
-        if (kw > 0) return;
-    }
-#pragma unroll
-    for (int r = 0; r < MW; ++r) {
-        const RowId id = row_id(r);
-        if (!id.live) continue;
-        const int row = (rw * MW + r) * 16 + n16;
-        if (out.direct) {
-            const size_t at = (size_t)id.tok * a.Hq + in.h * G + id.g;
-            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const f32x4_t y = o[d][r] * inv;
-                const size_t e = at * C::D + (dw * DB + d) * 16 + 4 * grp;
-                if constexpr (C::BF16) {
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
-                        make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-                } else {
-                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.o) + e) = y;
-                }
-            }
-            if (a.lse && dw == 0 && grp == 0) a.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + __log2f(l[r])) * kLn2;
-        } else {
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-                *reinterpret_cast<f32x4_t*>(out.o + (size_t)row * C::D + (dw * DB + d) * 16 + 4 * grp) = o[d][r];
-            if (dw == 0 && grp == 0) out.ml[row] = make_float2(m[r], l[r]);
-        }
-    }
+// inclusive sum over the lanes of a wave, by DPP (row shifts, then the rows' last lanes to the rows after)
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
 }
 
 // exclusive sum over the workgroup's threads, and the total
 __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int inc = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(inc, d, 64);
-        if (lane >= d) inc += u;
-    }
+    const int inc = wave_scan(v);
     __syncthreads();
     if (lane == 63) s.part[w] = inc;
     __syncthreads();
@@ -697,6 +338,13 @@ __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
     return base + inc - v;
 }
 
+// which list a piece is of
+template <class Config, bool SHARED>
+struct ListTag {
+    using C = Config;
+    static constexpr bool shared = SHARED;
+};
+
 // SH: the shared list's configuration, or void
 template <class OW, class SH>
 __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnArgs a, int nb)
@@ -705,6 +353,11 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     extern __shared__ __attribute__((aligned(1024))) char sm[];
     Small& s = *reinterpret_cast<Small*>(sm + 2 * OW::STAGE);
     constexpr bool kShared = !__is_same(SH, void);
+    constexpr int N = OW::N, QC = OW::QC, ROW = OW::ROW;
+    using OwnTag = ListTag<OW, false>;
+    using SharedTag = ListTag<SH, true>;
+    const int lane = threadIdx.x & 63, w = uni(threadIdx.x >> 6);
+    const int n16 = lane & 15, grp = lane >> 4;
     const int G = a.Hq / a.Hkv;
     int MS = 0;
     if constexpr (kShared) MS = SH::M;
@@ -714,15 +367,21 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     // ---- the lists' lengths: thread i sums the sequences [b0, b1)
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
-    int mine = 0, toks = 0;
+    int my_tiles = 0, my_segs = 0, toks = 0;
     for (int b = b0; b < b1; ++b) {
-        const Seq q = seq_of(a, b, OW::N, OW::M);
-        mine += q.units;
+        const int len = a.lens[b], count = count_of(a, b);
+        const Seq q = seq_from(a, len, count, N, OW::M);
+        my_tiles += q.segs * q.tiles;
+        my_segs += q.segs;
         if (q.part) toks += q.cnt;
+        if (b < kThreads) {
+            s.len[b] = len;
+            s.count[b] = count;
+        }
     }
-    int own;
-    const int own_base = scan_int(mine, s, own);
-    own = uni(own);
+    if (threadIdx.x == 0) s.bad_value = 0;
+    int own_tiles, own_segs;
+    const int tiles_base = scan_int(my_tiles, s, own_tiles), segs_base = scan_int(my_segs, s, own_segs);
     int tok_total = 0, tok_base = 0;
     int items = 0, row_tiles = 0, key_tiles = 0, splits = 0;
     if constexpr (kShared) {
@@ -730,117 +389,595 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
         s.tok_base[threadIdx.x] = tok_base;
         tok_total = uni(tok_total);
         row_tiles = (tok_total * G + SH::M - 1) / SH::M;
-        key_tiles = (a.prefix + SH::N - 1) / SH::N;
+        key_tiles = (a.prefix + N - 1) / N;
         splits = splits_for(a.Hkv * row_tiles, key_tiles, nb);
         items = a.Hkv * row_tiles * splits;
     }
     const RowTiles rts_of = row_tiles_of(a, OW::M);
+    // (with a part for every tile there is nothing to even out)
+    const int extra = uni(own_tiles) <= nb / rts_of.grouped ? 0 : kStartup;
+    const int own = uni(own_tiles + extra * own_segs), own_base = tiles_base + extra * segs_base;
+    const int mine = my_tiles + extra * my_segs;
     const int own_parts = parts_for(nb, rts_of.grouped, own);
     const int blocks = min(nb, items + own_parts * rts_of.grouped);
     // consecutive workgroups of the lists on one XCD (workgroups are dealt to the 8 XCDs in turn)
     const int per_xcd = (blocks + 7) / 8;
     const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{row_tiles, splits, own, own_parts};
+        if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{row_tiles, splits, own, own_parts, extra};
         PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + wk.plan);
         int base = own_base, tok = tok_base;
         for (int b = b0; b < b1; ++b) {
-            const Seq q = seq_of(a, b, OW::N, OW::M);
+            const Seq q = seq_of(a, b, N, OW::M);
             plan[b] = PlanSeq{base, q.part ? tok : -1};
-            base += q.units;
+            base += q.segs * (q.tiles + extra);
             tok += q.part ? q.cnt : 0;
         }
     }
     if ((int)(blockIdx.x >> 3) >= per_xcd || lb >= blocks) return;
 
-    // the own part: its units [own_u, own_u1), the first in sequence own_b, own_off units into it
+    // ---- the own part: its units [own_u, own_u1), the first in sequence found_b, found_off units into it
     const int own_block = blocks - 1 - lb;
     const bool has_own = own_block < own_parts * rts_of.grouped;
-    const int part = own_block / rts_of.grouped, rt_block = own_block - part * rts_of.grouped;
-    const int own_u = has_own ? first_unit(own, own_parts, part) : 0;
-    const int own_u1 = has_own ? first_unit(own, own_parts, part + 1) : 0;
+    const int own_part = own_block / rts_of.grouped;
+    const int own_u = uni(has_own ? first_unit(own, own_parts, own_part) : 0);
+    const int own_u1 = uni(has_own ? first_unit(own, own_parts, own_part + 1) : 0);
     if (own_base <= own_u && own_u < own_base + mine) {
         int base = own_base;
         for (int b = b0; b < b1; ++b) {
-            const Seq q = seq_of(a, b, OW::N, OW::M);
-            if (own_u < base + q.units) {
+            const Seq q = seq_of(a, b, N, OW::M);
+            const int units = q.segs * (q.tiles + extra);
+            if (own_u < base + units) {
                 s.found_b = b;
                 s.found_off = own_u - base;
                 break;
             }
-            base += q.units;
+            base += units;
         }
     }
+    if (threadIdx.x == 0) {
+        s.own_part = own_part;
+        s.rt_block = own_block - own_part * rts_of.grouped;
+        s.own_u1 = own_u1;
+        s.extra = extra;
+        s.row_tiles = row_tiles;
+        s.key_tiles = key_tiles;
+        s.splits = splits;
+        s.tok_total = tok_total;
+        s.base[0] = work + wk.o_s;
+        s.base[1] = work + wk.o_o;
+        s.base[2] = work + wk.ml_s;
+        s.base[3] = work + wk.ml_o;
+    }
     __syncthreads();
-    const int own_b = uni(s.found_b), own_off = uni(s.found_off);
 
+    auto seq_at = [&](int b) {
+        int len, count;
+        if (b < kThreads) {
+            len = uni(s.len[b]);
+            count = uni(s.count[b]);
+        } else {
+            len = uni(args_again().lens[b]);
+            count = uni(count_of(args_again(), b));
+        }
+        return seq_from(args_again(), len, count, N, OW::M);
+    };
+    // the piece of the own list at a place (it may have no tile) and on past it, or of an item of the shared one
+    auto piece_of = [&](auto tag, Ref& r) {
+        const AttnArgs& a = args_again();
+        const int G = a.Hq / a.Hkv;
+        Piece p;
+        if constexpr (tag.shared) {
+            const int row_tiles = uni(s.row_tiles), key_tiles = uni(s.key_tiles), splits = uni(s.splits);
+            const int hs = r.it / row_tiles, rt = r.it - hs * row_tiles, sp = hs % splits;
+            const int k0 = (int)((unsigned)key_tiles * sp / splits);
+            p.b = uni(s.tok[0]) / a.K;   // (all of the tile's sequences hold the same pages here)
+            p.h = hs / splits;
+            p.p0 = k0 * N;
+            p.tiles = (int)((unsigned)key_tiles * (sp + 1) / splits) - k0;
+            p.len = p.end = a.prefix;
+            p.r0 = rt * decltype(tag)::C::M;
+            p.tok0 = p.r0 / G;
+            p.tok1 = min((p.r0 + decltype(tag)::C::M - 1) / G + 1, uni(s.tok_total));
+            p.slot = r.it;
+        } else {
+            const Seq q = seq_at(r.b);
+            const RowTiles rts_of = row_tiles_of(a, OW::M);
+            const int rt_block = uni(s.rt_block);
+            const int extra = uni(s.extra), span = q.tiles + extra, seg = r.off / span, u0 = r.off - seg * span;
+            const int u1 = min(span, u0 + uni(s.own_u1) - r.u), k0 = max(u0 - extra, 0);
+            const int h = a.count ? seg / q.rts : seg, rt_list = a.count ? seg - h * q.rts : 0;
+            p.b = r.b;
+            p.h = h;
+            p.p0 = q.start + k0 * N;
+            p.tiles = u1 - extra - k0;
+            p.len = q.len;
+            p.end = q.end;
+            p.r0 = (rt_list + rt_block) * OW::M;
+            p.tok0 = 0;
+            p.tok1 = q.cnt;
+            p.slot = !q.part && p.tiles == q.tiles
+                         ? -1
+                         : (uni(s.own_part) + (r.b * a.Hkv + h) * rts_of.in_list + rt_list) * rts_of.grouped + rt_block;
+            r.u += u1 - u0;
+            r.off += u1 - u0;
+        }
+        return p;
+    };
+
+    // ---- the loader, which is one tile ahead of the work and goes on from a piece to the next: lane i holds the
+    // page of the slot first + i (a missing one as page 0, flagged), and that of the 64 slots after
+    const int page_mask = (1 << a.page_log2) - 1;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)sm;
+    const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_log2) * ROW;
+    auto slot_id = [&](const int32_t* row, int sl) { return sl < a.P ? row[sl] : -1; };
+    auto is_bad = [&](int id) { return (unsigned)id >= (unsigned)a.n_pages; };
+    const int32_t* ld_row = nullptr;   // its table row
+    int ld_first = 0, ld_p0 = 0, ids = 0, ids2 = 0, ids_next = 0;
+    uint32_t ld_head = 0;
+    unsigned long long bad = 0;
+    int buf = 0;             // the buffer that the next tile is loaded into
+    unsigned miss_next = 0;  // missing pages of the tile loaded last
+    auto row_at = [&](int b) { return a.table + (size_t)b * a.P; };
+    auto load_piece = [&](const Piece p, int page_ids) {
+        ld_row = row_at(p.b);
+        ld_p0 = p.p0;
+        ld_first = p.p0 >> a.page_log2;
+        ld_head = ((uint32_t)p.h << a.page_log2) * ROW;
+        ids = page_ids;
+        ids2 = slot_id(ld_row, ld_first + 64 + lane);
+        bad = __ballot(is_bad(ids));
+    };
+    // Wave w of 8 brings the keys w N/8 .. of K and V, in groups of up to 16 keys (of one page, as a page has 16 at
+    // least), a group in runs of CNT KB; the i-th KB of a group is i KPI keys on: bits of the key that no other part
+    // of it has, so they flip into the swizzle.
+    constexpr int WK = N / kWaves, GK = WK < 16 ? WK : 16, KPI = 1024 / ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
+    const int lkey = lane / OW::CH, lch = lane % OW::CH;
+    const uint32_t k_off = lkey * ROW + ((lch ^ k_swizzle<OW>((w * WK + lkey) & 15)) << 4);
+    const uint32_t v_off = lkey * ROW + ((lch ^ v_swizzle<OW>((w * WK + lkey) & 15)) << 4);
+    auto issue = [&](int j) {
+        const int pt = ld_p0 + j * N;
+        int s0 = (pt >> a.page_log2) - ld_first;
+        if (s0 >= 64) {
+            ids = ids2;
+            bad = __ballot(is_bad(ids));
+            ld_first += 64;
+            s0 -= 64;
+            ids2 = slot_id(ld_row, ld_first + 64 + lane);
+        }
+#pragma unroll
+        for (int g = 0; g < WK / GK; ++g) {
+            const int key = w * WK + g * GK;
+            int id = __builtin_amdgcn_readlane(ids, s0 + (key >> a.page_log2));
+            id = is_bad(id) ? 0 : id;
+            const uint64_t off = (uint64_t)(uint32_t)id * page_bytes + (ld_head + ((pt + key) & page_mask) * ROW);
+            const uint32_t to = lds0 + buf * OW::STAGE + key * ROW;
+#pragma unroll
+            for (int i = 0; i < NI; i += CNT) {
+                uint32_t ko[CNT], vo[CNT];
+#pragma unroll
+                for (int e = 0; e < CNT; ++e) {
+                    ko[e] = k_off ^ (k_swizzle<OW>((i + e) * KPI) << 4);
+                    vo[e] = v_off ^ (v_swizzle<OW>((i + e) * KPI) << 4);
+                }
+                load_lds<CNT>(to + i * 1024, ko, static_cast<const char*>(a.k_pages) + off + i * 1024);
+                load_lds<CNT>(to + OW::MAT + i * 1024, vo, static_cast<const char*>(a.v_pages) + off + i * 1024);
+            }
+        }
+        const int slots = max(N >> a.page_log2, 1);
+        miss_next = (unsigned)(bad >> s0) & ((1u << slots) - 1);
+        buf ^= 1;
+    };
+
+    // ---- the rows of a piece
+    // Row `row` of the tile: its token b * K + t, t, and the query head of its group.  Formed anew wherever it is
+    // asked for: kept, it would take registers through the loop.
+    auto row_of = [&](auto tag, const Piece p, int rw, int& tok, int& t, int& g) {
+        const AttnArgs& a = args_again();
+        const int G = a.Hq / a.Hkv;
+        int row = rw * 16 + (threadIdx.x & 15);
+        asm volatile("" : "+v"(row));
+        const int x = p.r0 - p.tok0 * G + row;   // below 2^17, so the quotient by floats is exact (half an x added)
+        const int tx = (int)(((float)x + 0.5f) * __builtin_amdgcn_rcpf((float)G)), ti = p.tok0 + tx;
+        const bool live = ti < p.tok1;
+        g = live ? x - tx * G : 0;
+        tok = !live ? 0 : tag.shared ? s.tok[ti - p.tok0] : p.b * a.K + ti;
+        t = !live ? 0 : tag.shared ? 0 : ti;
+        return live;
+    };
+    // scores enter the exponentials with a factor above 0: the sign of `scale` goes into q, and for a scale of 0 all of q
+    const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+    uint4 q[QC];
+    bool alive = false;      // a wave without rows only loads
+    auto load_q = [&](auto tag, const Piece p) {
+        const AttnArgs& a = args_again();
+        int tok, t, g;
+        const bool live = row_of(tag, p, w % decltype(tag)::C::RW, tok, t, g);
+        alive = __any(live);
+        const char* qp = static_cast<const char*>(a.q) +
+                         ((size_t)tok * a.q_stride + (size_t)(p.h * (a.Hq / a.Hkv) + g) * OW::D) * OW::ES + grp * 16;
+#pragma unroll
+        for (int e = 0; e < QC; ++e) {
+            q[e] = make_uint4(0, 0, 0, 0);
+            if (live) q[e] = *reinterpret_cast<const uint4*>(qp + e * 64);
+        }
+    };
+    const uint32_t flip = a.scale < 0.f ? (OW::BF16 ? 0x80008000u : 0x80000000u) : 0u;
+    const uint32_t keep = a.scale == 0.f ? 0u : ~0u;
+
+    int serial = 0;          // the pieces' numbers
+    const bool has_parent = a.parent != nullptr;
+    int parent_next = -1;    // (first wave) lane i: the parent of node i in the next piece's window
+    auto load_parent = [&](const Piece p) {   // (of own pieces)
+        if (w == 0 && p.p0 + p.tiles * N > p.len) {
+            const AttnArgs& a = args_again();
+            parent_next = -1;
+            if (a.parent && lane < a.K) parent_next = a.parent[(size_t)p.b * a.K + lane];
+        }
+    };
+
+    // Works on the piece at `now`, whose first tile and q are on their way; where `more`, brings the same of the own
+    // piece at `next` while it works.
+    auto run = [&](auto tag, const Piece p, const bool more, const Piece n) {
+        using C = typename decltype(tag)::C;
+        constexpr bool window = !tag.shared;
+        constexpr int KF = C::KF, DB = C::DB;
+        const int rw = w % C::RW, kw = (w / C::RW) % C::KW, dw = w / (C::RW * C::KW);
+        ++serial;
+        if (w == 0) s.path[serial & 1][lane] = has_parent ? ancestors(parent_next) : ~0ull >> (63 - lane);
+        if (more) {
+            ids_next = slot_id(row_at(n.b), (n.p0 >> a.page_log2) + lane);
+            load_parent(n);
+        }
+        const int p0 = p.p0, tiles = p.tiles, len = p.len, end = p.end;
+        float m = kNoMax, l = 0.f;
+        f32x4_t o[DB];
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < QC; ++e)
+            q[e] = make_uint4((q[e].x ^ flip) & keep, (q[e].y ^ flip) & keep, (q[e].z ^ flip) & keep, (q[e].w ^ flip) & keep);
+
+        // LDS addresses of this lane within a tile: chunk c of a row sits at its lane's chunk with the low bits of c
+        // flipped in, and further chunks, keys and 16-key groups lie at constant distances
+        const int kbase = kw * (N / C::KW);
+        const int vkey = C::BF16 ? 4 * grp + (n16 >> 2) : 4 * grp;   // (fp32 adds the register's index)
+        const uint32_t k_lane = lds0 + (kbase + n16) * ROW + ((grp ^ k_swizzle<C>(n16)) << 4);
+        const uint32_t v_lane =
+            lds0 + C::MAT + (kbase + vkey) * ROW + (dw * DB * 16 * C::ES & ~255) +
+            (C::BF16 ? ((((n16 >> 1) & 1) ^ v_swizzle<C>(vkey) ^ (2 * dw * DB & 15)) << 4) + (n16 & 1) * 8
+                     : (((n16 >> 2) ^ v_swizzle<C>(vkey)) << 4) + (n16 & 3) * 4);
+        static_assert((DB & (DB - 1)) == 0 && (C::BF16 || DB % 4 == 0), "a part's columns do not straddle swizzle groups");
+
+        for (int j = 0; j < tiles; ++j) {
+            const unsigned miss = miss_next;
+            load_wait();
+            block_barrier();   // every wave's part of this tile is there, and nobody reads the other buffer any more
+            const int here = buf ^ 1;
+            if (j + 1 < tiles) {
+                issue(j + 1);
+            } else if (more) {
+                load_piece(n, ids_next);
+                issue(0);
+            }
+            char* vt = sm + here * C::STAGE + C::MAT;
+            const int pt = p0 + j * N;
+            const bool masked = miss != 0 || (window && pt + N > len) || pt + N > end;
+
+            // Values nobody may see are cleared where they lie (0 times NaN is NaN), and so are the window's that are
+            // not finite: only some rows see them, and get them at the end.
+            if (masked) {
+                int e0 = threadIdx.x;
+                asm volatile("" : "+v"(e0));
+                for (int e = e0; e < N * C::CH; e += kThreads) {
+                    const int key = e / C::CH, pos = pt + key;
+                    uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
+                    if (pos >= end || (miss >> (key >> a.page_log2) & 1)) {
+                        *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
+                    } else if (window && pos >= len) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t u = v[i];
+                            uint32_t keep = u;
+                            if ((u & 0x7f800000u) == 0x7f800000u) keep &= C::BF16 ? 0xffffu : 0u;
+                            if (C::BF16 && (u & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                            if (keep != u) {
+                                v[i] = keep;
+                                s.bad_value = serial;
+                            }
+                        }
+                    }
+                }
+                block_barrier();
+            }
+            if (!alive) continue;
+
+            // opaque, so that the addresses are formed from them in the loop and not kept in dozens of registers
+            uint32_t k_at = k_lane + here * C::STAGE, v_at = v_lane + here * C::STAGE;
+            asm volatile("" : "+v"(k_at), "+v"(v_at));
+
+            // ---- S^T = K Q^T, the reads of a 16-byte column of K (for all keys) ahead of the products with the one
+            // before: left to itself the compiler waits for each read right after it
+            f32x4_t x[KF];
+#pragma unroll
+            for (int k = 0; k < KF; ++k) x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            uint4 kf[2][KF];
+            auto read_k = [&](int e) {
+#pragma unroll
+                for (int k = 0; k < KF; ++k)
+                    kf[e & 1][k] = lds_read16((k_at ^ (uint32_t)(((4 * e) & (C::CH - 1) & 15) << 4)) +
+                                              (4 * e / 16) * 256 + 16 * k * ROW);
+            };
+            read_k(0);
+#pragma unroll
+            for (int e = 0; e < QC; ++e) {
+                if (e + 1 < QC) read_k(e + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < KF; ++k) {
+                    const uint4 u = kf[e & 1][k];
+                    if constexpr (C::BF16) {
+                        x[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u),
+                                                                       __builtin_bit_cast(bf16x8_t, q[e]), x[k], 0, 0, 0);
+                    } else {
+                        const uint32_t ua[4] = {u.x, u.y, u.z, u.w};
+                        const uint32_t qa[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ua[i]), __uint_as_float(qa[i]),
+                                                                        x[k], 0, 0, 0);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+
+            // ---- weights e^{x-m}
+            if (masked) {
+                int key0 = kbase + 4 * grp;
+                asm volatile("" : "+v"(key0));   // (what follows is formed here, not kept through the loop)
+                int tok, t, g;
+                row_of(tag, p, rw, tok, t, g);
+                const unsigned long long sees = window ? s.path[serial & 1][t & 63] : 0;
+#pragma unroll
+                for (int k = 0; k < KF; ++k) {
+                    const int key = key0 + 16 * k;
+                    // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
+                    // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
+                    const int rel = pt + key - len, left = end - (pt + key);
+                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees >> (max(rel, 0) & 63));
+                    const int old = min(max(-rel, 0), 4);
+                    unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
+                    bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[k][i] = (bits >> i & 1) ? x[k][i] : -INFINITY;
+                }
+            }
+            float top = x[0][0];
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[k][i]);
+            if (__any(top * c > m + kSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                // a row moves its reference by its own keys alone, so its bits depend on no other row
+                const float mn = top * c > m + kSlack ? top * c : m, f = exp2_(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= f;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < KF; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[k][i] = exp2_(__builtin_fmaf(x[k][i], c, -m));   // (0 where it is -infinity: c > 0)
+                    sum += x[k][i];
+                }
+            l += sum;
+
+            // ---- O^T += V^T P^T
+            if constexpr (C::BF16) {
+                // the weights enter the product in bf16, as v is: half a step of 2^-8 each, unbiased
+                auto v_frag = [&](int k, int d) {
+                    lds_char* at = (lds_char*)(uintptr_t)((v_at ^ (uint32_t)((d & (C::CH / 2 - 1) & 7) << 5)) +
+                                                          (d / 8) * 256 + 16 * k * ROW);
+                    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at));
+                };
+                // groups of GV columns' reads, ahead of the products as above
+                constexpr int KP = KF == 1 ? 1 : KF / 2, GV = DB < 4 ? DB : 4, NG = KP * DB / GV;
+                uint2 vf[2][GV][2];
+                auto read_v = [&](int g) {
+#pragma unroll
+                    for (int i = 0; i < GV; ++i) {
+                        const int k = g * GV / DB * 2, d = g * GV % DB + i;
+                        vf[g & 1][i][0] = v_frag(k, d);
+                        if constexpr (KF > 1) vf[g & 1][i][1] = v_frag(k + 1, d);
+                    }
+                };
+                read_v(0);
+                uint4 y[KP];
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    y[k].x = pack2(x[2 * k][0], x[2 * k][1]);
+                    y[k].y = pack2(x[2 * k][2], x[2 * k][3]);
+                    if constexpr (KF > 1) {
+                        y[k].z = pack2(x[2 * k + 1][0], x[2 * k + 1][1]);
+                        y[k].w = pack2(x[2 * k + 1][2], x[2 * k + 1][3]);
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (g + 1 < NG) read_v(g + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < GV; ++i) {
+                        const int k = g * GV / DB, d = g * GV % DB + i;
+                        const uint2 v0 = vf[g & 1][i][0];
+                        if constexpr (KF == 1) {
+                            o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                                __builtin_bit_cast(bf16x4_t, v0),
+                                __builtin_bit_cast(bf16x4_t, make_uint2(y[0].x, y[0].y)), o[d], 0, 0, 0);
+                        } else {
+                            const uint2 v1 = vf[g & 1][i][1];
+                            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, make_uint4(v0.x, v0.y, v1.x, v1.y)),
+                                __builtin_bit_cast(bf16x8_t, y[k]), o[d], 0, 0, 0);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KF; ++k)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float v =
+                                lds_read4((v_at ^ (uint32_t)((d & 3) << 6)) + (d / 4) * 256 + (16 * k + i) * ROW);
+                            o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, x[k][i], o[d], 0, 0, 0);
+                        }
+            }
+        }
+
+        // ---- the next piece's q, while this one is put away
+        const bool was_alive = alive;
+        if (more) load_q(OwnTag{}, n);
+
+        // ---- the four lane groups' sums, then the waves of other keys, in a fixed order
+        l += __shfl_xor(l, 16, 64);
+        l += __shfl_xor(l, 32, 64);
+        int tok, t, g;
+        const bool live = row_of(tag, p, rw, tok, t, g);
+        const AttnArgs& a = args_again();
+        const int G = a.Hq / a.Hkv;
+        if (uni(s.bad_value) == serial && was_alive) {
+            // a window value that is not finite makes what it makes of the rows that see it
+            const unsigned long long sees = s.path[serial & 1][t & 63];
+            for (int pos = max(p.p0, p.len); pos < min(p.end, p.p0 + p.tiles * N); ++pos) {
+                if (((pos - p.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
+                const int page = slot_id(row_at(p.b), pos >> a.page_log2);
+                if (is_bad(page)) continue;
+                const size_t at = ((((size_t)page * a.Hkv + p.h) << a.page_log2) + (pos & page_mask)) * C::D;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const float4 y = load4<C::BF16>(a.v_pages, at + (dw * DB + d) * 16 + 4 * grp);
+                    const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((sees >> (pos - p.len) & 1) && !(fabsf(ya[i]) < INFINITY)) o[d][i] += ya[i];
+                }
+            }
+        }
+        if constexpr (C::KW > 1) {
+            // in the buffer of the last tile (the other one is being filled)
+            float* box = reinterpret_cast<float*>(sm + (more ? buf : buf ^ 1) * C::STAGE);
+            auto at = [&](int k, int f) {
+                return reinterpret_cast<f32x4_t*>(box + ((((k - 1) * C::DW + dw) * C::RW + rw) * DB + f) * 256 + lane * 4);
+            };
+            block_barrier();   // the tile is done with
+            if (kw > 0) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d) *at(kw, d) = o[d];
+                if (grp == 0) s.ml[w][n16] = make_float2(m, l);
+            }
+            block_barrier();
+            if (kw == 0) {
+#pragma nounroll
+                for (int k = 1; k < C::KW; ++k) {
+                    const float2 v = s.ml[w + k * C::RW][n16];
+                    const float mn = fmaxf(m, v.x), f = exp2_(m - mn), f2 = exp2_(v.x - mn);
+                    m = mn;
+                    l = l * f + v.y * f2;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[d] = o[d] * f + *at(k, d) * f2;
+                }
+            }
+        }
+        if (!live || kw > 0) return;
+        if (p.slot < 0) {
+            const size_t at = (size_t)tok * a.Hq + p.h * G + g;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const f32x4_t y = o[d] * inv;
+                const size_t e = at * C::D + (dw * DB + d) * 16 + 4 * grp;
+                if constexpr (C::BF16) {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
+                        make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+                } else {
+                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.o) + e) = y;
+                }
+            }
+            if (a.lse && dw == 0 && grp == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        } else {
+            const size_t row = (size_t)p.slot * C::M + rw * 16 + n16;
+            float* po = reinterpret_cast<float*>(const_cast<char*>(s.base[window])) + row * C::D;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(po + (dw * DB + d) * 16 + 4 * grp) = o[d];
+            if (dw == 0 && grp == 0)
+                reinterpret_cast<float2*>(const_cast<char*>(s.base[2 + window]))[row] = make_float2(m, l);
+        }
+    };
+
+    // the first tile and q of a piece that no other one brought
+    auto start = [&](auto tag, const Piece p) {
+        load_piece(p, slot_id(row_at(p.b), (p.p0 >> a.page_log2) + lane));
+        issue(0);
+        if constexpr (!tag.shared) load_parent(p);
+        load_q(tag, p);
+    };
+
+    Ref at{uni(s.found_b), uni(s.found_off), own_u, 0};
+    // the next own piece that has a tile; false: there is none
+    auto next_own = [&](Piece& p) {
+        while (at.u < uni(s.own_u1)) {
+            const Seq q = seq_at(at.b);
+            if (at.off >= q.segs * (q.tiles + uni(s.extra))) {
+                at.off = 0;
+                ++at.b;
+                continue;
+            }
+            p = piece_of(OwnTag{}, at);
+            if (p.tiles > 0) return true;
+        }
+        return false;
+    };
+    Piece own_piece{};
+    bool more = next_own(own_piece), started = false;
     if constexpr (kShared) {
         for (int it = lb; it < items; it += blocks) {
-            const int hs = it / row_tiles, rt = it - hs * row_tiles, h = hs / splits, sp = hs - h * splits;
-            const int k0 = (int)((unsigned)key_tiles * sp / splits), k1 = (int)((unsigned)key_tiles * (sp + 1) / splits);
             // the tile's tokens
-            const int r0 = rt * SH::M, t0 = r0 / G;
+            const int r0 = it % row_tiles * SH::M, t0 = r0 / G;
             const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
-            __syncthreads();
+            __syncthreads();   // nobody reads the tokens of the item before, nor its last tile
             int tok = s.tok_base[threadIdx.x];
             const int f0 = min((int)threadIdx.x * per, a.B), f1 = min(f0 + per, a.B);
             for (int b = f0; b < f1 && tok < t1; ++b) {
-                const Seq q = seq_of(a, b, OW::N, OW::M);
+                const Seq q = seq_of(a, b, N, OW::M);
                 if (!q.part) continue;
                 for (int t = max(0, t0 - tok); t < q.cnt && tok + t < t1; ++t) s.tok[tok + t - t0] = b * a.K + t;
                 tok += q.cnt;
             }
             __syncthreads();
-            const int lead = uni(s.tok[0] / a.K);
-            PieceIn in{a.table + (size_t)lead * a.P, nullptr, h, k0 * SH::N, k1 - k0, a.prefix, a.prefix, false};
-            const size_t slot = it;
-            PieceOut out{false, reinterpret_cast<float*>(work + wk.o_s) + slot * SH::M * SH::D,
-                         reinterpret_cast<float2*>(work + wk.ml_s) + slot * SH::M};
-            run_piece<SH>(a, sm, s, in, out, [&](int r) {
-                RowId id{0, 0, 0, false};
-                const int t = (r0 + r) / G;
-                id.live = t < t1;
-                if (id.live) {
-                    id.tok = s.tok[t - t0];
-                    id.t = id.tok % a.K;
-                    id.g = (r0 + r) - t * G;
-                }
-                return id;
-            });
+            Ref item{0, 0, 0, it};
+            const Piece now = piece_of(SharedTag{}, item);
+            start(SharedTag{}, now);
+            // (the item after needs the tokens' place for its own, so it is not brought; the own part is)
+            started = more && it + blocks >= items;
+            run(SharedTag{}, now, started, own_piece);
         }
     }
-
-    int b = own_b, off = own_off, u = own_u;
-    while (u < own_u1) {
-        const Seq q = seq_of(a, b, OW::N, OW::M);
-        const int tiles = uni(q.tiles), rts = a.count ? uni(q.rts) : 1;
-        if (off >= a.Hkv * rts * tiles) {
-            off = 0;
-            ++b;
-            continue;
-        }
-        const int seg = off / tiles, k0 = off - seg * tiles;
-        const int nt = min(tiles - k0, own_u1 - u);
-        const int h = seg / rts, rt_list = seg - h * rts, rt = rt_list + rt_block;
-        const size_t slot = ((size_t)part + ((size_t)b * a.Hkv + h) * rts_of.in_list + rt_list) * rts_of.grouped + rt_block;
-        PieceIn in{a.table + (size_t)b * a.P, a.parent ? a.parent + (size_t)b * a.K : nullptr, h,
-                   uni(q.start) + k0 * OW::N, nt, uni(q.len), uni(q.end), true};
-        PieceOut out{uni(q.part) == 0 && nt == tiles, reinterpret_cast<float*>(work + wk.o_o) + slot * OW::M * OW::D,
-                     reinterpret_cast<float2*>(work + wk.ml_o) + slot * OW::M};
-        const int r0 = rt * OW::M, cnt = uni(q.cnt);
-        run_piece<OW>(a, sm, s, in, out, [&](int r) {
-            RowId id{0, 0, 0, false};
-            const int t = (r0 + r) / G;
-            id.live = t < cnt;
-            if (id.live) {
-                id.tok = b * a.K + t;
-                id.t = t;
-                id.g = (r0 + r) - t * G;
-            }
-            return id;
-        });
-        u += nt;
-        off += nt;
+    if (more && !started) start(OwnTag{}, own_piece);
+#pragma nounroll
+    while (more) {
+        Piece n{};
+        const bool then = next_own(n);
+        run(OwnTag{}, own_piece, then, n);
+        own_piece = n;
+        more = then;
     }
 }
 
@@ -882,7 +1019,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
             const RowTiles rts_of = row_tiles_of(a, MO);
             const int r = t * G + g, rt = r / MO;
             const int rt_list = a.count ? rt : 0, rt_block = a.count ? 0 : rt;
-            const int u = plan.own_base + (h * (a.count ? q.rts : 1) + rt_list) * q.tiles;
+            const int u = plan.own_base + (h * (a.count ? q.rts : 1) + rt_list) * (q.tiles + head.own_extra) + head.own_extra;
             const int p0 = part_of(head.own_units, head.own_parts, u);
             n_o = part_of(head.own_units, head.own_parts, u + q.tiles - 1) - p0 + 1;
             const size_t slot =

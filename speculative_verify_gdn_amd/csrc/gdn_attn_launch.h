@@ -29,7 +29,7 @@ inline bool countable(const AttnArgs& a, const Pick& p, int N)
 {
     const long long G = a.Hq / a.Hkv, most = (1ll << 31) - 1;
     const long long own = (long long)a.B * a.Hkv * ((a.K * G + p.MO - 1) / p.MO);
-    const long long tiles = (((long long)a.P << a.page_log2) + N - 1) / N;
+    const long long tiles = (((long long)a.P << a.page_log2) + N - 1) / N + kStartup;
     const long long shared = p.MS ? a.Hkv * ((a.B * a.K * G + p.MS - 1) / p.MS) : 0;
     return own <= most / tiles && shared <= most / tiles;
 }
