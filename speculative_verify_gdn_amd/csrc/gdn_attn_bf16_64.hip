@@ -6,10 +6,10 @@ namespace attn {
 
 hipError_t launch_bf16_64(const AttnArgs& a, hipStream_t s)
 {
-    using M16 = Cfg<true, 64, 1, 8, 1>;
-    using M32 = Cfg<true, 64, 2, 4, 1>;
-    using M64 = Cfg<true, 64, 4, 2, 1>;
-    using M128 = Cfg<true, 64, 8, 1, 1>;
+    using M16 = Cfg<true, 64, 4, 1, 1, 4, 1>;
+    using M32 = Cfg<true, 64, 4, 2, 1, 2, 1>;
+    using M64 = Cfg<true, 64, 4, 4, 1, 1, 1>;
+    using M128 = Cfg<true, 64, 4, 4, 2, 1, 1>;
     return launch_all<true, 64, M16, M32, M64, M128>(a, s);
 }
 

@@ -6,10 +6,10 @@ namespace attn {
 
 hipError_t launch_f32_256(const AttnArgs& a, hipStream_t s)
 {
-    using M16 = Cfg<false, 256, 1, 2, 4>;
-    using M32 = Cfg<false, 256, 2, 2, 2>;
-    using M64 = Cfg<false, 256, 4, 2, 1>;
-    using M128 = Cfg<false, 256, 8, 1, 1>;
+    using M16 = Cfg<false, 256, 8, 1, 1, 2, 4>;
+    using M32 = Cfg<false, 256, 8, 2, 1, 2, 2>;
+    using M64 = Cfg<false, 256, 8, 4, 1, 2, 1>;
+    using M128 = Cfg<false, 256, 8, 8, 1, 1, 1>;
     return launch_all<false, 256, M16, M32, M64, M128>(a, s);
 }
 

@@ -24,6 +24,10 @@
 // at the same time share its L2: before the row tiles of a key range were
 // neighbours, four of five reads of a shared prefix missed it.
 //
+// Rows a wave.  In bf16 4 waves share a workgroup and 2 workgroups a CU, so a wave has 256 registers: enough for 32
+// rows (two groups of 16 that use each fragment of K and V twice) up to head size 128.  8 waves of 16 rows read twice
+// as much from LDS; with loads that nobody waited for early both came from 600 to 556 us over 128 windows of 16 tokens.
+//
 // A tile.  K and V rows go from memory straight into LDS (16 bytes a lane), one
 // tile ahead of the one being worked on.  S^T = K Q^T leaves a query row in the
 // lanes with the same lane & 15, 4 keys a register group; e^{x-m} of that layout
@@ -43,25 +47,25 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr float kNoMax = -1e37f;   // the reference of a row that has seen no key: finite, so differences are
+constexpr int kThreads = 512, kWaves = kThreads / 64;   // of a workgroup at most
+constexpr float kNoMax = -3.4028234e38f;   // the reference of a row that has seen no key: finite, so that -inf - kNoMax is
 constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// M rows by N keys over the 8 waves: RW groups of 16 rows x KW groups of keys x DW parts of the output's columns
-template <bool BF16_, int D_, int RW_, int KW_, int DW_>
+// M rows by N keys over W waves: RW groups of RG x 16 rows x KW groups of keys x DW parts of the output's columns
+template <bool BF16_, int D_, int W_, int RW_, int RG_, int KW_, int DW_>
 struct Cfg {
     static constexpr bool BF16 = BF16_;
-    static constexpr int D = D_, RW = RW_, KW = KW_, DW = DW_;
-    static_assert(RW * KW * DW == kWaves, "every wave has a part");
-    static constexpr int M = 16 * RW;
+    static constexpr int D = D_, WAVES = W_, THREADS = 64 * W_, RW = RW_, RG = RG_, KW = KW_, DW = DW_;
+    static_assert(RW * KW * DW == WAVES && WAVES <= kWaves, "every wave has a part");
+    static constexpr int M = 16 * RW * RG;
     static constexpr int ES = BF16 ? 2 : 4, ROW = D * ES, CH = ROW / 16;
     static constexpr int N = 8192 / D;             // keys a tile: K and V are 32 KB in bf16, 64 KB in fp32
     static constexpr int KF = N / KW / 16;         // 16-key groups of a wave
     static constexpr int DB = D / 16 / DW;         // 16-column groups of a wave's output
     static constexpr int MAT = N * ROW, STAGE = 2 * MAT;
     static constexpr int QC = BF16 ? D / 32 : D / 16;  // 16-byte pieces a lane holds of a row's q
-    static_assert((KW - 1) * DW * RW * DB * 1024 <= STAGE, "what the waves of other keys leave fits one buffer");
+    static_assert((KW - 1) * DW * RW * RG * DB * 1024 <= STAGE, "what the waves of other keys leave fits one buffer");
 };
 
 // where each 16-byte chunk of a key's row sits: chunk ^ swizzle(key)
@@ -218,7 +222,12 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, con
 
 __device__ __forceinline__ void load_wait()
 {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // by the builtin, which the compiler's own count of outstanding loads sees (vmcnt 0, the other counters free): after
+    // a wait in assembly it waited again for the page ids, behind the next tile's loads, which held every tile up for
+    // the time of its successor's loads
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ void block_barrier()
@@ -283,7 +292,7 @@ struct Small {
     int len[kThreads], count[kThreads]; // lengths and windows of the first sequences (all of them, mostly)
     unsigned long long path[2][64];     // the window's nodes on the path to each node, by the piece's number
     int tok[132];                       // window tokens (b * K + t) of a shared row tile
-    float2 ml[kWaves][16];              // (m, l) of the waves' rows, to be joined
+    float2 ml[kWaves][32];              // (m, l) of the waves' rows, to be joined
 };
 
 // where a piece starts: own: sequence b, `off` units into it, unit u of the list; shared: item it
@@ -322,6 +331,7 @@ __device__ __forceinline__ int wave_scan(int v)
 }
 
 // exclusive sum over the workgroup's threads, and the total
+template <int WAVES>
 __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -331,7 +341,7 @@ __device__ __forceinline__ int scan_int(int v, Small& s, int& total)
     __syncthreads();
     int base = 0;
     total = 0;
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
         base += i < w ? s.part[i] : 0;
         total += s.part[i];
     }
@@ -345,27 +355,38 @@ struct ListTag {
     static constexpr bool shared = SHARED;
 };
 
+template <class C>
+__device__ __forceinline__ constexpr int rows_of()
+{
+    if constexpr (__is_same(C, void)) return 0;
+    else return C::RG;
+}
+
 // SH: the shared list's configuration, or void
 template <class OW, class SH>
-__global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnArgs a, int nb)
+__global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb)
 {
     // all of LDS is asked for at the launch and starts at 0: the swizzled addresses flip bits below 256
     extern __shared__ __attribute__((aligned(1024))) char sm[];
     Small& s = *reinterpret_cast<Small*>(sm + 2 * OW::STAGE);
     constexpr bool kShared = !__is_same(SH, void);
-    constexpr int N = OW::N, QC = OW::QC, ROW = OW::ROW;
+    constexpr int N = OW::N, QC = OW::QC, ROW = OW::ROW, THREADS = OW::THREADS, WAVES = OW::WAVES;
     using OwnTag = ListTag<OW, false>;
     using SharedTag = ListTag<SH, true>;
     const int lane = threadIdx.x & 63, w = uni(threadIdx.x >> 6);
     const int n16 = lane & 15, grp = lane >> 4;
     const int G = a.Hq / a.Hkv;
+    constexpr int RGS = rows_of<SH>(), RGM = OW::RG > RGS ? OW::RG : RGS;
     int MS = 0;
-    if constexpr (kShared) MS = SH::M;
+    if constexpr (kShared) {
+        static_assert(SH::THREADS == THREADS);
+        MS = SH::M;
+    }
     const Layout wk = layout(a, nb, MS, OW::M);
     char* work = static_cast<char*>(a.work);
 
     // ---- the lists' lengths: thread i sums the sequences [b0, b1)
-    const int per = (a.B + kThreads - 1) / kThreads;
+    const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
     int my_tiles = 0, my_segs = 0, toks = 0;
     for (int b = b0; b < b1; ++b) {
@@ -381,11 +402,11 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     }
     if (threadIdx.x == 0) s.bad_value = 0;
     int own_tiles, own_segs;
-    const int tiles_base = scan_int(my_tiles, s, own_tiles), segs_base = scan_int(my_segs, s, own_segs);
+    const int tiles_base = scan_int<WAVES>(my_tiles, s, own_tiles), segs_base = scan_int<WAVES>(my_segs, s, own_segs);
     int tok_total = 0, tok_base = 0;
     int items = 0, row_tiles = 0, key_tiles = 0, splits = 0;
     if constexpr (kShared) {
-        tok_base = scan_int(toks, s, tok_total);
+        tok_base = scan_int<WAVES>(toks, s, tok_total);
         s.tok_base[threadIdx.x] = tok_base;
         tok_total = uni(tok_total);
         row_tiles = (tok_total * G + SH::M - 1) / SH::M;
@@ -513,25 +534,32 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     auto slot_id = [&](const int32_t* row, int sl) { return sl < a.P ? row[sl] : -1; };
     auto is_bad = [&](int id) { return (unsigned)id >= (unsigned)a.n_pages; };
     const int32_t* ld_row = nullptr;   // its table row
-    int ld_first = 0, ld_p0 = 0, ids = 0, ids2 = 0, ids_next = 0;
+    int ld_first = 0, ld_p0 = 0, ids = 0, ids2 = 0, ids_next = 0, ids2_next = 0;
     uint32_t ld_head = 0;
     unsigned long long bad = 0;
     int buf = 0;             // the buffer that the next tile is loaded into
     unsigned miss_next = 0;  // missing pages of the tile loaded last
     auto row_at = [&](int b) { return a.table + (size_t)b * a.P; };
-    auto load_piece = [&](const Piece p, int page_ids) {
+    auto load_ids = [&](const Piece p) {
+        const int32_t* row = row_at(p.b);
+        const int first = (p.p0 >> a.page_log2) + lane;
+        ids_next = slot_id(row, first);
+        ids2_next = slot_id(row, first + 64);
+    };
+    // (loads nothing: a load here, into registers that the loop goes on using, would be waited for behind every tile's)
+    auto load_piece = [&](const Piece p) {
         ld_row = row_at(p.b);
         ld_p0 = p.p0;
         ld_first = p.p0 >> a.page_log2;
         ld_head = ((uint32_t)p.h << a.page_log2) * ROW;
-        ids = page_ids;
-        ids2 = slot_id(ld_row, ld_first + 64 + lane);
+        ids = ids_next;
+        ids2 = ids2_next;
         bad = __ballot(is_bad(ids));
     };
-    // Wave w of 8 brings the keys w N/8 .. of K and V, in groups of up to 16 keys (of one page, as a page has 16 at
+    // Wave w of W brings the keys w N/W .. of K and V, in groups of up to 16 keys (of one page, as a page has 16 at
     // least), a group in runs of CNT KB; the i-th KB of a group is i KPI keys on: bits of the key that no other part
     // of it has, so they flip into the swizzle.
-    constexpr int WK = N / kWaves, GK = WK < 16 ? WK : 16, KPI = 1024 / ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
+    constexpr int WK = N / WAVES, GK = WK < 16 ? WK : 16, KPI = 1024 / ROW, NI = GK / KPI, CNT = NI < 4 ? NI : 4;
     const int lkey = lane / OW::CH, lch = lane % OW::CH;
     const uint32_t k_off = lkey * ROW + ((lch ^ k_swizzle<OW>((w * WK + lkey) & 15)) << 4);
     const uint32_t v_off = lkey * ROW + ((lch ^ v_swizzle<OW>((w * WK + lkey) & 15)) << 4);
@@ -587,19 +615,24 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     };
     // scores enter the exponentials with a factor above 0: the sign of `scale` goes into q, and for a scale of 0 all of q
     const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-    uint4 q[QC];
+    uint4 q[RGM][QC];
     bool alive = false;      // a wave without rows only loads
     auto load_q = [&](auto tag, const Piece p) {
         const AttnArgs& a = args_again();
-        int tok, t, g;
-        const bool live = row_of(tag, p, w % decltype(tag)::C::RW, tok, t, g);
-        alive = __any(live);
-        const char* qp = static_cast<const char*>(a.q) +
-                         ((size_t)tok * a.q_stride + (size_t)(p.h * (a.Hq / a.Hkv) + g) * OW::D) * OW::ES + grp * 16;
+        using C = typename decltype(tag)::C;
+        alive = false;
 #pragma unroll
-        for (int e = 0; e < QC; ++e) {
-            q[e] = make_uint4(0, 0, 0, 0);
-            if (live) q[e] = *reinterpret_cast<const uint4*>(qp + e * 64);
+        for (int r = 0; r < C::RG; ++r) {
+            int tok, t, g;
+            const bool live = row_of(tag, p, w % C::RW * C::RG + r, tok, t, g);
+            alive |= __any(live);
+            const char* qp = static_cast<const char*>(a.q) +
+                             ((size_t)tok * a.q_stride + (size_t)(p.h * (a.Hq / a.Hkv) + g) * OW::D) * OW::ES + grp * 16;
+#pragma unroll
+            for (int e = 0; e < QC; ++e) {
+                q[r][e] = make_uint4(0, 0, 0, 0);
+                if (live) q[r][e] = *reinterpret_cast<const uint4*>(qp + e * 64);
+            }
         }
     };
     const uint32_t flip = a.scale < 0.f ? (OW::BF16 ? 0x80008000u : 0x80000000u) : 0u;
@@ -621,22 +654,29 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
     auto run = [&](auto tag, const Piece p, const bool more, const Piece n) {
         using C = typename decltype(tag)::C;
         constexpr bool window = !tag.shared;
-        constexpr int KF = C::KF, DB = C::DB;
+        constexpr int KF = C::KF, DB = C::DB, RG = C::RG;
         const int rw = w % C::RW, kw = (w / C::RW) % C::KW, dw = w / (C::RW * C::KW);
         ++serial;
         if (w == 0) s.path[serial & 1][lane] = has_parent ? ancestors(parent_next) : ~0ull >> (63 - lane);
         if (more) {
-            ids_next = slot_id(row_at(n.b), (n.p0 >> a.page_log2) + lane);
+            load_ids(n);
             load_parent(n);
         }
         const int p0 = p.p0, tiles = p.tiles, len = p.len, end = p.end;
-        float m = kNoMax, l = 0.f;
-        f32x4_t o[DB];
+        float m[RG], l[RG];
+        f32x4_t o[RG][DB];
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < RG; ++r) {
+            m[r] = kNoMax;
+            l[r] = 0.f;
 #pragma unroll
-        for (int e = 0; e < QC; ++e)
-            q[e] = make_uint4((q[e].x ^ flip) & keep, (q[e].y ^ flip) & keep, (q[e].z ^ flip) & keep, (q[e].w ^ flip) & keep);
+            for (int d = 0; d < DB; ++d) o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < QC; ++e) {
+                const uint4 u = q[r][e];
+                q[r][e] = make_uint4((u.x ^ flip) & keep, (u.y ^ flip) & keep, (u.z ^ flip) & keep, (u.w ^ flip) & keep);
+            }
+        }
 
         // LDS addresses of this lane within a tile: chunk c of a row sits at its lane's chunk with the low bits of c
         // flipped in, and further chunks, keys and 16-key groups lie at constant distances
@@ -657,7 +697,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             if (j + 1 < tiles) {
                 issue(j + 1);
             } else if (more) {
-                load_piece(n, ids_next);
+                load_piece(n);
                 issue(0);
             }
             char* vt = sm + here * C::STAGE + C::MAT;
@@ -669,7 +709,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             if (masked) {
                 int e0 = threadIdx.x;
                 asm volatile("" : "+v"(e0));
-                for (int e = e0; e < N * C::CH; e += kThreads) {
+                for (int e = e0; e < N * C::CH; e += THREADS) {
                     const int key = e / C::CH, pos = pt + key;
                     uint32_t* v = reinterpret_cast<uint32_t*>(vt + e * 16);
                     if (pos >= end || (miss >> (key >> a.page_log2) & 1)) {
@@ -698,9 +738,11 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
 
             // ---- S^T = K Q^T, the reads of a 16-byte column of K (for all keys) ahead of the products with the one
             // before: left to itself the compiler waits for each read right after it
-            f32x4_t x[KF];
+            f32x4_t x[RG][KF];
 #pragma unroll
-            for (int k = 0; k < KF; ++k) x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < RG; ++r)
+#pragma unroll
+                for (int k = 0; k < KF; ++k) x[r][k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             uint4 kf[2][KF];
             auto read_k = [&](int e) {
 #pragma unroll
@@ -716,16 +758,20 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
 #pragma unroll
                 for (int k = 0; k < KF; ++k) {
                     const uint4 u = kf[e & 1][k];
-                    if constexpr (C::BF16) {
-                        x[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u),
-                                                                       __builtin_bit_cast(bf16x8_t, q[e]), x[k], 0, 0, 0);
-                    } else {
-                        const uint32_t ua[4] = {u.x, u.y, u.z, u.w};
-                        const uint32_t qa[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(ua[i]), __uint_as_float(qa[i]),
-                                                                        x[k], 0, 0, 0);
+                    for (int r = 0; r < RG; ++r) {
+                        if constexpr (C::BF16) {
+                            x[r][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u),
+                                                                              __builtin_bit_cast(bf16x8_t, q[r][e]),
+                                                                              x[r][k], 0, 0, 0);
+                        } else {
+                            const uint32_t ua[4] = {u.x, u.y, u.z, u.w};
+                            const uint32_t qa[4] = {q[r][e].x, q[r][e].y, q[r][e].z, q[r][e].w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[r][k] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                    __uint_as_float(ua[i]), __uint_as_float(qa[i]), x[r][k], 0, 0, 0);
+                        }
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -735,47 +781,62 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
             if (masked) {
                 int key0 = kbase + 4 * grp;
                 asm volatile("" : "+v"(key0));   // (what follows is formed here, not kept through the loop)
-                int tok, t, g;
-                row_of(tag, p, rw, tok, t, g);
-                const unsigned long long sees = window ? s.path[serial & 1][t & 63] : 0;
 #pragma unroll
-                for (int k = 0; k < KF; ++k) {
-                    const int key = key0 + 16 * k;
-                    // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
-                    // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
-                    const int rel = pt + key - len, left = end - (pt + key);
-                    const unsigned win = rel > 63 ? 0u : (unsigned)(sees >> (max(rel, 0) & 63));
-                    const int old = min(max(-rel, 0), 4);
-                    unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
-                    bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
+                for (int r = 0; r < RG; ++r) {
+                    int tok, t, g;
+                    row_of(tag, p, rw * RG + r, tok, t, g);
+                    const unsigned long long sees = window ? s.path[serial & 1][t & 63] : 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[k][i] = (bits >> i & 1) ? x[k][i] : -INFINITY;
+                    for (int k = 0; k < KF; ++k) {
+                        const int key = key0 + 16 * k;
+                        // the 4 keys from position pt + key on: committed ones (below len), then the window's by their
+                        // bits in `sees`, none from end on and none of a missing page; by shifts and selects only
+                        const int rel = pt + key - len, left = end - (pt + key);
+                        const unsigned win = rel > 63 ? 0u : (unsigned)(sees >> (max(rel, 0) & 63));
+                        const int old = min(max(-rel, 0), 4);
+                        unsigned bits = (win << old | ((1u << old) - 1)) & ((1u << min(max(left, 0), 4)) - 1);
+                        bits = (miss >> (key >> a.page_log2) & 1) ? 0u : bits;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[r][k][i] = (bits >> i & 1) ? x[r][k][i] : -INFINITY;
+                    }
                 }
             }
-            float top = x[0][0];
+            float top[RG];
+            bool move = false;
 #pragma unroll
-            for (int k = 0; k < KF; ++k)
+            for (int r = 0; r < RG; ++r) {
+                top[r] = x[r][0][0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[k][i]);
-            if (__any(top * c > m + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                // a row moves its reference by its own keys alone, so its bits depend on no other row
-                const float mn = top * c > m + kSlack ? top * c : m, f = exp2_(m - mn);
-                m = mn;
-                l *= f;
+                for (int k = 0; k < KF; ++k)
 #pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] *= f;
+                    for (int i = 0; i < 4; ++i) top[r] = fmaxf(top[r], x[r][k][i]);
+                move |= top[r] * c > m[r] + kSlack;
             }
-            float sum = 0.f;
+            if (__any(move)) {
 #pragma unroll
-            for (int k = 0; k < KF; ++k)
+                for (int r = 0; r < RG; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor(top[r], 16, 64));
+                    top[r] = fmaxf(top[r], __shfl_xor(top[r], 32, 64));
+                    // a row moves its reference by its own keys alone, so its bits depend on no other row
+                    const float mn = top[r] * c > m[r] + kSlack ? top[r] * c : m[r], f = exp2_(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[k][i] = exp2_(__builtin_fmaf(x[k][i], c, -m));   // (0 where it is -infinity: c > 0)
-                    sum += x[k][i];
+                    for (int d = 0; d < DB; ++d) o[r][d] *= f;
                 }
-            l += sum;
+            }
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < KF; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[r][k][i] = exp2_(__builtin_fmaf(x[r][k][i], c, -m[r]));   // (0 where it is -infinity: c > 0)
+                        sum += x[r][k][i];
+                    }
+                l[r] += sum;
+            }
 
             // ---- O^T += V^T P^T
             if constexpr (C::BF16) {
@@ -786,7 +847,7 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
                     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_bf16x4*)at));
                 };
                 // groups of GV columns' reads, ahead of the products as above
-                constexpr int KP = KF == 1 ? 1 : KF / 2, GV = DB < 4 ? DB : 4, NG = KP * DB / GV;
+                constexpr int KP = KF == 1 ? 1 : KF / 2, GV = DB < 4 ? DB : DB * RG > 16 ? 2 : 4, NG = KP * DB / GV;
                 uint2 vf[2][GV][2];
                 auto read_v = [&](int g) {
 #pragma unroll
@@ -797,16 +858,18 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
                     }
                 };
                 read_v(0);
-                uint4 y[KP];
+                uint4 y[RG][KP];
 #pragma unroll
-                for (int k = 0; k < KP; ++k) {
-                    y[k].x = pack2(x[2 * k][0], x[2 * k][1]);
-                    y[k].y = pack2(x[2 * k][2], x[2 * k][3]);
-                    if constexpr (KF > 1) {
-                        y[k].z = pack2(x[2 * k + 1][0], x[2 * k + 1][1]);
-                        y[k].w = pack2(x[2 * k + 1][2], x[2 * k + 1][3]);
+                for (int r = 0; r < RG; ++r)
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) {
+                        y[r][k].x = pack2(x[r][2 * k][0], x[r][2 * k][1]);
+                        y[r][k].y = pack2(x[r][2 * k][2], x[r][2 * k][3]);
+                        if constexpr (KF > 1) {
+                            y[r][k].z = pack2(x[r][2 * k + 1][0], x[r][2 * k + 1][1]);
+                            y[r][k].w = pack2(x[r][2 * k + 1][2], x[r][2 * k + 1][3]);
+                        }
                     }
-                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     if (g + 1 < NG) read_v(g + 1);
@@ -815,15 +878,18 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
                     for (int i = 0; i < GV; ++i) {
                         const int k = g * GV / DB, d = g * GV % DB + i;
                         const uint2 v0 = vf[g & 1][i][0];
-                        if constexpr (KF == 1) {
-                            o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
-                                __builtin_bit_cast(bf16x4_t, v0),
-                                __builtin_bit_cast(bf16x4_t, make_uint2(y[0].x, y[0].y)), o[d], 0, 0, 0);
-                        } else {
-                            const uint2 v1 = vf[g & 1][i][1];
-                            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8_t, make_uint4(v0.x, v0.y, v1.x, v1.y)),
-                                __builtin_bit_cast(bf16x8_t, y[k]), o[d], 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < RG; ++r) {
+                            if constexpr (KF == 1) {
+                                o[r][d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                                    __builtin_bit_cast(bf16x4_t, v0),
+                                    __builtin_bit_cast(bf16x4_t, make_uint2(y[r][0].x, y[r][0].y)), o[r][d], 0, 0, 0);
+                            } else {
+                                const uint2 v1 = vf[g & 1][i][1];
+                                o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8_t, make_uint4(v0.x, v0.y, v1.x, v1.y)),
+                                    __builtin_bit_cast(bf16x8_t, y[r][k]), o[r][d], 0, 0, 0);
+                            }
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
@@ -837,7 +903,9 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
                         for (int i = 0; i < 4; ++i) {
                             const float v =
                                 lds_read4((v_at ^ (uint32_t)((d & 3) << 6)) + (d / 4) * 256 + (16 * k + i) * ROW);
-                            o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, x[k][i], o[d], 0, 0, 0);
+#pragma unroll
+                            for (int r = 0; r < RG; ++r)
+                                o[r][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, x[r][k][i], o[r][d], 0, 0, 0);
                         }
             }
         }
@@ -847,84 +915,103 @@ __global__ __launch_bounds__(kThreads, OW::BF16 ? 4 : 2) void attn_kernel(AttnAr
         if (more) load_q(OwnTag{}, n);
 
         // ---- the four lane groups' sums, then the waves of other keys, in a fixed order
-        l += __shfl_xor(l, 16, 64);
-        l += __shfl_xor(l, 32, 64);
-        int tok, t, g;
-        const bool live = row_of(tag, p, rw, tok, t, g);
         const AttnArgs& a = args_again();
         const int G = a.Hq / a.Hkv;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+            l[r] += __shfl_xor(l[r], 16, 64);
+            l[r] += __shfl_xor(l[r], 32, 64);
+        }
         if (uni(s.bad_value) == serial && was_alive) {
             // a window value that is not finite makes what it makes of the rows that see it
-            const unsigned long long sees = s.path[serial & 1][t & 63];
-            for (int pos = max(p.p0, p.len); pos < min(p.end, p.p0 + p.tiles * N); ++pos) {
-                if (((pos - p.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
-                const int page = slot_id(row_at(p.b), pos >> a.page_log2);
-                if (is_bad(page)) continue;
-                const size_t at = ((((size_t)page * a.Hkv + p.h) << a.page_log2) + (pos & page_mask)) * C::D;
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const float4 y = load4<C::BF16>(a.v_pages, at + (dw * DB + d) * 16 + 4 * grp);
-                    const float ya[4] = {y.x, y.y, y.z, y.w};
+            for (int r = 0; r < RG; ++r) {
+                int tok, t, g;
+                row_of(tag, p, rw * RG + r, tok, t, g);
+                const unsigned long long sees = s.path[serial & 1][t & 63];
+#pragma nounroll
+                for (int pos = max(p.p0, p.len); pos < min(p.end, p.p0 + p.tiles * N); ++pos) {
+                    if (((pos - p.p0) % N) / (N / C::KW) != kw) continue;   // this wave's keys
+                    const int page = slot_id(row_at(p.b), pos >> a.page_log2);
+                    if (is_bad(page)) continue;
+                    const size_t at = ((((size_t)page * a.Hkv + p.h) << a.page_log2) + (pos & page_mask)) * C::D;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if ((sees >> (pos - p.len) & 1) && !(fabsf(ya[i]) < INFINITY)) o[d][i] += ya[i];
+                    for (int d = 0; d < DB; ++d) {
+                        const float4 y = load4<C::BF16>(a.v_pages, at + (dw * DB + d) * 16 + 4 * grp);
+                        const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((sees >> (pos - p.len) & 1) && !(fabsf(ya[i]) < INFINITY)) o[r][d][i] += ya[i];
+                    }
                 }
             }
         }
         if constexpr (C::KW > 1) {
             // in the buffer of the last tile (the other one is being filled)
             float* box = reinterpret_cast<float*>(sm + (more ? buf : buf ^ 1) * C::STAGE);
-            auto at = [&](int k, int f) {
-                return reinterpret_cast<f32x4_t*>(box + ((((k - 1) * C::DW + dw) * C::RW + rw) * DB + f) * 256 + lane * 4);
+            auto at = [&](int k, int r, int f) {
+                return reinterpret_cast<f32x4_t*>(
+                    box + (((((k - 1) * C::DW + dw) * C::RW + rw) * RG + r) * DB + f) * 256 + lane * 4);
             };
             block_barrier();   // the tile is done with
             if (kw > 0) {
 #pragma unroll
-                for (int d = 0; d < DB; ++d) *at(kw, d) = o[d];
-                if (grp == 0) s.ml[w][n16] = make_float2(m, l);
+                for (int r = 0; r < RG; ++r) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) *at(kw, r, d) = o[r][d];
+                    if (grp == 0) s.ml[w][r * 16 + n16] = make_float2(m[r], l[r]);
+                }
             }
             block_barrier();
             if (kw == 0) {
-#pragma nounroll
-                for (int k = 1; k < C::KW; ++k) {
-                    const float2 v = s.ml[w + k * C::RW][n16];
-                    const float mn = fmaxf(m, v.x), f = exp2_(m - mn), f2 = exp2_(v.x - mn);
-                    m = mn;
-                    l = l * f + v.y * f2;
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) o[d] = o[d] * f + *at(k, d) * f2;
-                }
+                for (int r = 0; r < RG; ++r)
+#pragma nounroll
+                    for (int k = 1; k < C::KW; ++k) {
+                        const float2 v = s.ml[w + k * C::RW][r * 16 + n16];
+                        const float mn = fmaxf(m[r], v.x), f = exp2_(m[r] - mn), f2 = exp2_(v.x - mn);
+                        m[r] = mn;
+                        l[r] = l[r] * f + v.y * f2;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) o[r][d] = o[r][d] * f + *at(k, r, d) * f2;
+                    }
             }
         }
-        if (!live || kw > 0) return;
-        if (p.slot < 0) {
-            const size_t at = (size_t)tok * a.Hq + p.h * G + g;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (kw > 0) return;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const f32x4_t y = o[d] * inv;
-                const size_t e = at * C::D + (dw * DB + d) * 16 + 4 * grp;
-                if constexpr (C::BF16) {
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
-                        make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-                } else {
-                    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.o) + e) = y;
+        for (int r = 0; r < RG; ++r) {
+            int tok, t, g;
+            if (!row_of(tag, p, rw * RG + r, tok, t, g)) continue;
+            if (p.slot < 0) {
+                const size_t at = (size_t)tok * a.Hq + p.h * G + g;
+                const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const f32x4_t y = o[r][d] * inv;
+                    const size_t e = at * C::D + (dw * DB + d) * 16 + 4 * grp;
+                    if constexpr (C::BF16) {
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
+                            make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+                    } else {
+                        *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.o) + e) = y;
+                    }
                 }
-            }
-            if (a.lse && dw == 0 && grp == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
-        } else {
-            const size_t row = (size_t)p.slot * C::M + rw * 16 + n16;
-            float* po = reinterpret_cast<float*>(const_cast<char*>(s.base[window])) + row * C::D;
+                if (a.lse && dw == 0 && grp == 0) a.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + __log2f(l[r])) * kLn2;
+            } else {
+                const size_t row = (size_t)p.slot * C::M + (rw * RG + r) * 16 + n16;
+                float* po = reinterpret_cast<float*>(const_cast<char*>(s.base[window])) + row * C::D;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(po + (dw * DB + d) * 16 + 4 * grp) = o[d];
-            if (dw == 0 && grp == 0)
-                reinterpret_cast<float2*>(const_cast<char*>(s.base[2 + window]))[row] = make_float2(m, l);
+                for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(po + (dw * DB + d) * 16 + 4 * grp) = o[r][d];
+                if (dw == 0 && grp == 0)
+                    reinterpret_cast<float2*>(const_cast<char*>(s.base[2 + window]))[row] = make_float2(m[r], l[r]);
+            }
         }
     };
 
     // the first tile and q of a piece that no other one brought
     auto start = [&](auto tag, const Piece p) {
-        load_piece(p, slot_id(row_at(p.b), (p.p0 >> a.page_log2) + lane));
+        load_ids(p);
+        load_piece(p);
         issue(0);
         if constexpr (!tag.shared) load_parent(p);
         load_q(tag, p);

@@ -18,7 +18,7 @@ inline Pick pick(const AttnArgs& a, bool bf16)
     Pick p;
     const int G = a.Hq / a.Hkv, R = a.K * G;
     p.blocks = bf16 ? 512 : 256;   // two workgroups fit a CU (64 KB of tiles each), one in fp32
-    const int most = bf16 && a.D == 256 ? 64 : 128;   // 128 rows of 256 columns do not fit the registers of 4 waves a SIMD
+    const int most = bf16 && a.D == 256 ? 64 : 128;
     p.MO = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : most;
     p.MS = a.prefix == 0 ? 0 : a.B * R <= 64 ? 64 : most;
     return p;
@@ -63,7 +63,7 @@ hipError_t launch_one(const AttnArgs& a, const Pick& p, hipStream_t s)
     auto* kernel = attn_kernel<OW, SH>;
     const hipError_t e = allow_lds(kernel, lds, done);
     if (e != hipSuccess) return e;
-    kernel<<<dim3(p.blocks), dim3(kThreads), lds, s>>>(a, p.blocks);
+    kernel<<<dim3(p.blocks), dim3(OW::THREADS), lds, s>>>(a, p.blocks);
     return hipGetLastError();
 }
 
