@@ -98,8 +98,8 @@ __device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int count, i
     s.end = (int)min((long long)s.len + s.cnt, (long long)cap);
     s.part = a.prefix > 0 && s.len >= a.prefix && s.cnt > 0;
     s.start = s.part ? a.prefix : 0;
-    s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) / N : 0;
-    s.rts = (s.cnt * (a.Hq / a.Hkv) + M - 1) / M;
+    s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) >> __builtin_ctz(N) : 0;   // (N and M are powers of two)
+    s.rts = (s.cnt * a.G + M - 1) >> __builtin_ctz(M);
     s.segs = s.tiles > 0 ? a.Hkv * (a.count ? s.rts : 1) : 0;
     return s;
 }
@@ -128,17 +128,14 @@ struct PlanSeq {
 };
 
 // workspace: Head | PlanSeq[B] | (m, l) of shared rows | of own rows | a of shared rows | of own rows
-struct Layout {
-    size_t plan, ml_s, ml_o, o_s, o_o, bytes;
-};
-__host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-__host__ __device__ inline Layout layout(const AttnArgs& a, int nb, int MS, int MO)
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline AttnWork layout(const AttnArgs& a, int nb, int MS, int MO)
 {
     const size_t G = a.Hq / a.Hkv;
     const size_t segs = MS ? a.Hkv * (((size_t)a.B * a.K * G + MS - 1) / MS) : 0;
     const size_t slots_s = MS ? (segs > 2 * (size_t)nb ? segs : 2 * (size_t)nb) : 0;
     const size_t slots_o = nb + (size_t)a.B * a.Hkv * ((a.K * G + MO - 1) / MO);
-    Layout w;
+    AttnWork w;
     w.plan = up256(sizeof(Head));
     w.ml_s = up256(w.plan + a.B * sizeof(PlanSeq));
     w.ml_o = up256(w.ml_s + slots_s * MS * 8);
@@ -186,13 +183,20 @@ struct RowTiles {
 };
 __host__ __device__ inline RowTiles row_tiles_of(const AttnArgs& a, int M)
 {
-    const int rt = (a.K * (a.Hq / a.Hkv) + M - 1) / M;
+    const int rt = (a.K * a.G + M - 1) >> __builtin_ctz(M);
     return a.count ? RowTiles{rt, 1} : RowTiles{1, rt};
 }
 // (a list is cut in no more parts than it has units, so that none is empty)
 __device__ __forceinline__ int parts_for(int nb, int grouped, int units) { return min(max(nb / grouped, 1), units); }
 
 // ---------------------------------------------------------------- pieces of a tile
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uni_ptr(const char* p)
+{
+    const uint64_t v = (uint64_t)p;
+    return (const char*)((uint64_t)(uint32_t)uni((int)v) | (uint64_t)(uint32_t)uni((int)(v >> 32)) << 32);
+}
+
 // COUNT KB of global memory to LDS: in the i-th, lane l's 16 bytes at base + 1024 i + voff[i] go to
 // lds + 1024 i + 16 l (the instruction's offset counts on both sides).  Written as assembly because the
 // compiler would otherwise wait for the tile on its way before it reads the tile that is there; nothing
@@ -202,6 +206,8 @@ template <int COUNT>
 __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, const char* base)
 {
     static_assert(COUNT == 2 || COUNT == 4, "2 or 4 KB");
+    lds = uni(lds);
+    base = uni_ptr(base);
     if constexpr (COUNT == 2)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %1, %3\n\t"
@@ -247,7 +253,6 @@ __device__ __forceinline__ float lds_read4(uint32_t at)
     return *(lds_f1*)(lds_char*)(uintptr_t)at;
 }
 
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -375,14 +380,13 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     using SharedTag = ListTag<SH, true>;
     const int lane = threadIdx.x & 63, w = uni(threadIdx.x >> 6);
     const int n16 = lane & 15, grp = lane >> 4;
-    const int G = a.Hq / a.Hkv;
+    const int G = a.G;
     constexpr int RGS = rows_of<SH>(), RGM = OW::RG > RGS ? OW::RG : RGS;
     int MS = 0;
     if constexpr (kShared) {
         static_assert(SH::THREADS == THREADS);
         MS = SH::M;
     }
-    const Layout wk = layout(a, nb, MS, OW::M);
     char* work = static_cast<char*>(a.work);
 
     // ---- the lists' lengths: thread i sums the sequences [b0, b1)
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) *reinterpret_cast<Head*>(work) = Head{row_tiles, splits, own, own_parts, extra};
-        PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + wk.plan);
+        PlanSeq* plan = reinterpret_cast<PlanSeq*>(work + a.at.plan);
         int base = own_base, tok = tok_base;
         for (int b = b0; b < b1; ++b) {
             const Seq q = seq_of(a, b, N, OW::M);
@@ -465,10 +469,10 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
         s.key_tiles = key_tiles;
         s.splits = splits;
         s.tok_total = tok_total;
-        s.base[0] = work + wk.o_s;
-        s.base[1] = work + wk.o_o;
-        s.base[2] = work + wk.ml_s;
-        s.base[3] = work + wk.ml_o;
+        s.base[0] = work + a.at.o_s;
+        s.base[1] = work + a.at.o_o;
+        s.base[2] = work + a.at.ml_s;
+        s.base[3] = work + a.at.ml_o;
     }
     __syncthreads();
 
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     // the piece of the own list at a place (it may have no tile) and on past it, or of an item of the shared one
     auto piece_of = [&](auto tag, Ref& r) {
         const AttnArgs& a = args_again();
-        const int G = a.Hq / a.Hkv;
+        const int G = a.G;
         Piece p;
         if constexpr (tag.shared) {
             const int row_tiles = uni(s.row_tiles), key_tiles = uni(s.key_tiles), splits = uni(s.splits);
@@ -602,7 +606,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     // asked for: kept, it would take registers through the loop.
     auto row_of = [&](auto tag, const Piece p, int rw, int& tok, int& t, int& g) {
         const AttnArgs& a = args_again();
-        const int G = a.Hq / a.Hkv;
+        const int G = a.G;
         int row = rw * 16 + (threadIdx.x & 15);
         asm volatile("" : "+v"(row));
         const int x = p.r0 - p.tok0 * G + row;   // below 2^17, so the quotient by floats is exact (half an x added)
@@ -627,7 +631,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
             const bool live = row_of(tag, p, w % C::RW * C::RG + r, tok, t, g);
             alive |= __any(live);
             const char* qp = static_cast<const char*>(a.q) +
-                             ((size_t)tok * a.q_stride + (size_t)(p.h * (a.Hq / a.Hkv) + g) * OW::D) * OW::ES + grp * 16;
+                             ((size_t)tok * a.q_stride + (size_t)(p.h * a.G + g) * OW::D) * OW::ES + grp * 16;
 #pragma unroll
             for (int e = 0; e < QC; ++e) {
                 q[r][e] = make_uint4(0, 0, 0, 0);
@@ -916,7 +920,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
 
         // ---- the four lane groups' sums, then the waves of other keys, in a fixed order
         const AttnArgs& a = args_again();
-        const int G = a.Hq / a.Hkv;
+        const int G = a.G;
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
             l[r] += __shfl_xor(l[r], 16, 64);
@@ -1034,37 +1038,54 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     };
     Piece own_piece{};
     bool more = next_own(own_piece), started = false;
-    if constexpr (kShared) {
-        for (int it = lb; it < items; it += blocks) {
-            // the tile's tokens
-            const int r0 = it % row_tiles * SH::M, t0 = r0 / G;
-            const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
-            __syncthreads();   // nobody reads the tokens of the item before, nor its last tile
-            int tok = s.tok_base[threadIdx.x];
-            const int f0 = min((int)threadIdx.x * per, a.B), f1 = min(f0 + per, a.B);
-            for (int b = f0; b < f1 && tok < t1; ++b) {
-                const Seq q = seq_of(a, b, N, OW::M);
-                if (!q.part) continue;
-                for (int t = max(0, t0 - tok); t < q.cnt && tok + t < t1; ++t) s.tok[tok + t - t0] = b * a.K + t;
-                tok += q.cnt;
+    auto shared_list = [&](const bool then_own) {
+        if constexpr (kShared) {
+            for (int it = lb; it < items; it += blocks) {
+                // the tile's tokens
+                const int r0 = it % row_tiles * SH::M, t0 = r0 / G;
+                const int t1 = min((r0 + SH::M - 1) / G + 1, tok_total);
+                __syncthreads();   // nobody reads the tokens of the item before, nor its last tile
+                int tok = s.tok_base[threadIdx.x];
+                const int f0 = min((int)threadIdx.x * per, a.B), f1 = min(f0 + per, a.B);
+                for (int b = f0; b < f1 && tok < t1; ++b) {
+                    const Seq q = seq_of(a, b, N, OW::M);
+                    if (!q.part) continue;
+                    for (int t = max(0, t0 - tok); t < q.cnt && tok + t < t1; ++t) s.tok[tok + t - t0] = b * a.K + t;
+                    tok += q.cnt;
+                }
+                __syncthreads();
+                Ref item{0, 0, 0, it};
+                const Piece now = piece_of(SharedTag{}, item);
+                start(SharedTag{}, now);
+                // (the item after needs the tokens' place for its own, so it is not brought; the own part is)
+                started = then_own && more && it + blocks >= items;
+                run(SharedTag{}, now, started, own_piece);
             }
-            __syncthreads();
-            Ref item{0, 0, 0, it};
-            const Piece now = piece_of(SharedTag{}, item);
-            start(SharedTag{}, now);
-            // (the item after needs the tokens' place for its own, so it is not brought; the own part is)
-            started = more && it + blocks >= items;
-            run(SharedTag{}, now, started, own_piece);
         }
-    }
-    if (more && !started) start(OwnTag{}, own_piece);
+    };
+    auto own_list = [&] {
+        if (more && !started) start(OwnTag{}, own_piece);
 #pragma nounroll
-    while (more) {
-        Piece n{};
-        const bool then = next_own(n);
-        run(OwnTag{}, own_piece, then, n);
-        own_piece = n;
-        more = then;
+        while (more) {
+            Piece n{};
+            const bool then = next_own(n);
+            run(OwnTag{}, own_piece, then, n);
+            own_piece = n;
+            more = then;
+        }
+    };
+    if constexpr (kShared && OW::BF16 && OW::M <= 32) {
+        // Half of the workgroups, one of a CU's two, take the lists the other way round: the shared one is bound by
+        // matrix products and vector work, the own one by memory, so that each has the other beside it.
+        const bool own_first = blockIdx.x >> 8 & 1;
+#pragma nounroll
+        for (int pass = 0; pass < 2; ++pass) {
+            if ((pass == 0) != own_first) shared_list(!own_first);
+            else own_list();
+        }
+    } else {
+        shared_list(true);
+        own_list();
     }
 }
 
@@ -1085,26 +1106,25 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
     const int c4 = (int)(unit % C4);
     int n_s = 0, n_o = 0;
     size_t at_s = 0, at_o = 0, step_s = 0, step_o = 0;   // first rows in the workspace, rows to the next piece
-    const Layout wk = layout(a, nb, MS, MO);
     const char* work = static_cast<const char*>(a.work);
     bool mine = row < (long long)a.B * a.K * a.Hq;
     if (mine) {
-        const int G = a.Hq / a.Hkv;
-        const int tok = (int)(row / a.Hq), hq = (int)(row - (long long)tok * a.Hq);
+        const int G = a.G;
+        const int tok = (int)row / a.Hq, hq = (int)row - tok * a.Hq;   // (below 2^28 rows)
         const int b = tok / a.K, t = tok - b * a.K, h = hq / G, g = hq - h * G;
         const Head head = *reinterpret_cast<const Head*>(work);
-        const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + wk.plan)[b];
+        const PlanSeq plan = reinterpret_cast<const PlanSeq*>(work + a.at.plan)[b];
         const Seq q = seq_of(a, b, N, MO);
         mine = t < q.cnt;
         if (mine && plan.tok_base >= 0) {
-            const int r = (plan.tok_base + t) * G + g, rt = r / MS;
+            const int r = (plan.tok_base + t) * G + g, rt = r >> __builtin_ctz(MS);
             n_s = head.splits;
             at_s = ((size_t)h * head.splits * head.row_tiles + rt) * MS + (r - rt * MS);
             step_s = (size_t)head.row_tiles * MS;
         }
         if (mine && q.tiles > 0) {
             const RowTiles rts_of = row_tiles_of(a, MO);
-            const int r = t * G + g, rt = r / MO;
+            const int r = t * G + g, rt = r >> __builtin_ctz(MO);
             const int rt_list = a.count ? rt : 0, rt_block = a.count ? 0 : rt;
             const int u = plan.own_base + (h * (a.count ? q.rts : 1) + rt_list) * (q.tiles + head.own_extra) + head.own_extra;
             const int p0 = part_of(head.own_units, head.own_parts, u);
@@ -1116,10 +1136,10 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
             if (n_o == 1 && !q.part) mine = false;   // written by its one piece
         }
     }
-    const float2* ml_s = reinterpret_cast<const float2*>(work + wk.ml_s) + at_s;
-    const float2* ml_o = reinterpret_cast<const float2*>(work + wk.ml_o) + at_o;
-    const f32x4_t* o_s = reinterpret_cast<const f32x4_t*>(work + wk.o_s) + at_s * C4 + c4;
-    const f32x4_t* o_o = reinterpret_cast<const f32x4_t*>(work + wk.o_o) + at_o * C4 + c4;
+    const float2* ml_s = reinterpret_cast<const float2*>(work + a.at.ml_s) + at_s;
+    const float2* ml_o = reinterpret_cast<const float2*>(work + a.at.ml_o) + at_o;
+    const f32x4_t* o_s = reinterpret_cast<const f32x4_t*>(work + a.at.o_s) + at_s * C4 + c4;
+    const f32x4_t* o_o = reinterpret_cast<const f32x4_t*>(work + a.at.o_o) + at_o * C4 + c4;
     const int n = mine ? n_s + n_o : 0;
     float M = kNoMax, L = 0.f;
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};

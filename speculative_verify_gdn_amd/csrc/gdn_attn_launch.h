@@ -78,9 +78,12 @@ hipError_t launch_with(const AttnArgs& a, const Pick& p, hipStream_t s)
 }
 
 template <bool BF16, int D, class M16, class M32, class M64, class M128>
-hipError_t launch_all(const AttnArgs& a, hipStream_t s)
+hipError_t launch_all(const AttnArgs& given, hipStream_t s)
 {
+    AttnArgs a = given;
     const Pick p = pick(a, BF16);
+    a.G = a.Hq / a.Hkv;
+    a.at = layout(a, p.blocks, p.MS, p.MO);
     hipError_t e;
     if (p.MS == 0) {
         e = launch_with<void, M16, M32, M64, M128>(a, p, s);

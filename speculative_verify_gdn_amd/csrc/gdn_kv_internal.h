@@ -63,6 +63,11 @@ struct KvCompactArgs {
     KvGeom g;
 };
 
+// where the parts of the attention's workspace start
+struct AttnWork {
+    size_t plan, ml_s, ml_o, o_s, o_o, bytes;
+};
+
 struct AttnArgs {
     const void* q;
     size_t q_stride;  // elements from one token to the next
@@ -73,6 +78,9 @@ struct AttnArgs {
     void* work;
     int B, K, Hq, Hkv, D, page_log2, n_pages, P, prefix;
     float scale;
+    // set at the launch: divisions and products that every workgroup would repeat
+    int G;  // Hq / Hkv
+    AttnWork at;
 };
 
 size_t kv_compact_words(int n_pages);
