@@ -576,6 +576,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
             ld_first += 64;
             s0 -= 64;
             ids2 = slot_id(ld_row, ld_first + 64 + lane);
+            load_wait();   // here, or it may be waited for where the ways meet again: behind every tile's loads
         }
 #pragma unroll
         for (int g = 0; g < WK / GK; ++g) {
