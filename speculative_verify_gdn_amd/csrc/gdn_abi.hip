@@ -97,6 +97,9 @@ int check_kv(const char* fn, int planes, int n_pages, int Hkv, int page, int D, 
     REQUIRE((long long)Hkv * page * D <= (1 << 28), GDN_EUNSUPPORTED, "%s: a page of %d x %d x %d passes 2^28 elements",
             fn, Hkv, page, D);
     REQUIRE(planes <= 65535, GDN_EUNSUPPORTED, "%s: planes = %d > 65535", fn, planes);
+    // (a token's 16-byte pieces in all planes are counted in 32 bits)
+    REQUIRE((long long)planes * Hkv * D * (int)elem_size(dtype) <= 1LL << 33, GDN_EUNSUPPORTED,
+            "%s: a token of %d planes x %d x %d passes 2^33 bytes", fn, planes, Hkv, D);
     g.planes = planes;
     g.n_pages = n_pages;
     g.Hkv = Hkv;
@@ -685,6 +688,8 @@ int gdn_kv_append(const void* k, const void* v, long long kv_stride, void* k_pag
     if (rc) return rc;
     REQUIRE(B >= 0 && K >= 1 && P >= 1, GDN_EINVAL, "%s: B = %d, K = %d, P = %d", fn, B, K, P);
     REQUIRE(B <= 65535 && K <= 65536, GDN_EUNSUPPORTED, "%s: B = %d or K = %d too large", fn, B, K);
+    REQUIRE((long long)K * Hkv * D * (int)elem_size(dtype) <= 1LL << 33, GDN_EUNSUPPORTED,
+            "%s: a window of %d x %d x %d passes 2^33 bytes", fn, K, Hkv, D);
     if (B == 0) return ok();
     REQUIRE(k && v && k_pages && v_pages && lens && table, GDN_EINVAL, "%s: null pointer", fn);
     const size_t es = elem_size(dtype), token = (size_t)Hkv * D;
@@ -739,6 +744,7 @@ int gdn_kv_free(const int32_t* rows, int32_t* lens, int32_t* table, int32_t* ref
     int rc = check_kv(fn, 1, n_pages, 1, 16, 64, GDN_F32, g);
     if (rc) return rc;
     REQUIRE(n >= 0 && B >= 0 && P >= 1, GDN_EINVAL, "%s: n = %d, B = %d, P = %d", fn, n, B, P);
+    REQUIRE(n <= 1 << 20, GDN_EUNSUPPORTED, "%s: n = %d > 2^20", fn, n);
     if (n == 0 || B == 0) return ok();
     REQUIRE(rows && lens && table && ref, GDN_EINVAL, "%s: null pointer", fn);
     REQUIRE(aligned4(rows) && aligned4(lens) && aligned4(table) && aligned4(ref), GDN_EINVAL,

@@ -24,14 +24,14 @@ inline Pick pick(const AttnArgs& a, bool bf16)
     return p;
 }
 
-// units of the two lists at most: they are counted in 32 bits
+// units of the two lists at most: they are counted in 32 bits, and so are the threads of the join
 inline bool countable(const AttnArgs& a, const Pick& p, int N)
 {
     const long long G = a.Hq / a.Hkv, most = (1ll << 31) - 1;
     const long long own = (long long)a.B * a.Hkv * ((a.K * G + p.MO - 1) / p.MO);
     const long long tiles = (((long long)a.P << a.page_log2) + N - 1) / N + kStartup;
     const long long shared = p.MS ? a.Hkv * ((a.B * a.K * G + p.MS - 1) / p.MS) : 0;
-    return own <= most / tiles && shared <= most / tiles;
+    return own <= most / tiles && shared <= most / tiles && (long long)a.B * a.K * a.Hq * (a.D / 4) <= 2 * most - 1024;
 }
 
 hipError_t launch_bf16_64(const AttnArgs& a, hipStream_t s);
