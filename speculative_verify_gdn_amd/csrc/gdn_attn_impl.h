@@ -48,7 +48,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;   // of a workgroup at most
-constexpr float kNoMax = -3.4028234e38f;   // the reference of a row that has seen no key: finite, so that -inf - kNoMax is
+constexpr float kNoMax = -3.4028234e38f;   // the reference of a row that has seen no key: finite, so that -inf less it is -inf
 constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -256,6 +256,16 @@ __device__ __forceinline__ float lds_read4(uint32_t at)
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A row's reference is one of its scores times the factor c, m.  Exponents are formed as fma(x, c, -m), one
+// instruction; from kFar on as (x - score) c: there the rounding of m, half a step, would grow past what a float's
+// exponent holds (2^31 and more gave infinities or no weight at all).  References are joined as m: rounding keeps
+// their order, and is off by less than the scores themselves.
+constexpr float kFar = 1048576.f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNoMax; }
+
+// scores enter the exponentials with a factor above 0: the sign of `scale` goes into q, and for a scale of 0 all of q
+__device__ __forceinline__ float factor_of(float scale) { return scale == 0.f ? 1.f : fabsf(scale) * kLog2e; }
+
 // two floats to bf16 (to nearest), packed
 __device__ __forceinline__ uint32_t pack2(float x, float y)
 {
@@ -297,6 +307,7 @@ struct Small {
     int len[kThreads], count[kThreads]; // lengths and windows of the first sequences (all of them, mostly)
     unsigned long long path[2][64];     // the window's nodes on the path to each node, by the piece's number
     int tok[132];                       // window tokens (b * K + t) of a shared row tile
+    float far[kWaves][32];              // the scores that references are of, for rows that are far
     float2 ml[kWaves][32];              // (m, l) of the waves' rows, to be joined
 };
 
@@ -618,8 +629,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
         t = !live ? 0 : tag.shared ? 0 : ti;
         return live;
     };
-    // scores enter the exponentials with a factor above 0: the sign of `scale` goes into q, and for a scale of 0 all of q
-    const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+    const float c = factor_of(a.scale);
     uint4 q[RGM][QC];
     bool alive = false;      // a wave without rows only loads
     auto load_q = [&](auto tag, const Piece p) {
@@ -669,6 +679,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
         }
         const int p0 = p.p0, tiles = p.tiles, len = p.len, end = p.end;
         float m[RG], l[RG];
+        bool far = false;   // a row of this wave is
         f32x4_t o[RG][DB];
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
@@ -816,18 +827,39 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top[r] = fmaxf(top[r], x[r][k][i]);
                 move |= top[r] * c > m[r] + kSlack;
+                if (far) move |= top[r] > s.far[w][r * 16 + n16] && is_far(m[r]);
             }
             if (__any(move)) {
+                bool now_far = false;
 #pragma unroll
                 for (int r = 0; r < RG; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], 16, 64));
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], 32, 64));
                     // a row moves its reference by its own keys alone, so its bits depend on no other row
-                    const float mn = top[r] * c > m[r] + kSlack ? top[r] * c : m[r], f = exp2_(m[r] - mn);
+                    bool up = top[r] * c > m[r] + kSlack;
+                    if (far) up |= top[r] > s.far[w][r * 16 + n16] && is_far(m[r]);
+                    const float mn = up ? top[r] * c : m[r], f = exp2_(m[r] - mn);
                     m[r] = mn;
+                    if (up) s.far[w][r * 16 + n16] = top[r];
+                    now_far |= is_far(mn);
                     l[r] *= f;
 #pragma unroll
                     for (int d = 0; d < DB; ++d) o[r][d] *= f;
+                }
+                far = __any(now_far);
+            }
+            float mc[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r) mc[r] = m[r];
+            if (far) {
+#pragma unroll
+                for (int r = 0; r < RG; ++r) {
+                    const float from = is_far(m[r]) ? s.far[w][r * 16 + n16] : 0.f;
+                    mc[r] = is_far(m[r]) ? 0.f : m[r];
+#pragma unroll
+                    for (int k = 0; k < KF; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[r][k][i] -= from;
                 }
             }
 #pragma unroll
@@ -837,7 +869,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
                 for (int k = 0; k < KF; ++k)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[r][k][i] = exp2_(__builtin_fmaf(x[r][k][i], c, -m[r]));   // (0 where it is -infinity: c > 0)
+                        x[r][k][i] = exp2_(__builtin_fmaf(x[r][k][i], c, -mc[r]));   // (0 where it is -infinity: c > 0)
                         sum += x[r][k][i];
                     }
                 l[r] += sum;
