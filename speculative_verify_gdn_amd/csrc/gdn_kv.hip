@@ -103,7 +103,77 @@ struct PageScan {
 };
 
 // ---------------------------------------------------------------- reserve
-// Thread i owns a run of consecutive sequences; their wants are numbered by an
+// slots of a sequence's window: [s0, s1); false where it asks for nothing or passes the table
+__device__ __forceinline__ bool window_of(const KvReserveArgs& a, int lens, int wants, int& s0, int& s1)
+{
+    const long long len = max(lens, 0), add = wants;
+    s0 = s1 = 0;
+    if (add <= 0 || ((len + add - 1) >> a.page_log2) >= a.P) return false;
+    s0 = (int)(len >> a.page_log2);
+    s1 = (int)((len + add - 1) >> a.page_log2) + 1;
+    return true;
+}
+
+// For up to kCtl sequences and kScan pages: a thread has one sequence and kScanPer pages, which are read once and kept,
+// and wants and free pages are numbered in one scan (two rounds of reads in all; the general kernel below, with its
+// five, took 4.9 us for one sequence).
+constexpr int kSlots = 4;   // slots of a window that are kept (more are read again)
+
+__global__ __launch_bounds__(kCtl) void kv_reserve_small_kernel(KvReserveArgs a)
+{
+    __shared__ int2 part[kCtlWaves];
+    __shared__ int ids[kScan];
+    const PageScan pages(a.ref, a.n_pages);
+    const int b = threadIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int add = 0, s0 = 0, s1 = 0, need = 0;
+    bool any = false;
+    unsigned empty = 0;
+    int32_t* row = a.table + (size_t)b * a.P;
+    if (b < a.B) {
+        const int len = a.lens[b];
+        add = a.add[b];
+        any = window_of(a, len, add, s0, s1);
+        int id[kSlots];
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) id[i] = s0 + i < s1 ? row[s0 + i] : 0;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            if (s0 + i < s1 && !held(id[i], a.n_pages)) empty |= 1u << i;
+        need = __popc(empty);
+        for (int s = s0 + kSlots; s < s1; ++s) need += !held(row[s], a.n_pages);
+        need = min(need, a.n_pages + 1);   // (more is as good, and keeps the sum in 32 bits)
+    }
+    const unsigned bits = pages.free_bits(0);
+    const int inc = wave_scan(need), inc_free = wave_scan(__popc(bits));
+    if (lane == 63) part[w] = make_int2(inc, inc_free);
+    __syncthreads();
+    int base = inc - need, r = inc_free - __popc(bits), have = 0;
+#pragma unroll
+    for (int i = 0; i < kCtlWaves; ++i) {
+        const int2 p = part[i];
+        base += i < w ? p.x : 0;
+        r += i < w ? p.y : 0;
+        have += p.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kScanPer; ++i)
+        if (bits >> i & 1) ids[r++] = (int)threadIdx.x * kScanPer + i;
+    __syncthreads();
+    if (b >= a.B) return;
+    const bool fits = any && (need == 0 || base + need <= have);
+    a.granted[b] = fits ? add : 0;
+    if (!fits || need == 0) return;
+    int next = base;
+    for (int s = s0; s < s1; ++s) {
+        const int i = s - s0;
+        if (i < kSlots ? !(empty >> i & 1) : held(row[s], a.n_pages)) continue;
+        const int id = ids[next++];
+        row[s] = id;
+        a.ref[id] = 1;
+    }
+}
+
+// Any number of them.  Thread i owns a run of consecutive sequences; their wants are numbered by an
 // exclusive sum, the free pages by another, and want r takes free page r.
 __global__ __launch_bounds__(kCtl) void kv_reserve_kernel(KvReserveArgs a)
 {
@@ -113,15 +183,7 @@ __global__ __launch_bounds__(kCtl) void kv_reserve_kernel(KvReserveArgs a)
     const int per = (a.B + kCtl - 1) / kCtl;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
 
-    // slots of sequence b's window: [s0, s1); false where it asks for nothing or passes the table
-    auto window = [&](int b, int& s0, int& s1) {
-        const long long len = max(a.lens[b], 0), add = a.add[b];
-        s0 = s1 = 0;
-        if (add <= 0 || ((len + add - 1) >> a.page_log2) >= a.P) return false;
-        s0 = (int)(len >> a.page_log2);
-        s1 = (int)((len + add - 1) >> a.page_log2) + 1;
-        return true;
-    };
+    auto window = [&](int b, int& s0, int& s1) { return window_of(a, a.lens[b], a.add[b], s0, s1); };
     auto need_of = [&](int b, int s0, int s1) {
         int n = 0;
         for (int s = s0; s < s1; ++s) n += !held(a.table[(size_t)b * a.P + s], a.n_pages);
@@ -253,20 +315,46 @@ __device__ __forceinline__ Kept kept_of(const KvRollbackArgs& a, int b)
     return k;
 }
 
+// The table row of a sequence in LDS, read when the kernel starts, beside the lengths and the tree: a read that waits
+// for another costs these kernels most (one layer of one sequence took 5.4 us with the row read after the length and
+// again after the moves).  Longer rows are read from memory where they are needed.
+constexpr int kRow = 2048;
+
+struct Row {
+    const int32_t* row;
+    int P;
+    const int32_t* staged;   // (nullptr: not staged)
+
+    __device__ __forceinline__ int at(long long slot) const
+    {
+        if (slot >= P) return -1;
+        return staged ? staged[slot] : row[slot];
+    }
+};
+
+__device__ __forceinline__ Row stage_row(const KvRollbackArgs& a, int b, int32_t* lds)
+{
+    Row r{a.table + (size_t)b * a.P, a.P, nullptr};
+    if (a.P <= kRow) {
+        for (int s = threadIdx.x; s < a.P; s += blockDim.x) lds[s] = r.row[s];
+        r.staged = lds;
+    }
+    return r;
+}
+
 // Moves the kept tokens of sequence b: this workgroup's threads take the 16-byte pieces first, first + step, .. of
 // all planes and heads.  A path's i-th node has an index >= i, so a thread that owns a piece and moves the path in
 // order never overwrites what it has yet to read; it reads a batch before it writes it.
-__device__ __forceinline__ void move_kept(const KvRollbackArgs& a, int b, const Kept& k, int first, int step)
+__device__ __forceinline__ void move_kept(const KvRollbackArgs& a, const Kept& k, const Row& row, int first, int step)
 {
     __shared__ int from_id[kKvWindowMax], to_id[kKvWindowMax], from_row[kKvWindowMax], to_row[kKvWindowMax];
     const int lane = threadIdx.x & 63, kept = __popcll(k.path);
-    const int32_t* row = a.table + (size_t)b * a.P;
     const int mask = (1 << a.g.page_log2) - 1;
+    __syncthreads();   // the row is there
     if (threadIdx.x < 64 && (k.path >> lane & 1)) {
         const int i = __popcll(k.path & ((1ull << lane) - 1));
         const long long from = k.len + lane, to = k.len + i;
-        const long long fs = from >> a.g.page_log2, ts = to >> a.g.page_log2;
-        const int f = fs < a.P ? row[fs] : -1, t = ts < a.P ? row[ts] : -1;
+        const int f = row.at(from >> a.g.page_log2), t = row.at(to >> a.g.page_log2);
         const bool move = i != lane && held(f, a.g.n_pages) && held(t, a.g.n_pages);
         from_id[i] = move ? f : -1;
         to_id[i] = t;
@@ -298,15 +386,14 @@ __device__ __forceinline__ void move_kept(const KvRollbackArgs& a, int b, const 
 }
 
 // Gives back the pages behind what sequence b keeps.
-__device__ __forceinline__ void cut_row(const KvRollbackArgs& a, int b, long long after)
+__device__ __forceinline__ void cut_row(const KvRollbackArgs& a, int b, long long after, const Row& row)
 {
-    int32_t* row = a.table + (size_t)b * a.P;
     const int mask = (1 << a.g.page_log2) - 1;
     for (long long s = ((after + mask) >> a.g.page_log2) + threadIdx.x; s < a.P; s += blockDim.x) {
-        const int id = row[s];
+        const int id = row.at(s);
         if (held(id, a.g.n_pages)) {
             atomicSub(a.ref + id, 1);
-            row[s] = -1;
+            a.table[(size_t)b * a.P + s] = -1;
         }
     }
     if (threadIdx.x == 0) a.lens_out[b] = (int32_t)after;
@@ -315,26 +402,32 @@ __device__ __forceinline__ void cut_row(const KvRollbackArgs& a, int b, long lon
 // A workgroup per sequence: every token moved, then the row cut.
 __global__ __launch_bounds__(kCtl) void kv_rollback_kernel(KvRollbackArgs a)
 {
+    __shared__ int32_t lds[kRow];
     const int b = blockIdx.x;
+    const Row row = stage_row(a, b, lds);
     const Kept k = kept_of(a, b);
-    move_kept(a, b, k, threadIdx.x, blockDim.x);
-    __syncthreads();   // (the row and lens, which lens_out may be, have been read)
-    cut_row(a, b, k.len + __popcll(k.path));
+    move_kept(a, k, row, threadIdx.x, blockDim.x);
+    __syncthreads();   // (a row that is not staged, and lens, which lens_out may be, have been read)
+    cut_row(a, b, k.len + __popcll(k.path), row);
 }
 
 // The two halves on their own, for more planes than a workgroup moves at once: many workgroups a sequence read its
 // row, so it may be cut only after the last of them.
 __global__ __launch_bounds__(256) void kv_move_kernel(KvRollbackArgs a)
 {
+    __shared__ int32_t lds[kRow];
+    const Row row = stage_row(a, blockIdx.y, lds);
     const Kept k = kept_of(a, blockIdx.y);
     // the new length, for kv_cut_kernel (unless it would overwrite what other workgroups read)
     if (a.lens_out != a.lens && blockIdx.x == 0 && threadIdx.x == 0)
         a.lens_out[blockIdx.y] = (int32_t)(k.len + __popcll(k.path));
-    move_kept(a, blockIdx.y, k, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+    move_kept(a, k, row, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 __global__ __launch_bounds__(64) void kv_cut_kernel(KvRollbackArgs a)
 {
+    __shared__ int32_t lds[kRow];
+    const Row row = stage_row(a, blockIdx.x, lds);
     long long after;
     if (a.lens_out != a.lens) {
         after = a.lens_out[blockIdx.x];
@@ -342,8 +435,8 @@ __global__ __launch_bounds__(64) void kv_cut_kernel(KvRollbackArgs a)
         const Kept k = kept_of(a, blockIdx.x);
         after = k.len + __popcll(k.path);
     }
-    __syncthreads();   // (lens has been read)
-    cut_row(a, blockIdx.x, after);
+    __syncthreads();   // (lens has been read, and the row is there)
+    cut_row(a, blockIdx.x, after, row);
 }
 
 // ---------------------------------------------------------------- free
@@ -577,7 +670,10 @@ size_t kv_compact_words(int n_pages) { return 4 + 2 * (((size_t)n_pages + 1) / 2
 
 hipError_t launch_kv_reserve(const KvReserveArgs& a, hipStream_t s)
 {
-    kv_reserve_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    if (a.B <= kCtl && a.n_pages <= kScan)
+        kv_reserve_small_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    else
+        kv_reserve_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
     return hipGetLastError();
 }
 
