@@ -297,6 +297,7 @@ __device__ __forceinline__ unsigned long long node_paths(const int32_t* parent, 
 }
 
 constexpr int kMoveBatch = 8;
+constexpr long long kForkAtOnce = 32 * 1024;   // bytes of pages that kv_fork copies in its one workgroup
 
 // what a sequence keeps of its window
 struct Kept {
@@ -506,9 +507,11 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(const int32_t* src, const 
 }
 
 // ---------------------------------------------------------------- fork
-// Which forks can be made, their new pages, and the rows.
+// Which forks can be made, their new pages, and the rows; with COPY the pages too, by this one workgroup.
+template <bool COPY>
 __global__ __launch_bounds__(kCtl) void kv_fork_kernel(KvForkArgs a)
 {
+    __shared__ int from_of[COPY ? kKvForkMax : 1];
     __shared__ int part[kCtlWaves];
     __shared__ int ids[kScan];
     __shared__ int page_of[kKvForkMax];          // -2 refused, -1 no new page, else its rank, then its id
@@ -572,6 +575,7 @@ __global__ __launch_bounds__(kCtl) void kv_fork_kernel(KvForkArgs a)
         if (id == -2) continue;
         const int src = a.src[i], dst = a.dst[i], len = length(i);
         const int full = len >> a.g.page_log2;
+        if (COPY && lane == 0) from_of[i] = id >= 0 ? a.table[(size_t)src * a.P + full] : -1;
         for (int s = lane; s < a.P; s += 64) {
             int to = -1;
             if (s < full) {
@@ -584,6 +588,29 @@ __global__ __launch_bounds__(kCtl) void kv_fork_kernel(KvForkArgs a)
             a.table[(size_t)dst * a.P + s] = to;
         }
         if (lane == 0) a.lens[dst] = len;
+    }
+    if constexpr (COPY) {
+        __syncthreads();
+        const size_t bytes = a.g.page_bytes();
+        const int pieces = (int)(bytes >> 4), all = a.n * a.g.planes * pieces;   // (at most kForkAtOnce / 16)
+        char* pool = static_cast<char*>(a.pool);
+        for (int e0 = threadIdx.x; e0 < all; e0 += kCtl * kMoveBatch) {
+            uint4 u[kMoveBatch];
+            uint4* to[kMoveBatch];
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j) {
+                const int e = e0 + j * kCtl, r = e / pieces, c = e - r * pieces, i = r / a.g.planes, pl = r - i * a.g.planes;
+                to[j] = nullptr;
+                if (e < all && page_of[i] >= 0 && held(from_of[i], a.g.n_pages)) {
+                    char* plane = pool + (size_t)pl * a.g.n_pages * bytes;
+                    to[j] = reinterpret_cast<uint4*>(plane + page_of[i] * bytes) + c;
+                    u[j] = reinterpret_cast<const uint4*>(plane + from_of[i] * bytes)[c];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j)
+                if (to[j]) *to[j] = u[j];
+        }
     }
 }
 
@@ -715,7 +742,14 @@ hipError_t launch_kv_copy(const int32_t* src, const int32_t* dst, void* pool, in
 
 hipError_t launch_kv_fork(const KvForkArgs& a, hipStream_t s)
 {
-    kv_fork_kernel<<<dim3(1), dim3(kCtl), 0, s>>>(a);
+    // A few pages are copied by the workgroup that decides, which saves a launch; more bytes than that take one CU
+    // longer than a launch of many (a free and a fork of 16 KB 9.2 us against 11.5 with a launch for the copy, 32 KB
+    // 10.4 against 12.0, 64 KB 12.5 against 12.1).
+    if ((long long)a.n * a.g.planes * (long long)a.g.page_bytes() <= kForkAtOnce) {
+        kv_fork_kernel<true><<<dim3(1), dim3(kCtl), 0, s>>>(a);
+        return hipGetLastError();
+    }
+    kv_fork_kernel<false><<<dim3(1), dim3(kCtl), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     kv_fork_copy_kernel<<<dim3(copy_grid(a.n, a.g)), dim3(256), 0, s>>>(a);
