@@ -13,8 +13,9 @@
 // holds the prefix; the splits are as many as make the items fill the grid best.
 // The own list has the units (sequence, head, key tile) in this order, with
 // kStartup empty ones before each head's tiles, and part i of n has the units
-// [i U / n, (i+1) U / n), so the load is even whatever the lengths are; a part's row tiles go to neighbouring workgroups (with windows of unequal length
-// the row tiles are units of the list instead).  No host knowledge of lengths is
+// [i U / n, (i+1) U / n), so the load is even whatever the lengths are; a part's row
+// tiles go to neighbouring workgroups (with windows of unequal length the row tiles
+// are units of the list instead).  No host knowledge of lengths is
 // needed: each workgroup sums them over the sequences by itself.  The workgroups
 // take the shared items in their order and the own parts from the last workgroup
 // down, so that short lists meet as little as may be.  A run of units of
@@ -34,6 +35,12 @@
 // is already the operand of O^T = V^T P^T, and V^T comes out of LDS by the
 // transposing 8-byte read.  The 16-byte chunks of a row are permuted by the key's
 // low bits so that both kinds of read meet every bank once.
+//
+// What bounds it.  A shared tile of 128 rows and 64 keys of 128: products 1020 cycles of a SIMD for each wave, vector
+// work (the exponentials) 1040, of 4100 that a wave takes with one other beside it.  At head size 256 a wave has 16
+// rows, a tile takes it 3170 cycles, and no unit is busy for more than a third of them (products 0.23, vector work
+// 0.31, LDS 0.25, the loads' 64 bytes a cycle 0.32): it is the chain of its steps that costs, with two waves a SIMD.
+// Own tiles of few rows stream at 6.1 TB/s.
 #pragma once
 
 #include "gdn_device.h"
@@ -827,17 +834,15 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top[r] = fmaxf(top[r], x[r][k][i]);
                 move |= top[r] * c > m[r] + kSlack;
-                if (far) move |= top[r] > s.far[w][r * 16 + n16] && is_far(m[r]);
             }
-            if (__any(move)) {
+            if (__any(move) || far) {
                 bool now_far = false;
 #pragma unroll
                 for (int r = 0; r < RG; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], 16, 64));
                     top[r] = fmaxf(top[r], __shfl_xor(top[r], 32, 64));
                     // a row moves its reference by its own keys alone, so its bits depend on no other row
-                    bool up = top[r] * c > m[r] + kSlack;
-                    if (far) up |= top[r] > s.far[w][r * 16 + n16] && is_far(m[r]);
+                    const bool up = top[r] * c > m[r] + kSlack || (is_far(m[r]) && top[r] > s.far[w][r * 16 + n16]);
                     const float mn = up ? top[r] * c : m[r], f = exp2_(m[r] - mn);
                     m[r] = mn;
                     if (up) s.far[w][r * 16 + n16] = top[r];
@@ -1109,7 +1114,8 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
     };
     if constexpr (kShared && OW::BF16 && OW::M <= 32) {
         // Half of the workgroups, one of a CU's two, take the lists the other way round: the shared one is bound by
-        // matrix products and vector work, the own one by memory, so that each has the other beside it.
+        // matrix products and vector work, the own one by memory where its tiles have few rows, so that each has the
+        // other beside it (64 single tokens behind 32768 shared keys 116 to 108 us; with 64-row own tiles it cost 2-3%).
         const bool own_first = blockIdx.x >> 8 & 1;
 #pragma nounroll
         for (int pass = 0; pass < 2; ++pass) {

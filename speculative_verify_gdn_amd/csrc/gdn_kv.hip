@@ -5,8 +5,9 @@
 // Two kinds of kernel.  Those that decide which page goes where (reserve, fork,
 // compact) are one workgroup: their answer is a running count over all pages
 // and all sequences, a few kilobytes of int32, and one workgroup needs no
-// second launch and no cross-workgroup order; what it costs is the latency of
-// about six dependent reads.  Those that move bytes (append, rollback, page
+// second launch and no cross-workgroup order; what it costs is the latency of its
+// dependent reads, about 0.7 us each (reserve 3.1 us, fork and the plan of a
+// compaction 5 us).  Those that move bytes (append, rollback, page
 // copies) spread 16-byte pieces over the chip.
 #include "gdn_device.h"
 #include "gdn_kv_internal.h"
@@ -115,8 +116,8 @@ __device__ __forceinline__ bool window_of(const KvReserveArgs& a, int lens, int 
 }
 
 // For up to kCtl sequences and kScan pages: a thread has one sequence and kScanPer pages, which are read once and kept,
-// and wants and free pages are numbered in one scan (two rounds of reads in all; the general kernel below, with its
-// five, took 4.9 us for one sequence).
+// and wants and free pages are numbered in one scan (two rounds of reads in all, 3.1 us for one sequence; the general
+// kernel below, with five, takes 4.9).
 constexpr int kSlots = 4;   // slots of a window that are kept (more are read again)
 
 __global__ __launch_bounds__(kCtl) void kv_reserve_small_kernel(KvReserveArgs a)
