@@ -456,8 +456,9 @@ int gdn_verify_tree_step(const int32_t *node_prev, int N_prev, const int32_t *pa
  *           an empty slot (written as -1)
  *   ref     [n_pages] int32: how many table entries hold the page (0: free)
  *   lens    [rows] int32: committed tokens of a sequence (below 0 taken as 0)
- * page is a power of two, 16..1024; D is 64, 128 or 256; Hkv >= 1; the
- * addressed bytes may pass 2^32.  int32 arrays need 4-byte alignment, the
+ * page is a power of two, 16..1024; D is 64, 128 or 256; 1 <= Hkv <= 1024;
+ * n_pages < 2^21 - 1; planes <= 65535, and one token's keys or values in all
+ * planes take at most 2^33 bytes; the addressed bytes may pass 2^32.  int32 arrays need 4-byte alignment, the
  * others 16.  Pages are taken lowest free id first and every result is a
  * function of the inputs alone.  A slot that is empty, or past the table, is
  * never read or written through: keys there are not seen, tokens not stored.
@@ -479,7 +480,8 @@ int gdn_kv_reserve(const int32_t *lens, const int32_t *add, int32_t *table, int3
  * t < count[b] (clamped into 0..K; NULL: K), of one layer, byte copies.
  *   k, v [B][K][Hkv][D]; token (b, t) starts kv_stride elements after the one
  *   before it (>= Hkv*D and a multiple of 16 bytes: a slice of a stacked
- *   projection row will do); lens, count [B]; table [B][P]
+ *   projection row will do); lens, count [B]; table [B][P]; K <= 65536, one
+ *   sequence's keys at most 2^33 bytes
  */
 int gdn_kv_append(const void *k, const void *v, long long kv_stride, void *k_pages, void *v_pages,
                   const int32_t *lens, const int32_t *count, const int32_t *table,
@@ -504,7 +506,7 @@ int gdn_kv_rollback_tree(const int32_t *node, const int32_t *parent, const int32
 /*
  * gdn_kv_free -- the rows given back: ref -1 for each page they hold, the
  * slots -1, lens 0.  rows [n] int32 (values outside [0, B) are passed over; a
- * row named twice is freed once); table [B][P], lens [B].
+ * row named twice is freed once); table [B][P], lens [B]; n <= 2^20.
  */
 int gdn_kv_free(const int32_t *rows, int32_t *lens, int32_t *table, int32_t *ref,
                 int n, int B, int P, int n_pages, void *stream);
@@ -575,7 +577,8 @@ int gdn_kv_copy(const int32_t *src, const int32_t *dst, void *pool, int n, int p
  *   o [B][K][Hq][D] dtype; lse [B][K][Hq] float or NULL
  *   workspace: gdn_attn_workspace bytes, 16-byte aligned, its contents not kept
  *   between calls (calls on different streams need one each)
- *   0 <= B <= 4096, 1 <= K <= 64, Hq % Hkv == 0, scale finite
+ *   0 <= B <= 4096, 1 <= K <= 64, Hq <= 1024, Hq % Hkv == 0, scale finite,
+ *   P * page <= 2^30, B * K * Hq * D below 2^34
  */
 int gdn_attn_verify(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
                     const int32_t *lens, const int32_t *count, const int32_t *parent,
