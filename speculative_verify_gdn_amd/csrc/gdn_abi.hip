@@ -889,7 +889,7 @@ int gdn_attn_verify(const void* q, long long q_stride, const void* k_pages, cons
                         ints(lens, B), ints(count, B), ints(parent, rows), ints(table, (size_t)B * P)};
     REQUIRE(!any_overlap(outs, 3, ins, 7), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
     const gdn::AttnArgs a{q, (size_t)q_stride, k_pages, v_pages, lens, count, parent, table, o, lse, workspace,
-                          B, K, Hq, Hkv, D, g.page_log2, n_pages, P, prefix_len, scale, 0, {}};
+                          B, K, Hq, Hkv, D, g.page_log2, n_pages, P, prefix_len, scale, 0, 0, {}};
     return launch_status(gdn::launch_attn(a, bf16, (hipStream_t)stream), fn);
 }
 

@@ -14,8 +14,8 @@
 // The own list has the units (sequence, head, key tile) in this order, with
 // kStartup empty ones before each head's tiles, and part i of n has the units
 // [i U / n, (i+1) U / n), so the load is even whatever the lengths are; a part's row
-// tiles go to neighbouring workgroups (with windows of unequal length the row tiles
-// are units of the list instead).  No host knowledge of lengths is
+// tiles go to neighbouring workgroups (with windows of unequal length, or more row
+// tiles than there are workgroups, the row tiles are units of the list instead).  No host knowledge of lengths is
 // needed: each workgroup sums them over the sequences by itself.  The workgroups
 // take the shared items in their order and the own parts from the last workgroup
 // down, so that short lists meet as little as may be.  A run of units of
@@ -96,7 +96,7 @@ struct Seq {
     int segs;        // runs of tiles: (head, row tile) pairs
 };
 
-__device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int count, int N, int M)
+__host__ __device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int count, int N, int M)
 {
     Seq s;
     const int cap = a.P << a.page_log2;
@@ -107,7 +107,7 @@ __device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int count, i
     s.start = s.part ? a.prefix : 0;
     s.tiles = s.cnt > 0 ? (s.end - s.start + N - 1) >> __builtin_ctz(N) : 0;   // (N and M are powers of two)
     s.rts = (s.cnt * a.G + M - 1) >> __builtin_ctz(M);
-    s.segs = s.tiles > 0 ? a.Hkv * (a.count ? s.rts : 1) : 0;
+    s.segs = s.tiles > 0 ? a.Hkv * (a.listed ? s.rts : 1) : 0;
     return s;
 }
 
@@ -156,11 +156,11 @@ inline AttnWork layout(const AttnArgs& a, int nb, int MS, int MO)
 // floor(((u + 1) n - 1) / U).  Both quotients by doubles (an integer division of 64 bits takes ten times as
 // long): their numerators are below 2^40 and exact, and half a unit added keeps the rounding of the quotient
 // (below 2^31 parts in 2^53) on the right side of every integer.
-__device__ __forceinline__ int first_unit(int units, int n, int i)
+__host__ __device__ __forceinline__ int first_unit(int units, int n, int i)
 {
     return (int)(((double)units * i + 0.5) / n);
 }
-__device__ __forceinline__ int part_of(int units, int n, int u)
+__host__ __device__ __forceinline__ int part_of(int units, int n, int u)
 {
     return (int)(((double)(u + 1) * n - 0.5) / units);
 }
@@ -183,18 +183,34 @@ __device__ __forceinline__ int splits_for(int segs, int tiles, int nb)
     return __builtin_amdgcn_readfirstlane(best);
 }
 
-// how the own list counts row tiles: with equal windows a unit stands for all RT of them, taken by RT
-// neighbouring workgroups; otherwise each is a unit of its own
+// How the own list counts row tiles: with equal windows a unit stands for all RT of them, taken by RT
+// neighbouring workgroups; otherwise each is a unit of its own.  So it is too where there are more of them than the nb
+// workgroups, of which some would then have none to take them.
 struct RowTiles {
     int in_list, grouped;
 };
+__host__ __device__ inline int own_row_tiles(const AttnArgs& a, int M) { return (a.K * a.G + M - 1) >> __builtin_ctz(M); }
+inline bool row_tiles_listed(const AttnArgs& a, int M, int nb) { return a.count || own_row_tiles(a, M) > nb; }
 __host__ __device__ inline RowTiles row_tiles_of(const AttnArgs& a, int M)
 {
-    const int rt = (a.K * a.G + M - 1) >> __builtin_ctz(M);
-    return a.count ? RowTiles{rt, 1} : RowTiles{1, rt};
+    const int rt = own_row_tiles(a, M);
+    return a.listed ? RowTiles{rt, 1} : RowTiles{1, rt};
 }
-// (a list is cut in no more parts than it has units, so that none is empty)
-__device__ __forceinline__ int parts_for(int nb, int grouped, int units) { return min(max(nb / grouped, 1), units); }
+
+// The own list of `tiles` tiles in `segs` runs: its units, the empty ones before a run's tiles, and into how many parts
+// it is cut (no more than it has units, so that none is empty), each the work of `grouped` of the nb workgroups.
+struct OwnList {
+    int units, extra, parts, blocks;
+};
+__host__ __device__ __forceinline__ OwnList own_list_of(const RowTiles& rts, int tiles, int segs, int nb)
+{
+    OwnList l;
+    l.extra = tiles <= nb / rts.grouped ? 0 : kStartup;   // (with a part for every tile there is nothing to even out)
+    l.units = tiles + l.extra * segs;
+    l.parts = min(max(nb / rts.grouped, 1), l.units);
+    l.blocks = l.parts * rts.grouped;
+    return l;
+}
 
 // ---------------------------------------------------------------- pieces of a tile
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -437,12 +453,11 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
         items = a.Hkv * row_tiles * splits;
     }
     const RowTiles rts_of = row_tiles_of(a, OW::M);
-    // (with a part for every tile there is nothing to even out)
-    const int extra = uni(own_tiles) <= nb / rts_of.grouped ? 0 : kStartup;
-    const int own = uni(own_tiles + extra * own_segs), own_base = tiles_base + extra * segs_base;
+    const OwnList list = own_list_of(rts_of, uni(own_tiles), uni(own_segs), nb);
+    const int extra = list.extra, own = list.units, own_base = tiles_base + extra * segs_base;
     const int mine = my_tiles + extra * my_segs;
-    const int own_parts = parts_for(nb, rts_of.grouped, own);
-    const int blocks = min(nb, items + own_parts * rts_of.grouped);
+    const int own_parts = list.parts;
+    const int blocks = min(nb, items + list.blocks);
     // consecutive workgroups of the lists on one XCD (workgroups are dealt to the 8 XCDs in turn)
     const int per_xcd = (blocks + 7) / 8;
     const int lb = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
@@ -461,7 +476,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
 
     // ---- the own part: its units [own_u, own_u1), the first in sequence found_b, found_off units into it
     const int own_block = blocks - 1 - lb;
-    const bool has_own = own_block < own_parts * rts_of.grouped;
+    const bool has_own = own_block < list.blocks;
     const int own_part = own_block / rts_of.grouped;
     const int own_u = uni(has_own ? first_unit(own, own_parts, own_part) : 0);
     const int own_u1 = uni(has_own ? first_unit(own, own_parts, own_part + 1) : 0);
@@ -529,7 +544,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
             const int rt_block = uni(s.rt_block);
             const int extra = uni(s.extra), span = q.tiles + extra, seg = r.off / span, u0 = r.off - seg * span;
             const int u1 = min(span, u0 + uni(s.own_u1) - r.u), k0 = max(u0 - extra, 0);
-            const int h = a.count ? seg / q.rts : seg, rt_list = a.count ? seg - h * q.rts : 0;
+            const int h = a.listed ? seg / q.rts : seg, rt_list = a.listed ? seg - h * q.rts : 0;
             p.b = r.b;
             p.h = h;
             p.p0 = q.start + k0 * N;
@@ -1164,8 +1179,8 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
         if (mine && q.tiles > 0) {
             const RowTiles rts_of = row_tiles_of(a, MO);
             const int r = t * G + g, rt = r >> __builtin_ctz(MO);
-            const int rt_list = a.count ? rt : 0, rt_block = a.count ? 0 : rt;
-            const int u = plan.own_base + (h * (a.count ? q.rts : 1) + rt_list) * (q.tiles + head.own_extra) + head.own_extra;
+            const int rt_list = a.listed ? rt : 0, rt_block = a.listed ? 0 : rt;
+            const int u = plan.own_base + (h * (a.listed ? q.rts : 1) + rt_list) * (q.tiles + head.own_extra) + head.own_extra;
             const int p0 = part_of(head.own_units, head.own_parts, u);
             n_o = part_of(head.own_units, head.own_parts, u + q.tiles - 1) - p0 + 1;
             const size_t slot =

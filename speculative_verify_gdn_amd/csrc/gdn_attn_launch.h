@@ -86,6 +86,7 @@ hipError_t launch_all(const AttnArgs& given, hipStream_t s)
     AttnArgs a = given;
     const Pick p = pick(a, BF16);
     a.G = a.Hq / a.Hkv;
+    a.listed = row_tiles_listed(a, p.MO, p.blocks);
     a.at = layout(a, p.blocks, p.MS, p.MO);
     hipError_t e;
     if (p.MS == 0) {

@@ -79,7 +79,8 @@ struct AttnArgs {
     int B, K, Hq, Hkv, D, page_log2, n_pages, P, prefix;
     float scale;
     // set at the launch: divisions and products that every workgroup would repeat
-    int G;  // Hq / Hkv
+    int G;       // Hq / Hkv
+    int listed;  // row tiles are units of the own list (attn::row_tiles_listed)
     AttnWork at;
 };
 
