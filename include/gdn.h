@@ -492,7 +492,7 @@ int gdn_kv_append(const void *k, const void *v, long long kv_stride, void *k_pag
  * of N tree nodes (the cache side of gdn_rollback_tree).  Sequence b keeps the
  * path root..node[b] (none where node[b] is outside [0, count[b])): in every
  * plane its i-th token moves from position lens[b]+path[i] to lens[b]+i (byte
- * copies), lens_out[b] <- lens[b] + |path|, and every page of a slot from
+ * copies), lens_out[b] <- lens[b] + |path| (2^31 - 1 at most), and every page of a slot from
  * ceil(lens_out[b]/page) on is given back (ref -1, slot -1).
  *   node, lens, lens_out [B]; parent [B][N] as the tree calls above, NULL for a
  *   chain (parent i-1: node = accepted tokens - 1); count [B] or NULL (N);

@@ -304,6 +304,9 @@ constexpr long long kForkAtOnce = 32 * 1024;   // bytes of pages that kv_fork co
 struct Kept {
     unsigned long long path;
     long long len;
+    // the new length: a length has 31 bits, also where the window reaches past them (wrapped, it would be a slot in
+    // front of the row)
+    __device__ __forceinline__ long long after() const { return min(len + __popcll(path), 0x7fffffffll); }
 };
 
 __device__ __forceinline__ Kept kept_of(const KvRollbackArgs& a, int b)
@@ -410,7 +413,7 @@ __global__ __launch_bounds__(kCtl) void kv_rollback_kernel(KvRollbackArgs a)
     const Kept k = kept_of(a, b);
     move_kept(a, k, row, threadIdx.x, blockDim.x);
     __syncthreads();   // (a row that is not staged, and lens, which lens_out may be, have been read)
-    cut_row(a, b, k.len + __popcll(k.path), row);
+    cut_row(a, b, k.after(), row);
 }
 
 // The two halves on their own, for more planes than a workgroup moves at once: many workgroups a sequence read its
@@ -422,7 +425,7 @@ __global__ __launch_bounds__(256) void kv_move_kernel(KvRollbackArgs a)
     const Kept k = kept_of(a, blockIdx.y);
     // the new length, for kv_cut_kernel (unless it would overwrite what other workgroups read)
     if (a.lens_out != a.lens && blockIdx.x == 0 && threadIdx.x == 0)
-        a.lens_out[blockIdx.y] = (int32_t)(k.len + __popcll(k.path));
+        a.lens_out[blockIdx.y] = (int32_t)k.after();
     move_kept(a, k, row, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
@@ -434,8 +437,7 @@ __global__ __launch_bounds__(64) void kv_cut_kernel(KvRollbackArgs a)
     if (a.lens_out != a.lens) {
         after = a.lens_out[blockIdx.x];
     } else {
-        const Kept k = kept_of(a, blockIdx.x);
-        after = k.len + __popcll(k.path);
+        after = kept_of(a, blockIdx.x).after();
     }
     __syncthreads();   // (lens has been read, and the row is there)
     cut_row(a, blockIdx.x, after, row);
