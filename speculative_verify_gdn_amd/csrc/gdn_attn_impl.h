@@ -237,7 +237,7 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, con
                      "global_load_lds_dwordx4 %2, %3 offset:1024"
                      :
                      : "s"(lds), "v"(voff[0]), "v"(voff[1]), "s"(base)
-                     : "memory");
+                     : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %1, %5\n\t"
@@ -246,7 +246,7 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint32_t* voff, con
                      "global_load_lds_dwordx4 %4, %5 offset:3072"
                      :
                      : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(base)
-                     : "memory");
+                     : "memory", "m0");
 }
 
 __device__ __forceinline__ void load_wait()
