@@ -520,8 +520,9 @@ int gdn_kv_free(const int32_t *rows, int32_t *lens, int32_t *table, int32_t *ref
  *   (gdn_kv_free it first), where row src[i] lacks a page of its tokens, or
  *   where the partial pages of the forks 0..i are more than the free ones (a
  *   fork without a partial page is always granted).
- *   src, dst, granted [n]; 0 <= n <= 4096; one call names a row as dst at most
- *   once and not as src as well
+ *   src, dst, granted [n]; 0 <= n <= 4096 (B == 0 is an empty call for n == 0
+ *   and refused above); one call names a row as dst at most once and not as src
+ *   as well
  */
 int gdn_kv_fork(const int32_t *src, const int32_t *dst, int32_t *lens, int32_t *table, int32_t *ref,
                 void *pool, int32_t *granted, int n, int B, int P, int planes, int n_pages,

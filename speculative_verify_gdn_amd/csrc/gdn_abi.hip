@@ -763,9 +763,10 @@ int gdn_kv_fork(const int32_t* src, const int32_t* dst, int32_t* lens, int32_t* 
     gdn::KvGeom g;
     int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
     if (rc) return rc;
-    REQUIRE(n >= 0 && B >= 1 && P >= 1, GDN_EINVAL, "%s: n = %d, B = %d, P = %d", fn, n, B, P);
+    REQUIRE(n >= 0 && B >= 0 && P >= 1, GDN_EINVAL, "%s: n = %d, B = %d, P = %d", fn, n, B, P);
     REQUIRE(n <= gdn::kKvForkMax, GDN_EUNSUPPORTED, "%s: n = %d > %d", fn, n, gdn::kKvForkMax);
     if (n == 0) return ok();
+    REQUIRE(B >= 1, GDN_EINVAL, "%s: %d forks of no rows", fn, n);
     REQUIRE(src && dst && lens && table && ref && pool && granted, GDN_EINVAL, "%s: null pointer", fn);
     REQUIRE(aligned16(pool), GDN_EINVAL, "%s: pool must be 16-byte aligned", fn);
     REQUIRE(aligned4(src) && aligned4(dst) && aligned4(lens) && aligned4(table) && aligned4(ref) && aligned4(granted),
