@@ -135,6 +135,15 @@ int small(int64_t n, const char* what)
     return (int)n;
 }
 
+int int_of(PyObject* o, const char* name)
+{
+    int past = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &past);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    if (past || v > 0x7fffffff || v < -0x7fffffff) raise(PyExc_ValueError, "%s does not fit in 32 bits", name);
+    return (int)v;
+}
+
 // an int32 array of a shape; None gives nullptr where it may
 int32_t* ints(PyObject* o, const char* name, std::initializer_list<int64_t> shape, bool optional = false)
 {
@@ -209,8 +218,7 @@ int do_reserve(PyObject* const* a, Py_ssize_t n)
     const Lib& lib = lib_of(a[0]);
     const Table t = table_of(a[4]);
     const at::Tensor& ref = dense(a[5], "ref");
-    const int page = (int)PyLong_AsLong(a[7]);
-    if (page == -1 && PyErr_Occurred()) throw Raised{};
+    const int page = int_of(a[7], "page");
     return lib.kv_reserve(ints(a[2], "lens", {t.B}), ints(a[3], "add", {t.B}), t.p, ints(a[5], "ref", {ref.numel()}),
                           ints(a[6], "granted", {t.B}), t.B, t.P, small(ref.numel(), "n_pages"), page, stream_of(a[1], a[4]));
 }
@@ -242,8 +250,7 @@ int do_rollback(PyObject* const* a, Py_ssize_t n)
     int N;
     if (a[3] == Py_None) {
         if (a[10] == Py_None) raise(PyExc_ValueError, "a chain (parent=None) needs its window length N");
-        N = (int)PyLong_AsLong(a[10]);
-        if (N == -1 && PyErr_Occurred()) throw Raised{};
+        N = int_of(a[10], "N");
     } else {
         const at::Tensor& p = dense(a[3], "parent");
         if (p.dim() != 2) raise(PyExc_ValueError, "parent must be [B][N]");
@@ -323,8 +330,7 @@ int do_attn(PyObject* const* a, Py_ssize_t n)
             raise(PyExc_ValueError, "lse must be float32 [B][K][Hq]");
         lse = static_cast<float*>(l.data_ptr());
     }
-    const long prefix = PyLong_AsLong(a[12]);
-    if (prefix == -1 && PyErr_Occurred()) throw Raised{};
+    const int prefix = int_of(a[12], "prefix_len");
     double scale;
     if (a[13] == Py_None) {
         scale = 1.0 / std::sqrt((double)g.D);
@@ -332,10 +338,9 @@ int do_attn(PyObject* const* a, Py_ssize_t n)
         scale = PyFloat_AsDouble(a[13]);
         if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
     }
-    if (prefix > 0x7fffffff || prefix < -0x7fffffff) raise(PyExc_ValueError, "prefix_len out of range");
     return lib.attn_verify(q.data_ptr(), s, g.p, vp, ints(a[5], "lens", {t.B}), ints(a[6], "count", {t.B}, true),
                            ints(a[7], "parent", {t.B, K}, true), t.p, o.data_ptr(), lse, w.data_ptr(), w.nbytes(), t.B,
-                           small(K, "K"), small(Hq, "Hq"), g.Hkv, g.D, g.page, g.n_pages, t.P, (int)prefix,
+                           small(K, "K"), small(Hq, "Hq"), g.Hkv, g.D, g.page, g.n_pages, t.P, prefix,
                            (float)scale, g.dtype, stream_of(a[1], a[8]));
 }
 
