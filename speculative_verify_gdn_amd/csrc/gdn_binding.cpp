@@ -23,6 +23,8 @@
 #include <initializer_list>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/gdn.h"
@@ -89,22 +91,45 @@ const Lib& lib_of(PyObject* o)
 
 PyObject* g_raw_stream;  // torch's current stream of a device, as an integer
 
-// the stream given, or (None) torch's current one on the device of `on`, an argument that is checked already
-void* stream_of(PyObject* o, PyObject* on)
-{
-    if (o == Py_None) {
-        PyObject* i = PyLong_FromLong(THPVariable_Unpack(on).get_device());
-        o = i ? PyObject_CallOneArg(g_raw_stream, i) : nullptr;
-        Py_XDECREF(i);
-        if (!o) throw Raised{};
-        void* s = PyLong_AsVoidPtr(o);
-        Py_DECREF(o);
-        if (!s && PyErr_Occurred()) throw Raised{};
-        return s;
+// Where a call is launched: the device of `on`, an argument that is checked already, made current for the call (the
+// library launches on the current one), and the stream given, or (None) torch's current one there.  Asked for and
+// switched only where there are several: setting and restoring the same one cost 0.25 us a call.
+struct Launch {
+    c10::OptionalDeviceGuard guard;
+    void* stream;
+
+    Launch(PyObject* o, PyObject* on)
+    {
+        const c10::Device device = THPVariable_Unpack(on).device();
+        const c10::impl::VirtualGuardImpl gpu(device.type());
+        static const int devices = gpu.deviceCount();
+        if (devices > 1 && gpu.getDevice() != device) guard.reset_device(device);
+        if (o == Py_None) {
+            PyObject* i = PyLong_FromLong(device.index());
+            o = i ? PyObject_CallOneArg(g_raw_stream, i) : nullptr;
+            Py_XDECREF(i);
+            if (!o) throw Raised{};
+            stream = PyLong_AsVoidPtr(o);
+            Py_DECREF(o);
+        } else {
+            stream = PyLong_AsVoidPtr(o);
+        }
+        if (!stream && PyErr_Occurred()) throw Raised{};
     }
-    void* s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw Raised{};
-    return s;
+};
+
+// the tensors of a call are on one device
+void same_device(PyObject* const* a, Py_ssize_t n)
+{
+    int device = -1;
+    for (Py_ssize_t i = 2; i < n; ++i) {
+        if (a[i] == Py_None || PyLong_Check(a[i]) || !THPVariable_Check(a[i])) continue;
+        const at::Tensor& t = THPVariable_Unpack(a[i]);
+        if (!t.is_cuda()) continue;   // (turned down by name, where it is taken)
+        if (device >= 0 && t.get_device() != device)
+            raise(PyExc_ValueError, "libgdn takes tensors of one device (here of %d and %d)", device, (int)t.get_device());
+        device = t.get_device();
+    }
 }
 
 // a tensor argument (never None)
@@ -219,8 +244,9 @@ int do_reserve(PyObject* const* a, Py_ssize_t n)
     const Table t = table_of(a[4]);
     const at::Tensor& ref = dense(a[5], "ref");
     const int page = int_of(a[7], "page");
+    const Launch where(a[1], a[4]);
     return lib.kv_reserve(ints(a[2], "lens", {t.B}), ints(a[3], "add", {t.B}), t.p, ints(a[5], "ref", {ref.numel()}),
-                          ints(a[6], "granted", {t.B}), t.B, t.P, small(ref.numel(), "n_pages"), page, stream_of(a[1], a[4]));
+                          ints(a[6], "granted", {t.B}), t.B, t.P, small(ref.numel(), "n_pages"), page, where.stream);
 }
 
 int do_append(PyObject* const* a, Py_ssize_t n)
@@ -236,9 +262,10 @@ int do_append(PyObject* const* a, Py_ssize_t n)
     const long long s = token_stride(k, "k", t.B, K, g.Hkv, g.D, g.dtype);
     if (token_stride(v, "v", t.B, K, g.Hkv, g.D, g.dtype) != s)
         raise(PyExc_ValueError, "k and v must have the same token stride");
+    const Launch where(a[1], a[8]);
     return lib.kv_append(k.data_ptr(), v.data_ptr(), s, g.p, vp, ints(a[6], "lens", {t.B}),
                          ints(a[7], "count", {t.B}, true), t.p, t.B, small(K, "K"), g.Hkv, g.D, g.page, g.n_pages, t.P,
-                         g.dtype, stream_of(a[1], a[8]));
+                         g.dtype, where.stream);
 }
 
 int do_rollback(PyObject* const* a, Py_ssize_t n)
@@ -256,10 +283,11 @@ int do_rollback(PyObject* const* a, Py_ssize_t n)
         if (p.dim() != 2) raise(PyExc_ValueError, "parent must be [B][N]");
         N = small(p.size(1), "N");
     }
+    const Launch where(a[1], a[6]);
     return lib.kv_rollback_tree(ints(a[2], "node", {t.B}), ints(a[3], "parent", {t.B, N}, true),
                                 ints(a[4], "lens", {t.B}), ints(a[5], "count", {t.B}, true), t.p,
                                 ints(a[7], "ref", {g.n_pages}), g.p, ints(a[9], "lens_out", {t.B}), t.B, N, t.P,
-                                g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, stream_of(a[1], a[6]));
+                                g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, where.stream);
 }
 
 int do_free(PyObject* const* a, Py_ssize_t n)
@@ -268,8 +296,9 @@ int do_free(PyObject* const* a, Py_ssize_t n)
     const Lib& lib = lib_of(a[0]);
     const Table t = table_of(a[4]);
     const int64_t rows = dense(a[2], "rows").numel(), pages = dense(a[5], "ref").numel();
+    const Launch where(a[1], a[4]);
     return lib.kv_free(ints(a[2], "rows", {rows}), ints(a[3], "lens", {t.B}), t.p, ints(a[5], "ref", {pages}),
-                       small(rows, "n"), t.B, t.P, small(pages, "n_pages"), stream_of(a[1], a[4]));
+                       small(rows, "n"), t.B, t.P, small(pages, "n_pages"), where.stream);
 }
 
 int do_fork(PyObject* const* a, Py_ssize_t n)
@@ -279,9 +308,10 @@ int do_fork(PyObject* const* a, Py_ssize_t n)
     const Pages g = pages_of(a[7], "pool", 5);
     const Table t = table_of(a[5]);
     const int64_t forks = dense(a[2], "src").numel();
+    const Launch where(a[1], a[5]);
     return lib.kv_fork(ints(a[2], "src", {forks}), ints(a[3], "dst", {forks}), ints(a[4], "lens", {t.B}), t.p,
                        ints(a[6], "ref", {g.n_pages}), g.p, ints(a[8], "granted", {forks}), small(forks, "n"), t.B, t.P,
-                       g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, stream_of(a[1], a[5]));
+                       g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, where.stream);
 }
 
 int do_compact(PyObject* const* a, Py_ssize_t n)
@@ -293,9 +323,10 @@ int do_compact(PyObject* const* a, Py_ssize_t n)
     if (t.scalar_type() != at::kInt || to.scalar_type() != at::kInt)
         raise(PyExc_TypeError, "table and table_out must be int32");
     if (t.sizes() != to.sizes()) raise(PyExc_ValueError, "table_out must have table's shape");
+    const Launch where(a[1], a[2]);
     return lib.kv_compact(static_cast<int32_t*>(t.data_ptr()), ints(a[3], "ref", {g.n_pages}), g.p,
                           static_cast<int32_t*>(to.data_ptr()), ints(a[6], "ref_out", {g.n_pages}), w.data_ptr(),
-                          w.nbytes(), t.numel(), g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, stream_of(a[1], a[2]));
+                          w.nbytes(), t.numel(), g.planes, g.n_pages, g.Hkv, g.page, g.D, g.dtype, where.stream);
 }
 
 int do_copy(PyObject* const* a, Py_ssize_t n)
@@ -304,8 +335,9 @@ int do_copy(PyObject* const* a, Py_ssize_t n)
     const Lib& lib = lib_of(a[0]);
     const Pages g = pages_of(a[4], "pool", 5);
     const int64_t pairs = dense(a[2], "src").numel();
+    const Launch where(a[1], a[2]);
     return lib.kv_copy(ints(a[2], "src", {pairs}), ints(a[3], "dst", {pairs}), g.p, small(pairs, "n"), g.planes,
-                       g.n_pages, g.Hkv, g.page, g.D, g.dtype, stream_of(a[1], a[2]));
+                       g.n_pages, g.Hkv, g.page, g.D, g.dtype, where.stream);
 }
 
 int do_attn(PyObject* const* a, Py_ssize_t n)
@@ -338,10 +370,11 @@ int do_attn(PyObject* const* a, Py_ssize_t n)
         scale = PyFloat_AsDouble(a[13]);
         if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
     }
+    const Launch where(a[1], a[8]);
     return lib.attn_verify(q.data_ptr(), s, g.p, vp, ints(a[5], "lens", {t.B}), ints(a[6], "count", {t.B}, true),
                            ints(a[7], "parent", {t.B, K}, true), t.p, o.data_ptr(), lse, w.data_ptr(), w.nbytes(), t.B,
                            small(K, "K"), small(Hq, "Hq"), g.Hkv, g.D, g.page, g.n_pages, t.P, prefix,
-                           (float)scale, g.dtype, stream_of(a[1], a[8]));
+                           (float)scale, g.dtype, where.stream);
 }
 
 // no C++ exception leaves the extension
@@ -349,6 +382,7 @@ template <int (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
     try {
+        same_device(args, n);
         return PyLong_FromLong(F(args, n));
     } catch (const Raised&) {
         return nullptr;
