@@ -547,7 +547,8 @@ int gdn_kv_compact_workspace(int n_pages, size_t *bytes);
 /*
  * gdn_kv_copy -- page src[i] to page dst[i] in every plane, i < n (a pair with
  * an id outside [0, n_pages) is passed over).  No page may be a source and a
- * destination, or a destination twice, in one call.
+ * destination, or a destination twice, in one call.  n * planes * (16 KB pieces
+ * of a page, rounded up) <= 2^50.
  */
 int gdn_kv_copy(const int32_t *src, const int32_t *dst, void *pool, int n, int planes, int n_pages,
                 int Hkv, int page, int D, int dtype, void *stream);

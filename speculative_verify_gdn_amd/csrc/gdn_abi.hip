@@ -822,6 +822,7 @@ int gdn_kv_copy(const int32_t* src, const int32_t* dst, void* pool, int n, int p
     int rc = check_kv(fn, planes, n_pages, Hkv, page, D, dtype, g);
     if (rc) return rc;
     REQUIRE(n >= 0, GDN_EINVAL, "%s: n = %d < 0", fn, n);
+    REQUIRE(gdn::kv_copy_countable(n, g), GDN_EUNSUPPORTED, "%s: %d pages in %d planes are too many pieces", fn, n, planes);
     if (n == 0) return ok();
     REQUIRE(src && dst && pool, GDN_EINVAL, "%s: null pointer", fn);
     REQUIRE(aligned16(pool) && aligned4(src) && aligned4(dst), GDN_EINVAL,

@@ -465,6 +465,8 @@ __global__ __launch_bounds__(256) void kv_free_kernel(const int32_t* rows, int32
 constexpr int kCopyPer = 4;
 constexpr int kCopyChunk = 256 * kCopyPer;   // pieces a workgroup moves in one go
 constexpr int kCopyGrid = 256 * 8;           // workgroups that fill the chip
+// 1 / chunks and the product are rounded, so a quotient is off by 2^-52 of itself, and half a step from the next integer
+constexpr long long kCopyExact = 1LL << 50;
 
 template <typename F>
 __device__ __forceinline__ void copy_pages(char* pool, const KvGeom& g, long long n, F pair)
@@ -474,7 +476,7 @@ __device__ __forceinline__ void copy_pages(char* pool, const KvGeom& g, long lon
     const size_t bytes = g.page_bytes();
     const double by_chunks = 1.0 / chunks, by_planes = 1.0 / g.planes;
     for (long long w = blockIdx.x; w < all; w += gridDim.x) {
-        // quotients by doubles: exact below 2^52, at a tenth of an integer division's time
+        // quotients by doubles: exact below kCopyExact, at a tenth of an integer division's time
         const long long r = (long long)(((double)w + 0.5) * by_chunks), c = w - r * chunks;
         const long long i = (long long)(((double)r + 0.5) * by_planes), pl = r - i * g.planes;
         int from, to;
@@ -695,6 +697,12 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(KvCompactArgs a)
 }
 
 }  // namespace
+
+bool kv_copy_countable(long long n, const KvGeom& g)
+{
+    const long long chunks = ((long long)(g.page_bytes() >> 4) + kCopyChunk - 1) / kCopyChunk;
+    return n <= kCopyExact / (g.planes * chunks);
+}
 
 size_t kv_compact_words(int n_pages) { return 4 + 2 * (((size_t)n_pages + 1) / 2) + (size_t)n_pages; }
 

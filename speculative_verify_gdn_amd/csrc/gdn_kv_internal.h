@@ -85,6 +85,7 @@ struct AttnArgs {
 };
 
 size_t kv_compact_words(int n_pages);
+bool kv_copy_countable(long long n, const KvGeom& g);  // n pages' pieces stay where the copies count them exactly
 size_t attn_work_bytes(int B, int K, int Hq, int Hkv, int D, int page_log2, int P, int prefix, bool bf16);
 
 hipError_t launch_kv_reserve(const KvReserveArgs& a, hipStream_t s);

@@ -16,3 +16,14 @@ def test_ok(lib, name, kw):  # noqa: F811
 @pytest.mark.parametrize("kw", [dict(B=0, n=1), dict(B=-1, n=0), dict(B=0, n=0, P=0)])
 def test_refused(lib, kw):  # noqa: F811
     assert call(lib, "gdn_kv_fork", **kw) == gdn.GDN_EINVAL
+
+
+COPY = "gdn_kv_copy"
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=2 ** 31 - 1, planes=65535, Hkv=128, page=1024, D=256),           # 2^59 pieces of 16 KB and more
+    dict(n=2 ** 26, planes=65535, Hkv=8, page=1024, D=256, dtype=gdn.GDN_F32)])
+def test_copies_that_cannot_be_counted_are_refused(lib, kw):  # noqa: F811
+    assert call(lib, COPY, **kw) == gdn.GDN_EUNSUPPORTED
+    assert lib.gdn_last_error().decode().startswith(COPY)
