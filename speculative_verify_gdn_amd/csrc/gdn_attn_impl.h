@@ -56,6 +56,7 @@ typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;   // of a workgroup at most
 constexpr float kNoMax = -3.4028234e38f;   // the reference of a row that has seen no key: finite, so that -inf less it is -inf
+constexpr float kNoScore = -0x1.fffffcp127f;   // of one that has seen keys, all with a score of -inf: the next above
 constexpr float kSlack = 8.0f;     // a reference is kept while no exponent passes it by more than 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -285,6 +286,12 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // their order, and is off by less than the scores themselves.
 constexpr float kFar = 1048576.f;
 __device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNoMax; }
+
+// 1 / l of a row; without any weight 0 where it has seen no key, and the 0 / 0 of the formula where all its scores are -inf
+__device__ __forceinline__ float inverse_of(float l, float m)
+{
+    return l != 0.f ? 1.f / l : m == kNoMax ? 0.f : __builtin_nanf("");
+}
 
 // scores enter the exponentials with a factor above 0: the sign of `scale` goes into q, and for a scale of 0 all of q
 __device__ __forceinline__ float factor_of(float scale) { return scale == 0.f ? 1.f : fabsf(scale) * kLog2e; }
@@ -979,6 +986,28 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
             l[r] += __shfl_xor(l[r], 16, 64);
             l[r] += __shfl_xor(l[r], 32, 64);
         }
+        bool none = false;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) none |= l[r] == 0.f;
+        if (was_alive && __any(none)) {
+            // no weight: such a row sees nothing of this piece, or only scores of -inf
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                int tok, t, g;
+                row_of(tag, p, rw * RG + r, tok, t, g);
+                const unsigned long long sees = window ? s.path[serial & 1][t & 63] : 0;
+                const int last = min(p.end, p.p0 + p.tiles * N);
+                bool some = l[r] != 0.f;
+#pragma nounroll
+                for (int pos = p.p0, next; pos < last && !__all(some); pos = next) {   // a page after the other
+                    next = min(((pos >> a.page_log2) + 1) << a.page_log2, last);
+                    if (is_bad(slot_id(row_at(p.b), pos >> a.page_log2))) continue;
+                    const int i0 = max(pos - p.len, 0), i1 = next - p.len;   // nodes i0 .. i1-1 of the window
+                    some |= pos < p.len || (window && (sees >> i0 & ~0ull >> (64 - (i1 - i0))) != 0);
+                }
+                if (l[r] == 0.f && some) m[r] = kNoScore;
+            }
+        }
         if (uni(s.bad_value) == serial && was_alive) {
             // a window value that is not finite makes what it makes of the rows that see it
 #pragma unroll
@@ -1041,7 +1070,7 @@ __global__ __launch_bounds__(OW::THREADS, 2) void attn_kernel(AttnArgs a, int nb
             if (!row_of(tag, p, rw * RG + r, tok, t, g)) continue;
             if (p.slot < 0) {
                 const size_t at = (size_t)tok * a.Hq + p.h * G + g;
-                const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+                const float inv = inverse_of(l[r], m[r]);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     const f32x4_t y = o[r][d] * inv;
@@ -1240,7 +1269,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int nb, in
         }
     }
     if (!mine) return;
-    const f32x4_t y = acc * (L == 0.f ? 0.f : 1.f / L);
+    const f32x4_t y = acc * inverse_of(L, M);
     if constexpr (BF16)
         reinterpret_cast<uint2*>(a.o)[unit] = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
     else
