@@ -12,7 +12,8 @@ read by gdn_debug_clamped_accepts.
 
 Each .hip file under csrc/ is compiled to an object in _build/ (in parallel),
 then linked into speculative_verify_gdn_amd/libgdn.so; the Python extension
-_gdn_binding.so (csrc/gdn_binding.cpp) is compiled beside it.  Flags:
+_gdn_binding.so (csrc/gdn_binding.cpp) is compiled beside it, where there is a
+torch for it to bind (a C program needs hipcc alone).  Flags:
   --offload-arch=gfx950          MI355X only
   -ffp-contract=off              every fused multiply-add is written out
   -fhip-fp32-correctly-rounded-divide-sqrt, -fno-gpu-flush-denormals-to-zero
@@ -69,17 +70,27 @@ def _compile(src: str, build_dir: str = BUILD, extra=()) -> str:
     return obj
 
 
-def build_binding() -> str:
+def _host_compiler() -> list:
+    """$CXX, g++, or hipcc's own compiler as one for C++."""
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    return [cxx] if cxx else [HIPCC, "-x", "c++"]
+
+
+def build_binding():
     """Compile the Python extension that marshals the cache and attention calls (csrc/gdn_binding.cpp) with the
-    host compiler, against torch's headers; returns its path."""
+    host compiler, against torch's headers; returns its path, or None where there is no torch (nothing then loads
+    it: the Python side takes torch tensors)."""
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return None
 
     lib = os.path.join(PKG, "_gdn_binding.so")
     tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = [*_host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
            *("-isystem" + d for d in cpp_extension.include_paths()), "-I" + sysconfig.get_paths()["include"],
            "-o", tmp, os.path.join(CSRC, "gdn_binding.cpp"),
@@ -112,7 +123,7 @@ def build(verbose: bool = False, timeline: bool = False, debug: bool = False) ->
     if not variant:
         binding = build_binding()
         if verbose:
-            print("built", binding)
+            print("built " + binding if binding else "no torch: the Python binding is left out")
     if verbose:
         print("built", lib)
     return lib
