@@ -562,9 +562,13 @@ int gdn_kv_copy(const int32_t *src, const int32_t *dst, void *pool, int n, int p
  *   x_j = scale * q . k_j,   o = sum_j e^{x_j} v_j / sum_j e^{x_j},
  *   lse = log sum_j e^{x_j}
  * over the keys it sees, with x, the sums and the running maximum in fp32 (for
- * bf16 the weights e^{x_j - max} enter the product with v rounded to bf16).  A
- * row that sees no key has o = 0, lse = -inf.  What is in unseen keys and values
- * (NaN, infinities) changes nothing.  Rows t >= count[b] are left untouched.
+ * bf16 the weights e^{x_j - max} enter the product with v rounded to bf16; the
+ * maximum that is subtracted may be passed by up to 2^8 in the exponential, and x
+ * carries a factor of log2 e: values up to 2^119 / (number of keys) and scores up
+ * to 2^127 in size stay within fp32).  A row that sees no key has o = 0,
+ * lse = -inf; one all of whose scores are -inf has o = NaN, lse = -inf.  What is
+ * in unseen keys and values (NaN, infinities) changes nothing.  Rows
+ * t >= count[b] are left untouched.
  *
  * prefix_len > 0 (a multiple of page, at most P*page): every sequence with
  * lens[b] >= prefix_len holds the SAME pages in its first prefix_len/page slots

@@ -6,7 +6,7 @@
 // compact) are one workgroup: their answer is a running count over all pages
 // and all sequences, a few kilobytes of int32, and one workgroup needs no
 // second launch and no cross-workgroup order; what it costs is the latency of its
-// dependent reads, about 0.7 us each (reserve 3.1 us, fork and the plan of a
+// dependent reads, about 0.7 us each (reserve 2.8 to 3.2 us, fork and the plan of a
 // compaction 5 us).  Those that move bytes (append, rollback, page
 // copies) spread 16-byte pieces over the chip.
 #include "gdn_device.h"
@@ -116,7 +116,7 @@ __device__ __forceinline__ bool window_of(const KvReserveArgs& a, int lens, int 
 }
 
 // For up to kCtl sequences and kScan pages: a thread has one sequence and kScanPer pages, which are read once and kept,
-// and wants and free pages are numbered in one scan (two rounds of reads in all, 3.1 us for one sequence; the general
+// and wants and free pages are numbered in one scan (two rounds of reads in all, 2.8 to 3.1 us for one sequence; the general
 // kernel below, with five, takes 4.9).
 constexpr int kSlots = 4;   // slots of a window that are kept (more are read again)
 
@@ -321,8 +321,9 @@ __device__ __forceinline__ Kept kept_of(const KvRollbackArgs& a, int b)
 }
 
 // The table row of a sequence in LDS, read when the kernel starts, beside the lengths and the tree: a read that waits
-// for another costs these kernels most (one layer of one sequence took 5.4 us with the row read after the length and
-// again after the moves).  Longer rows are read from memory where they are needed.
+// for another costs these kernels most (a step of 64 sequences and 8 layers took 23.2 us with the row read after the
+// length and again after the moves, and takes 20.5 to 21.5; one layer of one sequence gains less, 5.1 to 5.3 us of 5.4).
+// Longer rows are read from memory where they are needed.
 constexpr int kRow = 2048;
 
 struct Row {
@@ -459,9 +460,12 @@ __global__ __launch_bounds__(256) void kv_free_kernel(const int32_t* rows, int32
 // ---------------------------------------------------------------- page copies
 // 16-byte pieces of the pages src -> dst of every plane; a workgroup takes
 // kCopyPer pieces of a thread at a time and walks on until all are done.  Memory
-// bounds it: 118 MB read and written in 37 us (900 pages of 2 layers, 6.4 TB/s).
-// Stores past the caches took 36 us there but 40 instead of 38 where 32 copies of one
-// page are made, loads past them 40 and 47; 8 pieces a thread or other grids the same.
+// bounds it: 900 pages of 32 KB in 4 planes, 118 MB read and as much written, take 58 us from a pool of 7.9 GB
+// (4.1 TB/s, a large plain copy reaches 5.2) and 37 to 38 us again and again, when they stay in the last cache.
+// Stores past the caches took 36 us in the second case but 40 instead of 38 where 32 copies
+// of one page are made, loads past them 40 and 47; 8 pieces a thread or other grids the same.
+// Small pages are far from that: a chunk never crosses a page, so 500 pages of 2 KB in 16
+// planes, 33 MB read and written, take 23 us (1.4 TB/s).
 constexpr int kCopyPer = 4;
 constexpr int kCopyChunk = 256 * kCopyPer;   // pieces a workgroup moves in one go
 constexpr int kCopyGrid = 256 * 8;           // workgroups that fill the chip
@@ -725,7 +729,7 @@ hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s)
 hipError_t launch_kv_rollback(const KvRollbackArgs& a, hipStream_t s)
 {
     // One launch up to kCtl pieces a sequence, two above: 16 planes of 64 sequences took 25.6 us in one (64 workgroups
-    // with two pieces a thread), 14 us in two; one layer of one sequence takes 3.3 us in one.
+    // with two pieces a thread), 14 us in two; one layer of one sequence takes 5.1 to 5.3 us in one.
     const int pieces = a.g.planes * a.g.Hkv * (a.g.row_bytes >> 4);
     if (pieces <= kCtl) {
         kv_rollback_kernel<<<dim3(a.B), dim3(pieces <= 256 ? 256 : kCtl), 0, s>>>(a);
