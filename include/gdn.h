@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define GDN_VERSION 4
+#define GDN_VERSION 5
 
 enum gdn_status {
     GDN_OK = 0,
@@ -595,6 +595,154 @@ int gdn_attn_verify(const void *q, long long q_stride, const void *k_pages, cons
 /* bytes that gdn_attn_verify needs as workspace for these sizes */
 int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, int prefix_len,
                        int dtype, size_t *bytes);
+
+/*
+ * What a window passes around the attention -- its queries and keys normed and
+ * turned to their positions on the way into the cache, and at the other end
+ * its logits adjusted and the accepted node found (gdn_kv_rollback_tree,
+ * gdn_rollback_tree and gdn_verify_tree_step take it from there).
+ *
+ * The position of token (b, t) is pos[b][t] where pos is given (any int32; a
+ * negative position turns back), else max(lens[b], 0) + depth(t) (lens NULL: 0),
+ * with depth(t) = t for a chain (parent NULL) and the number of t's ancestors in a
+ * tree (parent as the tree calls above; K <= 64).  So a path that
+ * gdn_kv_rollback_tree moves to the front of its window keeps its positions.
+ * With theta = position * freqs[i] (in 64 bits), c = mscale cos(theta),
+ * s = mscale sin(theta), pair i < rot/2 of a head becomes
+ *   (x_a, x_b) -> (x_a c - x_b s, x_b c + x_a s),
+ *   GDN_ROPE_HALVES: a = i, b = i + rot/2;  GDN_ROPE_INTERLEAVED: a = 2i, b = 2i + 1
+ * and the elements from rot on stay as they are.  The norm of a head, where there
+ * is one, comes first: x_d / sqrt(mean(x^2) + eps) * w_d over all D elements
+ * (in fp32: heads whose squares sum to less than 2^127).  All is fp32 inside
+ * and rounded once; theta is rounded to 32 bits as a part of half a turn, 2^-25 of it
+ * at most.
+ *   D a multiple of 16, at most 512; rot even, 0..D (gdn_rope: from 2); freqs [rot/2] double,
+ *   8-byte aligned, radians a position (gdn_rope_freqs); at most 1024 heads;
+ *   B <= 65535, K <= 65536, B * K < 2^31
+ *   x, q, k, v [B][K][H][D] dtype, 16-byte aligned, with strides: HOST arrays of
+ *   three numbers, the elements from one sequence, token and head to the next (each a multiple of
+ *   16 bytes, 0 repeats it; NULL: dense), so that a slice of a stacked projection row or a
+ *   head-major layout will do; a head's own elements are dense
+ *   wq, wk [D] float; pos [B][K], lens, count [B], parent [B][K] int32, each or
+ *   NULL; rows t >= count[b] (clamped into 0..K; NULL: K) are left untouched
+ * The wide path takes rot in multiples of 32 bytes of elements (16 in bf16, 8 in
+ * fp32); other rot go element by element.
+ */
+enum gdn_rope_layout { GDN_ROPE_HALVES = 0, GDN_ROPE_INTERLEAVED = 1 };
+enum gdn_rope_scaling {
+    GDN_ROPE_PLAIN = 0,
+    GDN_ROPE_LINEAR = 1,
+    GDN_ROPE_NTK = 2,
+    GDN_ROPE_BANDS = 3,
+    GDN_ROPE_YARN = 4
+};
+
+/*
+ * gdn_rope_freqs -- the frequencies of the pairs, on the HOST (nothing is
+ * launched): f_i = base^(-2i/rot), scaled for contexts `factor` (>= 1) times as long
+ * as the `original` one.  With n_i = original * f_i / (2 pi) turns over it:
+ *   PLAIN   f_i                       (factor, low, high, original unused)
+ *   LINEAR  f_i / factor              (low, high, original unused)
+ *   NTK     f_i with base * factor^(rot/(rot-2)) for the base (the same unused; rot > 2)
+ *   BANDS   k f_i + (1-k) f_i / factor, k = (n_i - low) / (high - low) in 0..1
+ *   YARN    the same with k = log(n_i / low) / log(high / low) in 0..1, and
+ *           mscale = 0.1 log(factor) + 1 (Peng et al. 2023; low 1, high 32 there)
+ *   freqs   HOST pointer, rot/2 doubles; mscale HOST pointer (1 except YARN)
+ *   base > 1, 0 < low < high, rot even, 2..512
+ */
+int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low, double high, double original,
+                   double *freqs, float *mscale);
+
+/*
+ * gdn_rope -- y <- x turned.  y [B][K][H][D] with strides of its own, whose rows
+ * do not meet; y may be x with the same strides (in place), else their spans do not overlap.
+ */
+int gdn_rope(const void *x, const long long *x_strides, void *y, const long long *y_strides, const int32_t *pos,
+             const int32_t *lens, const int32_t *parent, const int32_t *count, const double *freqs, int rot,
+             int layout, float mscale, int B, int K, int H, int D, int dtype, void *stream);
+
+/*
+ * gdn_qk_norm_rope -- queries and keys normed and turned: q_out [B][K][Hq][D],
+ * k_out [B][K][Hk][D] dense (a dense q may be q_out, a dense k k_out).  rot = 0: the norm alone (freqs
+ * unused).
+ */
+int gdn_qk_norm_rope(const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+                     const float *wq, const float *wk, float eps, void *q_out, void *k_out, const int32_t *pos,
+                     const int32_t *lens, const int32_t *parent, const int32_t *count, const double *freqs, int rot,
+                     int layout, float mscale, int B, int K, int Hq, int Hk, int D, int dtype, void *stream);
+
+/*
+ * gdn_kv_append_rope -- gdn_kv_append with the keys normed (wk; NULL: not) and
+ * turned on the way, the values byte copies; token (b, t) goes to slot lens[b]+t, also
+ * where its position is another.  In the same launch q (NULL, q_out NULL and Hq = 0: none)
+ * is normed (wq; NULL: not) and turned into q_out [B][K][Hq][D], as gdn_attn_verify takes it.
+ * Keys and queries are gdn_qk_norm_rope's bits (gdn_rope's without weights).
+ * lens and table are required; geometry and table as the cache calls above, D 64, 128 or 256.
+ */
+int gdn_kv_append_rope(const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+                       const void *v, const long long *v_strides, const float *wq, const float *wk, float eps,
+                       void *q_out, void *k_pages, void *v_pages, const int32_t *pos, const int32_t *lens,
+                       const int32_t *parent, const int32_t *count, const int32_t *table, const double *freqs,
+                       int rot, int layout, float mscale, int B, int K, int Hq, int Hkv, int D, int page, int n_pages,
+                       int P, int dtype, void *stream);
+
+/*
+ * gdn_logits_adjust -- the logits of every node of a window, adjusted in this order:
+ *   with s how often v stands in history[b][0 .. history_lens[b]) or on the path
+ *   root..t of tokens, and n how often from history_start[b] on (0 where NULL; the
+ *   path counts in both):
+ *   s > 0: x <- x > 0 ? x / repetition : x * repetition
+ *   n > 0: x <- x - frequency * n, then x - presence
+ *   x <- x + bias of v;  x <- -inf where v is not allowed;
+ *   x <- x / temperature (where that is above 0)
+ * each step rounded once in fp32.  out (NULL: not wanted) receives x in out_dtype, best (NULL:
+ * not wanted) the token with the largest x + noise, the lowest of equal ones, -1 where
+ * every one is -inf (NaN is never the best).
+ *   logits [B][K][V] dtype, row (b, t) starting logits_stride elements after
+ *   the one before it (>= V); out likewise with out_stride; out may be logits with the same
+ *   type and stride
+ *   history [B][capacity] int32 (NULL: none; history_lens clamped into 0..capacity);
+ *   tokens [B][K] int32, the window's own (NULL: none), parent and count as above
+ *   params [B][4] float: repetition, presence, frequency, temperature (NULL: 1, 0,
+ *   0, 1, and history and tokens are not looked at)
+ *   bias_ids, bias_values [B][n_bias] (n_bias = 0: none; an id named twice: its last
+ *   entry counts); tokens and ids outside [0, V) count for nothing
+ *   mask [B][K][ceil(V/32)] uint32: bit v%32 of word v/32 set where v is allowed (NULL: all)
+ *   noise [B][K][V] float (NULL: none; only with best): with Gumbel noise, -log(-log u),
+ *   best is a sample of softmax(x)
+ *   workspace (with best): gdn_logits_workspace bytes, its contents not kept
+ *   between calls (calls on different streams need one each)
+ *   B <= 65535, K <= 64, V <= 2^24, n_bias <= 2^20, capacity <= 2^30; logits, out, noise and
+ *   workspace 16-byte aligned, the others 4
+ */
+int gdn_logits_adjust(const void *logits, long long logits_stride, void *out, long long out_stride, int32_t *best,
+                      const int32_t *history, const int32_t *history_lens, const int32_t *history_start, int capacity,
+                      const int32_t *tokens, const int32_t *parent, const int32_t *count, const float *params,
+                      const int32_t *bias_ids, const float *bias_values, int n_bias, const uint32_t *mask,
+                      const float *noise, void *workspace, size_t workspace_bytes, int B, int K, int V, int dtype,
+                      int out_dtype, void *stream);
+
+/* bytes that gdn_logits_adjust needs as workspace for these sizes */
+int gdn_logits_workspace(int B, int K, int V, size_t *bytes);
+
+/*
+ * gdn_accept_tree -- the deepest node (the lowest index of equally deep ones) whose
+ * path is confirmed: every node on it, t < count[b], has the token that its parent's row
+ * found best, tokens[b][i] == target[b][parent] >= 0, and its root has the token
+ * root[b] (any token where root is NULL or root[b] < 0: the window then starts with a token that is
+ * already certain).
+ *   node[b] <- that node (-1: none), as gdn_kv_rollback_tree takes it;
+ *   next[b] <- target[b][node] (root[b] where there is none, -1 without root): the
+ *   token that follows what is kept
+ *   history [B][capacity], lens, lens_out [B] (all or none): the tokens of the
+ *   path go to history[b][lens[b] ..] (those past capacity nowhere), lens_out[b] <- the
+ *   new length (capacity at most); lens clamped into 0..capacity; lens_out may be lens
+ *   target, tokens [B][K] (target: gdn_logits_adjust's best); parent [B][K] or NULL (a
+ *   chain); count, root [B] or NULL; K <= 64, B <= 2^20, capacity <= 2^30
+ */
+int gdn_accept_tree(const int32_t *target, const int32_t *tokens, const int32_t *parent, const int32_t *count,
+                    const int32_t *root, int32_t *node, int32_t *next, int32_t *history, const int32_t *lens,
+                    int32_t *lens_out, int capacity, int B, int K, void *stream);
 
 #ifdef __cplusplus
 }

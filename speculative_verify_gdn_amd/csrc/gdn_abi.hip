@@ -9,7 +9,9 @@
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
 #include "gdn_kv_internal.h"
+#include "gdn_window_internal.h"
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -893,6 +895,342 @@ int gdn_attn_verify(const void* q, long long q_stride, const void* k_pages, cons
     const gdn::AttnArgs a{q, (size_t)q_stride, k_pages, v_pages, lens, count, parent, table, o, lse, workspace,
                           B, K, Hq, Hkv, D, g.page_log2, n_pages, P, prefix_len, scale, 0, 0, {}};
     return launch_status(gdn::launch_attn(a, bf16, (hipStream_t)stream), fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Where x [B][K][H][D] lies: strides in elements from one sequence, token and head to the next (NULL: dense), as bytes
+// in `step` (0 where there is no next), and the bytes from its first to its last element in `bytes`.  An output's rows
+// must not meet one another (`apart`).
+int check_heads(const char* fn, const char* what, const long long* strides, int B, int K, int H, int D, size_t es,
+                bool apart, long long step[3], size_t& bytes)
+{
+    const long long n[3] = {B, K, H};
+    const long long dense[3] = {(long long)K * H * D, (long long)H * D, D};
+    const long long row = (long long)D * (long long)es;
+    long long last = 0;
+    for (int i = 0; i < 3; ++i) {
+        const long long s = strides ? strides[i] : dense[i];
+        step[i] = 0;
+        if (n[i] <= 1) continue;
+        REQUIRE(s >= 0 && s < (1LL << 40) && s * (long long)es % 16 == 0, GDN_EINVAL,
+                "%s: a stride of %s (%lld) is below 0, too large or no multiple of 16 bytes", fn, what, s);
+        step[i] = s * (long long)es;
+        REQUIRE(step[i] == 0 || n[i] - 1 <= (1LL << 46) / step[i], GDN_EUNSUPPORTED, "%s: %s passes 2^46 bytes", fn, what);
+        last += (n[i] - 1) * step[i];
+    }
+    if (apart) {
+        // from the smallest step on, each has to pass what the smaller ones reach
+        bool done[3] = {n[0] <= 1, n[1] <= 1, n[2] <= 1};
+        long long reach = row;
+        for (int k = 0; k < 3; ++k) {
+            int m = -1;
+            for (int i = 0; i < 3; ++i)
+                if (!done[i] && (m < 0 || step[i] < step[m])) m = i;
+            if (m < 0) break;
+            REQUIRE(step[m] >= reach, GDN_EINVAL, "%s: rows of %s overlap", fn, what);
+            reach += (n[m] - 1) * step[m];
+            done[m] = true;
+        }
+    }
+    bytes = (size_t)(last + row);
+    return GDN_OK;
+}
+
+// what the three rotary calls share
+int check_rope(const char* fn, int B, int K, int D, const int32_t* parent, const double* freqs, int rot, int layout,
+               float mscale, float eps, int dtype, bool may_rest)
+{
+    REQUIRE(valid_dtype(dtype), GDN_EINVAL, "%s: bad dtype code %d", fn, dtype);
+    REQUIRE(B >= 0 && K >= 1 && D >= 1, GDN_EINVAL, "%s: B = %d, K = %d, D = %d", fn, B, K, D);
+    REQUIRE(layout == GDN_ROPE_HALVES || layout == GDN_ROPE_INTERLEAVED, GDN_EINVAL, "%s: bad layout code %d", fn, layout);
+    REQUIRE(rot >= 0 && rot % 2 == 0 && rot <= D, GDN_EINVAL, "%s: rot = %d is odd or outside 0..D = %d", fn, rot, D);
+    REQUIRE(rot > 0 || may_rest, GDN_EINVAL, "%s: rot = 0 leaves nothing to do", fn);
+    REQUIRE(mscale - mscale == 0.0f, GDN_EINVAL, "%s: mscale is not finite", fn);
+    REQUIRE(eps >= 0.0f && eps - eps == 0.0f, GDN_EINVAL, "%s: eps is below 0 or not finite", fn);
+    REQUIRE(D % 16 == 0 && D <= gdn::kRopeHeadMax, GDN_EUNSUPPORTED, "%s: D = %d is no multiple of 16 up to %d", fn, D,
+            gdn::kRopeHeadMax);
+    REQUIRE(B <= 65535 && K <= 65536 && (long long)B * K < (1LL << 31), GDN_EUNSUPPORTED, "%s: B = %d, K = %d too large",
+            fn, B, K);
+    REQUIRE(!parent || K <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: a tree of K = %d > %d nodes", fn, K,
+            gdn::kKvWindowMax);
+    REQUIRE(rot == 0 || freqs || B == 0, GDN_EINVAL, "%s: null freqs", fn);
+    REQUIRE((reinterpret_cast<uintptr_t>(freqs) & 7u) == 0, GDN_EINVAL, "%s: freqs must be 8-byte aligned", fn);
+    return GDN_OK;
+}
+
+bool heads_in_range(int H) { return H >= 1 && H <= 1024; }
+
+}  // namespace
+
+extern "C" {
+
+int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low, double high, double original,
+                   double* freqs, float* mscale)
+{
+    const char* fn = "gdn_rope_freqs";
+    REQUIRE(rot >= 2 && rot % 2 == 0, GDN_EINVAL, "%s: rot = %d is odd or below 2", fn, rot);
+    REQUIRE(rot <= gdn::kRopeHeadMax, GDN_EUNSUPPORTED, "%s: rot = %d > %d", fn, rot, gdn::kRopeHeadMax);
+    REQUIRE(std::isfinite(base) && base > 1.0, GDN_EINVAL, "%s: base = %g is not above 1", fn, base);
+    REQUIRE(scaling >= GDN_ROPE_PLAIN && scaling <= GDN_ROPE_YARN, GDN_EINVAL, "%s: bad scaling code %d", fn, scaling);
+    REQUIRE(freqs && mscale, GDN_EINVAL, "%s: null pointer", fn);
+    if (scaling != GDN_ROPE_PLAIN)
+        REQUIRE(std::isfinite(factor) && factor >= 1.0, GDN_EINVAL, "%s: factor = %g is below 1", fn, factor);
+    if (scaling == GDN_ROPE_NTK) REQUIRE(rot > 2, GDN_EINVAL, "%s: one pair has no base to enlarge", fn);
+    if (scaling == GDN_ROPE_BANDS || scaling == GDN_ROPE_YARN)
+        REQUIRE(std::isfinite(original) && original > 0.0 && low > 0.0 && high > low && std::isfinite(high), GDN_EINVAL,
+                "%s: original = %g, low = %g, high = %g", fn, original, low, high);
+    const double two_pi = 6.283185307179586476925;
+    if (scaling == GDN_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot);
+        const double turns = original * f / two_pi;   // over the original context
+        // how much of the frequency is kept, the rest being divided by the factor
+        double keep = scaling == GDN_ROPE_LINEAR ? 0.0 : 1.0;
+        if (scaling == GDN_ROPE_BANDS) keep = (turns - low) / (high - low);
+        // (the pair's index is linear in the logarithm of its turns)
+        if (scaling == GDN_ROPE_YARN) keep = std::log(turns / low) / std::log(high / low);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        freqs[i] = keep == 1.0 ? f : keep * f + (1.0 - keep) * f / factor;
+    }
+    *mscale = scaling == GDN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return ok();
+}
+
+int gdn_rope(const void* x, const long long* x_strides, void* y, const long long* y_strides, const int32_t* pos,
+             const int32_t* lens, const int32_t* parent, const int32_t* count, const double* freqs, int rot, int layout,
+             float mscale, int B, int K, int H, int D, int dtype, void* stream)
+{
+    const char* fn = "gdn_rope";
+    int rc = check_rope(fn, B, K, D, parent, freqs, rot, layout, mscale, 0.0f, dtype, false);
+    if (rc) return rc;
+    REQUIRE(H >= 1, GDN_EINVAL, "%s: H = %d < 1", fn, H);
+    REQUIRE(heads_in_range(H), GDN_EUNSUPPORTED, "%s: H = %d > 1024", fn, H);
+    if (B == 0) return ok();
+    REQUIRE(x && y, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned16(x) && aligned16(y), GDN_EINVAL, "%s: x and y must be 16-byte aligned", fn);
+    REQUIRE(aligned4(pos) && aligned4(lens) && aligned4(parent) && aligned4(count), GDN_EINVAL,
+            "%s: int32 pointers must be 4-byte aligned", fn);
+    const size_t es = elem_size(dtype), tokens = (size_t)B * K;
+    gdn::RopeArgs a{};
+    gdn::RopePart& q = a.part[0];
+    size_t in, out;
+    if ((rc = check_heads(fn, "x", x_strides, B, K, H, D, es, false, q.xs, in))) return rc;
+    if ((rc = check_heads(fn, "y", y_strides, B, K, H, D, es, true, q.ys, out))) return rc;
+    const bool in_place = x == y && memcmp(q.xs, q.ys, sizeof(q.xs)) == 0;
+    const Span outs[] = {Span{y, out}};
+    const Span ins[] = {Span{in_place ? nullptr : x, in}, ints(pos, tokens), ints(lens, B), ints(parent, tokens),
+                        ints(count, B), Span{freqs, (size_t)rot / 2 * 8}};
+    REQUIRE(!any_overlap(outs, 1, ins, 6), GDN_EINVAL, "%s: y overlaps an input", fn);
+    q.x = x, q.y = y, q.H = H, q.turned = 1;
+    a.pos = pos, a.lens = lens, a.parent = parent, a.count = count, a.freqs = freqs;
+    a.rot = rot, a.mscale = mscale, a.B = B, a.K = K, a.D = D;
+    return launch_status(gdn::launch_rope(a, dtype == GDN_BF16, layout == GDN_ROPE_INTERLEAVED, (hipStream_t)stream), fn);
+}
+
+int gdn_qk_norm_rope(const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+                     const float* wq, const float* wk, float eps, void* q_out, void* k_out, const int32_t* pos,
+                     const int32_t* lens, const int32_t* parent, const int32_t* count, const double* freqs, int rot,
+                     int layout, float mscale, int B, int K, int Hq, int Hk, int D, int dtype, void* stream)
+{
+    const char* fn = "gdn_qk_norm_rope";
+    int rc = check_rope(fn, B, K, D, parent, freqs, rot, layout, mscale, eps, dtype, true);
+    if (rc) return rc;
+    REQUIRE(Hq >= 1 && Hk >= 1, GDN_EINVAL, "%s: Hq = %d, Hk = %d must be >= 1", fn, Hq, Hk);
+    REQUIRE(heads_in_range(Hq) && heads_in_range(Hk), GDN_EUNSUPPORTED, "%s: Hq = %d or Hk = %d > 1024", fn, Hq, Hk);
+    if (B == 0) return ok();
+    REQUIRE(q && k && wq && wk && q_out && k_out, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned16(q) && aligned16(k) && aligned16(q_out) && aligned16(k_out), GDN_EINVAL,
+            "%s: q, k, q_out and k_out must be 16-byte aligned", fn);
+    REQUIRE(aligned4(wq) && aligned4(wk) && aligned4(pos) && aligned4(lens) && aligned4(parent) && aligned4(count),
+            GDN_EINVAL, "%s: weights and int32 pointers must be 4-byte aligned", fn);
+    const size_t es = elem_size(dtype), tokens = (size_t)B * K;
+    gdn::RopeArgs a{};
+    const void* x[2] = {q, k};
+    void* y[2] = {q_out, k_out};
+    const long long* strides[2] = {q_strides, k_strides};
+    const float* w[2] = {wq, wk};
+    const int H[2] = {Hq, Hk};
+    const char* name[2] = {"q", "k"};
+    size_t in[2], out[2];
+    bool in_place[2];
+    for (int i = 0; i < 2; ++i) {
+        gdn::RopePart& p = a.part[i];
+        if ((rc = check_heads(fn, name[i], strides[i], B, K, H[i], D, es, false, p.xs, in[i]))) return rc;
+        if ((rc = check_heads(fn, name[i], nullptr, B, K, H[i], D, es, true, p.ys, out[i]))) return rc;
+        p.x = x[i], p.y = y[i], p.w = w[i], p.H = H[i], p.turned = 1;
+        in_place[i] = x[i] == y[i] && memcmp(p.xs, p.ys, sizeof(p.xs)) == 0;
+    }
+    // a dense q may be q_out, a dense k k_out; nothing else may be shared
+    const Span spans[] = {Span{q, in[0]}, Span{k, in[1]}};
+    const Span outs[] = {Span{q_out, out[0]}, Span{k_out, out[1]}};
+    const Span ins[] = {ints(pos, tokens), ints(lens, B), ints(parent, tokens), ints(count, B), Span{wq, (size_t)D * 4},
+                        Span{wk, (size_t)D * 4}, Span{freqs, (size_t)rot / 2 * 8}};
+    REQUIRE(!any_overlap(outs, 2, ins, 7), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            REQUIRE((i == j && in_place[i]) || !overlap(outs[i], spans[j]), GDN_EINVAL, "%s: %s_out overlaps %s", fn,
+                    name[i], name[j]);
+    a.pos = pos, a.lens = lens, a.parent = parent, a.count = count, a.freqs = freqs;
+    a.rot = rot, a.mscale = mscale, a.eps = eps, a.B = B, a.K = K, a.D = D;
+    return launch_status(gdn::launch_rope(a, dtype == GDN_BF16, layout == GDN_ROPE_INTERLEAVED, (hipStream_t)stream), fn);
+}
+
+int gdn_kv_append_rope(const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+                       const void* v, const long long* v_strides, const float* wq, const float* wk, float eps,
+                       void* q_out, void* k_pages, void* v_pages, const int32_t* pos, const int32_t* lens,
+                       const int32_t* parent, const int32_t* count, const int32_t* table, const double* freqs, int rot,
+                       int layout, float mscale, int B, int K, int Hq, int Hkv, int D, int page, int n_pages, int P,
+                       int dtype, void* stream)
+{
+    const char* fn = "gdn_kv_append_rope";
+    gdn::RopeArgs a{};
+    int rc = check_kv(fn, 1, n_pages, Hkv, page, D, dtype, a.g);
+    if (rc) return rc;
+    if ((rc = check_rope(fn, B, K, D, parent, freqs, rot, layout, mscale, eps, dtype, true))) return rc;
+    REQUIRE(P >= 1, GDN_EINVAL, "%s: P = %d < 1", fn, P);
+    REQUIRE(Hq >= 0, GDN_EINVAL, "%s: Hq = %d < 0", fn, Hq);
+    REQUIRE(Hq <= 1024, GDN_EUNSUPPORTED, "%s: Hq = %d > 1024", fn, Hq);
+    if (B == 0) return ok();
+    REQUIRE(k && v && k_pages && v_pages && lens && table, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE((q != nullptr) == (Hq > 0) && (q_out != nullptr) == (Hq > 0), GDN_EINVAL,
+            "%s: q and q_out are both given (Hq heads) or both NULL (Hq = 0)", fn);
+    REQUIRE(!wq || Hq > 0, GDN_EINVAL, "%s: wq without q", fn);
+    REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(q_out) && aligned16(k_pages) && aligned16(v_pages),
+            GDN_EINVAL, "%s: q, k, v, q_out and the planes must be 16-byte aligned", fn);
+    REQUIRE(aligned4(wq) && aligned4(wk) && aligned4(pos) && aligned4(lens) && aligned4(parent) && aligned4(count) &&
+                aligned4(table),
+            GDN_EINVAL, "%s: weights and int32 pointers must be 4-byte aligned", fn);
+    const size_t es = elem_size(dtype), tokens = (size_t)B * K, plane = (size_t)n_pages * a.g.page_bytes();
+    gdn::RopePart &pq = a.part[0], &pk = a.part[1], &pv = a.part[2];
+    size_t in_q = 0, in_k, in_v, out_q = 0;
+    if (Hq > 0) {
+        if ((rc = check_heads(fn, "q", q_strides, B, K, Hq, D, es, false, pq.xs, in_q))) return rc;
+        if ((rc = check_heads(fn, "q_out", nullptr, B, K, Hq, D, es, true, pq.ys, out_q))) return rc;
+    }
+    if ((rc = check_heads(fn, "k", k_strides, B, K, Hkv, D, es, false, pk.xs, in_k))) return rc;
+    if ((rc = check_heads(fn, "v", v_strides, B, K, Hkv, D, es, false, pv.xs, in_v))) return rc;
+    pq.x = q, pq.y = q_out, pq.w = wq, pq.H = Hq, pq.turned = 1;
+    pk.x = k, pk.y = k_pages, pk.w = wk, pk.H = Hkv, pk.turned = 1, pk.paged = 1;
+    pv.x = v, pv.y = v_pages, pv.H = Hkv, pv.paged = 1;
+    const bool in_place = q == q_out && memcmp(pq.xs, pq.ys, sizeof(pq.xs)) == 0;
+    const Span sq{q, in_q}, so{q_out, out_q};
+    const Span outs[] = {so, Span{k_pages, plane}, Span{v_pages, plane}};
+    const Span ins[] = {Span{k, in_k}, Span{v, in_v}, ints(pos, tokens), ints(lens, B), ints(parent, tokens),
+                        ints(count, B), ints(table, (size_t)B * P), Span{wq, (size_t)D * 4}, Span{wk, (size_t)D * 4},
+                        Span{freqs, (size_t)rot / 2 * 8}};
+    REQUIRE(!any_overlap(outs, 3, ins, 10), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    REQUIRE(!overlap(outs[1], sq) && !overlap(outs[2], sq) && (in_place || !overlap(so, sq)), GDN_EINVAL,
+            "%s: an output overlaps q", fn);
+    a.pos = pos, a.lens = lens, a.parent = parent, a.count = count, a.table = table, a.freqs = freqs;
+    a.rot = rot, a.mscale = mscale, a.eps = eps, a.B = B, a.K = K, a.D = D, a.P = P;
+    return launch_status(gdn::launch_rope(a, dtype == GDN_BF16, layout == GDN_ROPE_INTERLEAVED, (hipStream_t)stream), fn);
+}
+
+static int check_logits(const char* fn, int B, int K, int V)
+{
+    REQUIRE(B >= 0 && K >= 1 && V >= 1, GDN_EINVAL, "%s: B = %d, K = %d, V = %d", fn, B, K, V);
+    REQUIRE(B <= 65535, GDN_EUNSUPPORTED, "%s: B = %d > 65535", fn, B);
+    REQUIRE(K <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: K = %d > %d", fn, K, gdn::kKvWindowMax);
+    REQUIRE(V <= 1 << 24, GDN_EUNSUPPORTED, "%s: V = %d > 2^24", fn, V);
+    return GDN_OK;
+}
+
+int gdn_logits_workspace(int B, int K, int V, size_t* bytes)
+{
+    const char* fn = "gdn_logits_workspace";
+    int rc = check_logits(fn, B, K, V);
+    if (rc) return rc;
+    REQUIRE(bytes, GDN_EINVAL, "%s: null bytes", fn);
+    *bytes = (size_t)B * K * gdn::logits_slices(B, V) * 8;
+    return ok();
+}
+
+int gdn_logits_adjust(const void* logits, long long logits_stride, void* out, long long out_stride, int32_t* best,
+                      const int32_t* history, const int32_t* history_lens, const int32_t* history_start, int capacity,
+                      const int32_t* tokens, const int32_t* parent, const int32_t* count, const float* params,
+                      const int32_t* bias_ids, const float* bias_values, int n_bias, const uint32_t* mask,
+                      const float* noise, void* workspace, size_t workspace_bytes, int B, int K, int V, int dtype,
+                      int out_dtype, void* stream)
+{
+    const char* fn = "gdn_logits_adjust";
+    int rc = check_logits(fn, B, K, V);
+    if (rc) return rc;
+    REQUIRE(valid_dtype(dtype) && valid_dtype(out_dtype), GDN_EINVAL, "%s: bad dtype code (%d, %d)", fn, dtype, out_dtype);
+    REQUIRE(n_bias >= 0 && n_bias <= 1 << 20, GDN_EINVAL, "%s: n_bias = %d is not in 0..2^20", fn, n_bias);
+    if (B == 0) return ok();
+    REQUIRE(logits && (out || best), GDN_EINVAL, "%s: null logits, or neither out nor best", fn);
+    const size_t es = elem_size(dtype), oe = elem_size(out_dtype), rows = (size_t)B * K;
+    REQUIRE(logits_stride >= V && logits_stride < (1LL << 40), GDN_EINVAL, "%s: logits_stride = %lld < V = %d", fn,
+            logits_stride, V);
+    if (out)
+        REQUIRE(out_stride >= V && out_stride < (1LL << 40), GDN_EINVAL, "%s: out_stride = %lld < V = %d", fn, out_stride, V);
+    REQUIRE(aligned16(logits) && aligned16(out) && aligned16(noise) && aligned16(workspace), GDN_EINVAL,
+            "%s: logits, out, noise and workspace must be 16-byte aligned", fn);
+    REQUIRE(aligned4(best) && aligned4(history) && aligned4(history_lens) && aligned4(history_start) &&
+                aligned4(tokens) && aligned4(parent) && aligned4(count) && aligned4(params) && aligned4(bias_ids) &&
+                aligned4(bias_values) && aligned4(mask),
+            GDN_EINVAL, "%s: int32 and float pointers must be 4-byte aligned", fn);
+    if (history) {
+        REQUIRE(history_lens, GDN_EINVAL, "%s: history without history_lens", fn);
+        REQUIRE(capacity >= 1 && capacity <= 1 << 30, GDN_EINVAL, "%s: capacity = %d is not in 1..2^30", fn, capacity);
+    }
+    REQUIRE(n_bias == 0 || (bias_ids && bias_values), GDN_EINVAL, "%s: biases without bias_ids or bias_values", fn);
+    REQUIRE(!noise || best, GDN_EINVAL, "%s: noise is for finding best", fn);
+    size_t need = 0;
+    if (best) {
+        need = rows * gdn::logits_slices(B, V) * 8;
+        REQUIRE(workspace && workspace_bytes >= need, GDN_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn,
+                workspace ? workspace_bytes : (size_t)0, need);
+    }
+    const bool in_place = logits == out && dtype == out_dtype && logits_stride == out_stride;
+    const Span sx{logits, ((rows - 1) * logits_stride + V) * es};
+    const Span outs[] = {Span{out, out ? ((rows - 1) * out_stride + V) * oe : 0}, ints(best, rows),
+                         Span{best ? workspace : nullptr, need}};
+    const Span ins[] = {ints(history, history ? (size_t)B * capacity : 0), ints(history_lens, B), ints(history_start, B),
+                        ints(tokens, rows), ints(parent, rows), ints(count, B), Span{params, (size_t)B * 16},
+                        ints(n_bias ? bias_ids : nullptr, (size_t)B * n_bias),
+                        Span{n_bias ? bias_values : nullptr, (size_t)B * n_bias * 4},
+                        Span{mask, rows * (((size_t)V + 31) / 32) * 4}, Span{noise, rows * V * 4}};
+    REQUIRE(!any_overlap(outs, 3, ins, 11), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    REQUIRE(!overlap(outs[1], sx) && !overlap(outs[2], sx) && (in_place || !overlap(outs[0], sx)), GDN_EINVAL,
+            "%s: an output overlaps logits", fn);
+    gdn::LogitsArgs a{};
+    a.x = logits, a.out = out, a.x_stride = (size_t)logits_stride, a.out_stride = out ? (size_t)out_stride : 0;
+    a.best = best, a.history = history, a.history_lens = history_lens, a.history_start = history_start;
+    a.tokens = tokens, a.parent = parent, a.count = count, a.params = params, a.bias_ids = bias_ids;
+    a.bias_values = bias_values, a.mask = mask, a.noise = noise, a.work = static_cast<int2*>(workspace);
+    a.B = B, a.K = K, a.V = V, a.capacity = capacity, a.n_bias = n_bias;
+    return launch_status(gdn::launch_logits(a, dtype == GDN_BF16, out_dtype == GDN_BF16, (hipStream_t)stream), fn);
+}
+
+int gdn_accept_tree(const int32_t* target, const int32_t* tokens, const int32_t* parent, const int32_t* count,
+                    const int32_t* root, int32_t* node, int32_t* next, int32_t* history, const int32_t* lens,
+                    int32_t* lens_out, int capacity, int B, int K, void* stream)
+{
+    const char* fn = "gdn_accept_tree";
+    REQUIRE(B >= 0 && K >= 1, GDN_EINVAL, "%s: B = %d, K = %d", fn, B, K);
+    REQUIRE(K <= gdn::kKvWindowMax, GDN_EUNSUPPORTED, "%s: K = %d > %d", fn, K, gdn::kKvWindowMax);
+    REQUIRE(B <= 1 << 20, GDN_EUNSUPPORTED, "%s: B = %d > 2^20", fn, B);
+    if (B == 0) return ok();
+    REQUIRE(target && tokens && node && next, GDN_EINVAL, "%s: null pointer", fn);
+    REQUIRE((history != nullptr) == (lens != nullptr) && (history != nullptr) == (lens_out != nullptr), GDN_EINVAL,
+            "%s: history, lens and lens_out are all given or all NULL", fn);
+    if (history)
+        REQUIRE(capacity >= 1 && capacity <= 1 << 30, GDN_EINVAL, "%s: capacity = %d is not in 1..2^30", fn, capacity);
+    REQUIRE(aligned4(target) && aligned4(tokens) && aligned4(parent) && aligned4(count) && aligned4(root) &&
+                aligned4(node) && aligned4(next) && aligned4(history) && aligned4(lens) && aligned4(lens_out),
+            GDN_EINVAL, "%s: pointers must be 4-byte aligned", fn);
+    const size_t n = (size_t)B * K;
+    const Span outs[] = {ints(node, B), ints(next, B), ints(history, history ? (size_t)B * capacity : 0),
+                         ints(lens_out, B)};
+    const Span ins[] = {ints(target, n), ints(tokens, n), ints(parent, n), ints(count, B), ints(root, B),
+                        ints(lens == lens_out ? nullptr : lens, B)};
+    REQUIRE(!any_overlap(outs, 4, ins, 6), GDN_EINVAL, "%s: an output overlaps another buffer", fn);
+    const gdn::AcceptArgs a{target, tokens, parent, count, root, node, next, history, lens, lens_out, B, K, capacity};
+    return launch_status(gdn::launch_accept(a, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

@@ -1,10 +1,11 @@
 // gdn_binding.cpp -- the argument marshalling of the paged cache and window
-// attention calls, as a Python extension (_gdn_binding, imported by gdn.py).
+// attention calls and of those around them (rotary positions, logits, acceptance),
+// as a Python extension (_gdn_binding, imported by gdn.py).
 //
 // Nothing is computed here: each function checks its torch tensors (on the
 // device, dense, of the right type and shape), and passes their pointers and
 // sizes to the C entry point of the same name.  The calls are short (a few
-// microseconds on the GPU) and take up to ten tensors; with the checks and the
+// microseconds on the GPU) and take up to fifteen tensors; with the checks and the
 // conversions in Python a call costs 6 to 14 us of host time before anything is
 // launched, here below 1.
 //
@@ -53,6 +54,11 @@ struct Lib {
     decltype(&gdn_kv_compact) kv_compact;
     decltype(&gdn_kv_copy) kv_copy;
     decltype(&gdn_attn_verify) attn_verify;
+    decltype(&gdn_rope) rope;
+    decltype(&gdn_qk_norm_rope) qk_norm_rope;
+    decltype(&gdn_kv_append_rope) kv_append_rope;
+    decltype(&gdn_logits_adjust) logits_adjust;
+    decltype(&gdn_accept_tree) accept_tree;
     void* handle = nullptr;
 };
 
@@ -84,6 +90,11 @@ const Lib& lib_of(PyObject* o)
     symbol(h, n.kv_compact, "gdn_kv_compact");
     symbol(h, n.kv_copy, "gdn_kv_copy");
     symbol(h, n.attn_verify, "gdn_attn_verify");
+    symbol(h, n.rope, "gdn_rope");
+    symbol(h, n.qk_norm_rope, "gdn_qk_norm_rope");
+    symbol(h, n.kv_append_rope, "gdn_kv_append_rope");
+    symbol(h, n.logits_adjust, "gdn_logits_adjust");
+    symbol(h, n.accept_tree, "gdn_accept_tree");
     n.handle = h;
     g_libs.push_back(n);
     return g_libs.back();
@@ -377,6 +388,229 @@ int do_attn(PyObject* const* a, Py_ssize_t n)
                            (float)scale, g.dtype, where.stream);
 }
 
+// a float32 array of a shape; None gives nullptr where it may
+float* floats(PyObject* o, const char* name, std::initializer_list<int64_t> shape, bool optional = false)
+{
+    if (optional && o == Py_None) return nullptr;
+    const at::Tensor& t = dense(o, name);
+    if (t.scalar_type() != at::kFloat) raise(PyExc_TypeError, "%s must be float32", name);
+    if (t.sizes() != at::IntArrayRef(shape)) raise(PyExc_ValueError, "%s has the wrong shape", name);
+    return static_cast<float*>(t.data_ptr());
+}
+
+float float_of(PyObject* o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return (float)v;
+}
+
+int layout_of(PyObject* interleaved)
+{
+    const int yes = PyObject_IsTrue(interleaved);
+    if (yes < 0) throw Raised{};
+    return yes ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALVES;
+}
+
+// x [B][K][H][D] with any strides above its elements
+struct Heads {
+    void* p = nullptr;
+    int64_t B = 0, K = 0, H = 0, D = 0;
+    int dtype = 0;
+    long long s[3] = {0, 0, 0};
+};
+
+Heads heads_of(PyObject* o, const char* name)
+{
+    const at::Tensor& t = tensor(o, name);
+    if (!t.is_cuda()) raise(PyExc_ValueError, "libgdn takes device tensors (%s)", name);
+    if (t.dim() != 4) raise(PyExc_ValueError, "%s must be [B][K][heads][D]", name);
+    if (t.size(3) > 1 && t.stride(3) != 1) raise(PyExc_ValueError, "%s must have dense heads", name);
+    Heads h;
+    h.p = t.data_ptr(), h.dtype = dtype_of(t, name);
+    h.B = t.size(0), h.K = t.size(1), h.H = t.size(2), h.D = t.size(3);
+    for (int i = 0; i < 3; ++i) h.s[i] = t.stride(i);
+    return h;
+}
+
+// a dense output of x's shape and type
+void* like(PyObject* o, const char* name, const Heads& x)
+{
+    const at::Tensor& t = dense(o, name);
+    if (t.sizes() != at::IntArrayRef({x.B, x.K, x.H, x.D}) || dtype_of(t, name) != x.dtype)
+        raise(PyExc_ValueError, "%s must have its input's shape and type", name);
+    return t.data_ptr();
+}
+
+struct Freqs {
+    double* p = nullptr;
+    int rot = 0;
+};
+
+Freqs freqs_of(PyObject* o, bool optional)
+{
+    Freqs f;
+    if (optional && o == Py_None) return f;
+    const at::Tensor& t = dense(o, "freqs");
+    if (t.scalar_type() != at::kDouble) raise(PyExc_TypeError, "freqs must be float64");
+    if (t.dim() != 1) raise(PyExc_ValueError, "freqs must be [rot/2]");
+    f.p = static_cast<double*>(t.data_ptr());
+    f.rot = small(2 * t.numel(), "rot");
+    return f;
+}
+
+int do_rope(PyObject* const* a, Py_ssize_t n)
+{
+    want(n, 11);  // lib stream x y freqs pos lens parent count interleaved mscale
+    const Lib& lib = lib_of(a[0]);
+    const Heads x = heads_of(a[2], "x"), y = heads_of(a[3], "y");
+    if (x.B != y.B || x.K != y.K || x.H != y.H || x.D != y.D || x.dtype != y.dtype)
+        raise(PyExc_ValueError, "y must have x's shape and type");
+    const Freqs f = freqs_of(a[4], false);
+    const int layout = layout_of(a[9]);
+    const float mscale = float_of(a[10]);
+    const Launch where(a[1], a[2]);
+    return lib.rope(x.p, x.s, y.p, y.s, ints(a[5], "pos", {x.B, x.K}, true), ints(a[6], "lens", {x.B}, true),
+                    ints(a[7], "parent", {x.B, x.K}, true), ints(a[8], "count", {x.B}, true), f.p, f.rot, layout, mscale,
+                    small(x.B, "B"), small(x.K, "K"), small(x.H, "H"), small(x.D, "D"), x.dtype, where.stream);
+}
+
+int do_qk_norm_rope(PyObject* const* a, Py_ssize_t n)
+{
+    want(n, 16);  // lib stream q k wq wk freqs q_out k_out pos lens parent count eps interleaved mscale
+    const Lib& lib = lib_of(a[0]);
+    const Heads q = heads_of(a[2], "q"), k = heads_of(a[3], "k");
+    if (q.B != k.B || q.K != k.K || q.D != k.D || q.dtype != k.dtype)
+        raise(PyExc_ValueError, "q and k must agree in all but their heads");
+    void *qo = like(a[7], "q_out", q), *ko = like(a[8], "k_out", k);
+    const Freqs f = freqs_of(a[6], true);
+    const float eps = float_of(a[13]), mscale = float_of(a[15]);
+    const int layout = layout_of(a[14]);
+    const Launch where(a[1], a[2]);
+    return lib.qk_norm_rope(q.p, q.s, k.p, k.s, floats(a[4], "wq", {q.D}), floats(a[5], "wk", {q.D}), eps, qo, ko,
+                            ints(a[9], "pos", {q.B, q.K}, true), ints(a[10], "lens", {q.B}, true),
+                            ints(a[11], "parent", {q.B, q.K}, true), ints(a[12], "count", {q.B}, true), f.p, f.rot, layout,
+                            mscale, small(q.B, "B"), small(q.K, "K"), small(q.H, "Hq"), small(k.H, "Hk"), small(q.D, "D"),
+                            q.dtype, where.stream);
+}
+
+int do_append_rope(PyObject* const* a, Py_ssize_t n)
+{
+    want(n, 19);  // lib stream k v k_pages v_pages lens table freqs q q_out wq wk pos parent count eps interleaved mscale
+    const Lib& lib = lib_of(a[0]);
+    void* vp;
+    const Pages g = plane_pair(a[4], a[5], &vp);
+    const Table t = table_of(a[7]);
+    const Heads k = heads_of(a[2], "k"), v = heads_of(a[3], "v");
+    if (k.B != t.B || k.H != g.Hkv || k.D != g.D || k.dtype != g.dtype || v.B != k.B || v.K != k.K || v.H != k.H ||
+        v.D != k.D || v.dtype != k.dtype)
+        raise(PyExc_ValueError, "k and v must be [B][K][Hkv][D] of the cache's type");
+    Heads q;
+    void* qo = nullptr;
+    if (a[9] != Py_None) {
+        q = heads_of(a[9], "q");
+        if (q.B != k.B || q.K != k.K || q.D != k.D || q.dtype != k.dtype)
+            raise(PyExc_ValueError, "q must be [B][K][Hq][D] of the cache's type");
+        qo = like(a[10], "q_out", q);
+    } else if (a[10] != Py_None) {
+        raise(PyExc_ValueError, "q_out without q");
+    }
+    const Freqs f = freqs_of(a[8], true);
+    const float eps = float_of(a[16]), mscale = float_of(a[18]);
+    const int layout = layout_of(a[17]);
+    const Launch where(a[1], a[7]);
+    return lib.kv_append_rope(q.p, q.s, k.p, k.s, v.p, v.s, floats(a[11], "wq", {g.D}, true),
+                              floats(a[12], "wk", {g.D}, true), eps, qo, g.p, vp, ints(a[13], "pos", {k.B, k.K}, true),
+                              ints(a[6], "lens", {t.B}), ints(a[14], "parent", {k.B, k.K}, true),
+                              ints(a[15], "count", {t.B}, true), t.p, f.p, f.rot, layout, mscale, t.B, small(k.K, "K"),
+                              small(q.H, "Hq"), g.Hkv, g.D, g.page, g.n_pages, t.P, g.dtype, where.stream);
+}
+
+// elements between the rows of x [B][K][V], which may be slices of wider ones
+long long row_stride(const at::Tensor& x, const char* name, int64_t B, int64_t K, int64_t V)
+{
+    if (!x.is_cuda()) raise(PyExc_ValueError, "libgdn takes device tensors (%s)", name);
+    if (x.sizes() != at::IntArrayRef({B, K, V})) raise(PyExc_ValueError, "%s must be [B][K][V]", name);
+    if (x.numel() == 0 || x.is_contiguous()) return V;
+    const int64_t s = K > 1 ? x.stride(1) : B > 1 ? x.stride(0) : V;
+    if ((V > 1 && x.stride(2) != 1) || (B > 1 && x.stride(0) != K * s) || s < V)
+        raise(PyExc_ValueError, "%s must have dense, evenly spaced rows", name);
+    return s;
+}
+
+int do_logits(PyObject* const* a, Py_ssize_t n)
+{
+    want(n, 17);  // lib stream logits out best history history_lens history_start tokens parent count params bias_ids
+                  // bias_values mask noise workspace
+    const Lib& lib = lib_of(a[0]);
+    const at::Tensor& x = tensor(a[2], "logits");
+    if (x.dim() != 3) raise(PyExc_ValueError, "logits must be [B][K][V]");
+    const int64_t B = x.size(0), K = x.size(1), V = x.size(2);
+    const long long xs = row_stride(x, "logits", B, K, V);
+    const int dtype = dtype_of(x, "logits");
+    void* out = nullptr;
+    long long os = 0;
+    int out_dtype = dtype;
+    if (a[3] != Py_None) {
+        const at::Tensor& o = tensor(a[3], "out");
+        os = row_stride(o, "out", B, K, V);
+        out_dtype = dtype_of(o, "out");
+        out = o.data_ptr();
+    }
+    int64_t capacity = 0, n_bias = 0;
+    if (a[5] != Py_None) {
+        const at::Tensor& h = dense(a[5], "history");
+        if (h.dim() != 2) raise(PyExc_ValueError, "history must be [B][capacity]");
+        capacity = h.size(1);
+        if (a[6] == Py_None) raise(PyExc_ValueError, "history needs history_lens");
+    }
+    if (a[12] != Py_None) {
+        const at::Tensor& i = dense(a[12], "bias_ids");
+        if (i.dim() != 2) raise(PyExc_ValueError, "bias_ids must be [B][n]");
+        n_bias = i.size(1);
+        if (a[13] == Py_None) raise(PyExc_ValueError, "bias_ids needs bias_values");
+    }
+    void* work = nullptr;
+    size_t work_bytes = 0;
+    if (a[16] != Py_None) {
+        const at::Tensor& w = dense(a[16], "workspace");
+        work = w.data_ptr(), work_bytes = w.nbytes();
+    } else if (a[4] != Py_None) {
+        raise(PyExc_ValueError, "best needs a workspace (logits_workspace)");
+    }
+    const Launch where(a[1], a[2]);
+    return lib.logits_adjust(
+        x.data_ptr(), xs, out, os, ints(a[4], "best", {B, K}, true), ints(a[5], "history", {B, capacity}, true),
+        ints(a[6], "history_lens", {B}, true), ints(a[7], "history_start", {B}, true), small(capacity, "capacity"),
+        ints(a[8], "tokens", {B, K}, true), ints(a[9], "parent", {B, K}, true), ints(a[10], "count", {B}, true),
+        floats(a[11], "params", {B, 4}, true), ints(a[12], "bias_ids", {B, n_bias}, true),
+        floats(a[13], "bias_values", {B, n_bias}, true), small(n_bias, "n_bias"),
+        reinterpret_cast<uint32_t*>(ints(a[14], "mask", {B, K, (V + 31) / 32}, true)),
+        floats(a[15], "noise", {B, K, V}, true), work, work_bytes, small(B, "B"), small(K, "K"), small(V, "V"), dtype,
+        out_dtype, where.stream);
+}
+
+int do_accept(PyObject* const* a, Py_ssize_t n)
+{
+    want(n, 12);  // lib stream target tokens node next parent count root history lens lens_out
+    const Lib& lib = lib_of(a[0]);
+    const at::Tensor& t = dense(a[2], "target");
+    if (t.dim() != 2) raise(PyExc_ValueError, "target must be [B][K]");
+    const int64_t B = t.size(0), K = t.size(1);
+    int64_t capacity = 0;
+    if (a[9] != Py_None) {
+        const at::Tensor& h = dense(a[9], "history");
+        if (h.dim() != 2) raise(PyExc_ValueError, "history must be [B][capacity]");
+        capacity = h.size(1);
+    }
+    const Launch where(a[1], a[2]);
+    return lib.accept_tree(ints(a[2], "target", {B, K}), ints(a[3], "tokens", {B, K}), ints(a[6], "parent", {B, K}, true),
+                           ints(a[7], "count", {B}, true), ints(a[8], "root", {B}, true), ints(a[4], "node", {B}),
+                           ints(a[5], "next", {B}), ints(a[9], "history", {B, capacity}, true),
+                           ints(a[10], "lens", {B}, true), ints(a[11], "lens_out", {B}, true),
+                           small(capacity, "capacity"), small(B, "B"), small(K, "K"), where.stream);
+}
+
 // no C++ exception leaves the extension
 template <int (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
@@ -402,9 +636,18 @@ PyMethodDef methods[] = {
     ENTRY("kv_compact", do_compact, "lib stream table ref pool table_out ref_out workspace"),
     ENTRY("kv_copy", do_copy, "lib stream src dst pool"),
     ENTRY("attn_verify", do_attn, "lib stream q k_pages v_pages lens count parent table o lse workspace prefix scale"),
+    ENTRY("rope", do_rope, "lib stream x y freqs pos lens parent count interleaved mscale"),
+    ENTRY("qk_norm_rope", do_qk_norm_rope,
+          "lib stream q k wq wk freqs q_out k_out pos lens parent count eps interleaved mscale"),
+    ENTRY("kv_append_rope", do_append_rope,
+          "lib stream k v k_pages v_pages lens table freqs q q_out wq wk pos parent count eps interleaved mscale"),
+    ENTRY("logits_adjust", do_logits,
+          "lib stream logits out best history history_lens history_start tokens parent count params bias_ids "
+          "bias_values mask noise workspace"),
+    ENTRY("accept_tree", do_accept, "lib stream target tokens node next parent count root history lens lens_out"),
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_binding", "marshalling of the libgdn cache and attention calls", -1,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_binding", "marshalling of the libgdn cache and window calls", -1,
                       methods};
 
 }  // namespace

@@ -1,5 +1,6 @@
 """Binding of libgdn.so (include/gdn.h) for torch device tensors, by ctypes (the
-cache and attention calls by a compiled extension, csrc/gdn_binding.cpp).
+cache and attention calls and those around them by a compiled extension,
+csrc/gdn_binding.cpp).
 
 Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  Each function takes torch tensors that already live on the GPU,
@@ -24,12 +25,16 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libgdn_debug.so")
 
 GDN_OK, GDN_EINVAL, GDN_EUNSUPPORTED, GDN_EHIP = 0, -1, -2, -3
 GDN_F32, GDN_BF16 = 0, 1
+GDN_ROPE_HALVES, GDN_ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = ("plain", "linear", "ntk", "bands", "yarn")   # gdn_rope_scaling, in order
 EXPORTS = ("gdn_version", "gdn_last_error", "gdn_conv_step", "gdn_verify", "gdn_rollback", "gdn_prefill_chunked",
            "gdn_rollback_conv_step", "gdn_conv_step_ex", "gdn_verify_ex", "gdn_rollback_ex", "gdn_replay",
            "gdn_conv_tree", "gdn_verify_tree", "gdn_rollback_tree", "gdn_verify_step",
            "gdn_debug_clamped_accepts", "gdn_verify_tree_step",
            "gdn_kv_reserve", "gdn_kv_append", "gdn_kv_rollback_tree", "gdn_kv_free", "gdn_kv_fork",
-           "gdn_kv_compact", "gdn_kv_compact_workspace", "gdn_kv_copy", "gdn_attn_verify", "gdn_attn_workspace")
+           "gdn_kv_compact", "gdn_kv_compact_workspace", "gdn_kv_copy", "gdn_attn_verify", "gdn_attn_workspace",
+           "gdn_rope_freqs", "gdn_rope", "gdn_qk_norm_rope", "gdn_kv_append_rope", "gdn_logits_adjust",
+           "gdn_logits_workspace", "gdn_accept_tree")
 
 
 class GdnError(RuntimeError):
@@ -113,6 +118,15 @@ def open_library(path: str):
     lib.gdn_kv_copy.argtypes = [P, P, P, I, I, I, I, I, I, I, P]
     lib.gdn_attn_verify.argtypes = [P, L, P, P, P, P, P, P, P, P, P, Z, I, I, I, I, I, I, I, I, I, F, I, P]
     lib.gdn_attn_workspace.argtypes = [I, I, I, I, I, I, I, I, I, P]
+    N = ctypes.c_double
+    lib.gdn_rope_freqs.argtypes = [I, N, I, N, N, N, N, P, P]
+    lib.gdn_rope.argtypes = [P, P, P, P, P, P, P, P, P, I, I, F, I, I, I, I, I, P]
+    lib.gdn_qk_norm_rope.argtypes = [P, P, P, P, P, P, F, P, P, P, P, P, P, P, I, I, F, I, I, I, I, I, I, P]
+    lib.gdn_kv_append_rope.argtypes = [P, P, P, P, P, P, P, P, F, P, P, P, P, P, P, P, P, P, I, I, F,
+                                       I, I, I, I, I, I, I, I, I, P]
+    lib.gdn_logits_adjust.argtypes = [P, L, P, L, P, P, P, P, I, P, P, P, P, P, P, I, P, P, P, Z, I, I, I, I, I, P]
+    lib.gdn_logits_workspace.argtypes = [I, I, I, P]
+    lib.gdn_accept_tree.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, P]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_char_p if name == "gdn_last_error" else I
     return lib
@@ -419,3 +433,64 @@ def attn_verify(q, k_pages, v_pages, lens, table, o, prefix_len=0, count=None, p
     whose pages every sequence that long shares; scale None: D ** -0.5; workspace: attn_workspace(...)."""
     _check(_B().attn_verify(_L()._handle, _raw(stream), q, k_pages, v_pages, lens, count, parent, table, o, lse,
                             workspace, prefix_len, scale))
+
+
+# ---------------------------------------------------------------- positions and norms, logits and acceptance
+def rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, low=1.0, high=32.0, original=0.0, device="cuda"):
+    """gdn_rope_freqs: the rot/2 frequencies as a float64 tensor on `device`, and mscale; scaling one of
+    ROPE_SCALINGS."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    freqs, mscale = (ctypes.c_double * max(1, int(rot) // 2))(), ctypes.c_float(0.0)
+    _check(_L().gdn_rope_freqs(int(rot), float(base), ROPE_SCALINGS.index(scaling), float(factor), float(low), float(high),
+                               float(original), freqs, ctypes.byref(mscale)))
+    return torch.tensor(list(freqs), dtype=torch.float64, device=device), mscale.value
+
+
+def rope(x, y, freqs, pos=None, lens=None, parent=None, count=None, interleaved=False, mscale=1.0, stream=None):
+    """gdn_rope: y [B][K][H][D] <- x turned by the positions pos [B][K], or lens [B] (None: 0) + the token's place in a
+    chain or its depth in the tree parent [B][K]; freqs [rot/2] float64.  x and y may be strided (dense heads), y may
+    be x."""
+    _check(_B().rope(_L()._handle, _raw(stream), x, y, freqs, pos, lens, parent, count, interleaved, mscale))
+
+
+def qk_norm_rope(q, k, wq, wk, freqs, q_out, k_out, pos=None, lens=None, parent=None, count=None, eps=1e-6,
+                 interleaved=False, mscale=1.0, stream=None):
+    """gdn_qk_norm_rope: q [B][K][Hq][D] and k [B][K][Hk][D] (strided, dense heads), each head RMS-normed with wq, wk
+    [D] f32 and turned (freqs None: the norm alone), into q_out and k_out (dense)."""
+    _check(_B().qk_norm_rope(_L()._handle, _raw(stream), q, k, wq, wk, freqs, q_out, k_out, pos, lens, parent, count, eps,
+                             interleaved, mscale))
+
+
+def kv_append_rope(k, v, k_pages, v_pages, lens, table, freqs, q=None, q_out=None, wq=None, wk=None, pos=None, parent=None,
+                   count=None, eps=1e-6, interleaved=False, mscale=1.0, stream=None):
+    """gdn_kv_append_rope: kv_append with k [B][K][Hkv][D] normed (wk; None: not) and turned on the way, and in the same
+    launch q [B][K][Hq][D] normed (wq) and turned into q_out (dense); freqs None: no turn."""
+    _check(_B().kv_append_rope(_L()._handle, _raw(stream), k, v, k_pages, v_pages, lens, table, freqs, q, q_out, wq, wk, pos,
+                               parent, count, eps, interleaved, mscale))
+
+
+def logits_workspace(logits):
+    """The workspace of logits_adjust for logits [B][K][V] (one for each stream that calls it)."""
+    return torch.empty(_bytes(_L().gdn_logits_workspace, *logits.shape), dtype=torch.uint8, device=logits.device)
+
+
+def logits_adjust(logits, out=None, best=None, history=None, history_lens=None, history_start=None, tokens=None,
+                  parent=None, count=None, params=None, bias_ids=None, bias_values=None, mask=None, noise=None,
+                  workspace=None, stream=None):
+    """gdn_logits_adjust: logits [B][K][V] (rows may be slices of wider ones) with penalties for the tokens of history
+    [B][capacity] and of the path through the window's tokens [B][K], biases, a mask [B][K][ceil(V/32)] int32 and a
+    temperature, into out (may be logits) and their best tokens (plus noise [B][K][V] f32) into best [B][K] int32.
+    params [B][4] f32: repetition, presence, frequency, temperature; bias_ids int32 and bias_values f32 [B][n];
+    workspace: logits_workspace(logits), needed with best."""
+    _check(_B().logits_adjust(_L()._handle, _raw(stream), logits, out, best, history, history_lens, history_start, tokens,
+                              parent, count, params, bias_ids, bias_values, mask, noise, workspace))
+
+
+def accept_tree(target, tokens, node, next, parent=None, count=None, root=None, history=None, lens=None, lens_out=None,
+                stream=None):
+    """gdn_accept_tree: node [B] <- the deepest node of the window tokens [B][K] whose path target [B][K] confirms
+    (-1: none), next [B] <- the token after it; with history [B][capacity], lens and lens_out [B] the path's tokens
+    are appended.  All int32."""
+    _check(_B().accept_tree(_L()._handle, _raw(stream), target, tokens, node, next, parent, count, root, history, lens,
+                            lens_out))
