@@ -691,11 +691,11 @@ int gdn_kv_append_rope(const void *q, const long long *q_strides, const void *k,
  *   with s how often v stands in history[b][0 .. history_lens[b]) or on the path
  *   root..t of tokens, and n how often from history_start[b] on (0 where NULL; the
  *   path counts in both):
- *   s > 0: x <- x > 0 ? x / repetition : x * repetition
- *   n > 0: x <- x - frequency * n, then x - presence
+ *   s > 0: x <- x * (x > 0 ? 1 / repetition : repetition)
+ *   n > 0: x <- x - (frequency * n + presence)
  *   x <- x + bias of v;  x <- -inf where v is not allowed;
- *   x <- x / temperature (where that is above 0)
- * each step rounded once in fp32.  out (NULL: not wanted) receives x in out_dtype, best (NULL:
+ *   x <- x * (1 / temperature) (where that is 2^-126 or more)
+ * each operation, the reciprocals too, rounded once in fp32.  out (NULL: not wanted) receives x in out_dtype, best (NULL:
  * not wanted) the token with the largest x + noise, the lowest of equal ones, -1 where
  * every one is -inf (NaN is never the best).
  *   logits [B][K][V] dtype, row (b, t) starting logits_stride elements after

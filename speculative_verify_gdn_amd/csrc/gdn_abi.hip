@@ -1144,7 +1144,7 @@ int gdn_logits_workspace(int B, int K, int V, size_t* bytes)
     int rc = check_logits(fn, B, K, V);
     if (rc) return rc;
     REQUIRE(bytes, GDN_EINVAL, "%s: null bytes", fn);
-    *bytes = (size_t)B * K * gdn::logits_slices(B, V) * 8;
+    *bytes = (size_t)B * K * gdn::logits_slices(V) * 8;
     return ok();
 }
 
@@ -1181,7 +1181,7 @@ int gdn_logits_adjust(const void* logits, long long logits_stride, void* out, lo
     REQUIRE(!noise || best, GDN_EINVAL, "%s: noise is for finding best", fn);
     size_t need = 0;
     if (best) {
-        need = rows * gdn::logits_slices(B, V) * 8;
+        need = rows * gdn::logits_slices(V) * 8;
         REQUIRE(workspace && workspace_bytes >= need, GDN_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn,
                 workspace ? workspace_bytes : (size_t)0, need);
     }
@@ -1201,7 +1201,7 @@ int gdn_logits_adjust(const void* logits, long long logits_stride, void* out, lo
     a.x = logits, a.out = out, a.x_stride = (size_t)logits_stride, a.out_stride = out ? (size_t)out_stride : 0;
     a.best = best, a.history = history, a.history_lens = history_lens, a.history_start = history_start;
     a.tokens = tokens, a.parent = parent, a.count = count, a.params = params, a.bias_ids = bias_ids;
-    a.bias_values = bias_values, a.mask = mask, a.noise = noise, a.work = static_cast<int2*>(workspace);
+    a.bias_values = bias_values, a.mask = mask, a.noise = noise, a.work = static_cast<unsigned long long*>(workspace);
     a.B = B, a.K = K, a.V = V, a.capacity = capacity, a.n_bias = n_bias;
     return launch_status(gdn::launch_logits(a, dtype == GDN_BF16, out_dtype == GDN_BF16, (hipStream_t)stream), fn);
 }

@@ -6,16 +6,18 @@
 // A logit x of token v behind node t becomes, with n how often v stands in the
 // text since `start` and on the path to t, and seen if it stands in the text at all
 // or on that path:
-//   seen: x > 0 ? x / repetition : x * repetition;   x - frequency n;
-//   n > 0: x - presence;   x + bias;   not allowed: -inf;   x / temperature
+//   seen: x (x > 0 ? 1 / repetition : repetition);   n > 0: x - (frequency n + presence);
+//   x + bias;   not allowed: -inf;   x (1 / temperature)
 // One read of the logits and one write: memory bound, if the counts cost
-// little.  So a workgroup takes a slice of the vocabulary for the rows of one
-// sequence: it walks the history once, counts the tokens of its slice in LDS, and
-// marks them in a bit map.  Eight logits whose byte of that map is 0, which is nearly
-// all of them, skip the penalties (two correctly rounded divisions among
-// them); the others take the long way.
+// little.  So a workgroup takes a slice of the vocabulary for some rows of one
+// sequence: it walks the text once, counts the tokens of its slice in LDS (16
+// bits each, 16 KB for 8192 tokens), and then streams.  Eight logits whose eight counts are 0,
+// which is nearly all of them, take the short way.
 // Every operation is one rounding of 32 bits in the order above, so that equal
 // logits stay equal and the best is the lowest of them.
+//
+// Measured apart: with the logits of the counted tokens left to a second kernel (a hash table
+// a sequence), that kernel's scattered reads and writes took 13 us behind a window of 32 x 8 rows of 131072.
 #include "gdn_device.h"
 #include "gdn_window_internal.h"
 
@@ -24,31 +26,63 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kSliceMax = 4096;            // tokens of the vocabulary of a workgroup
-constexpr uint32_t kSeen = 0x80000000u;    // stands in the text before `start`
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 // 16 bytes at an element's own alignment (rows of an odd length start anywhere)
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
+// eight values as they lie in memory
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, size_t at, float* f)
-{
-    if constexpr (BF16) {
-        const u32x4_any_t u = *reinterpret_cast<const u32x4_any_t*>(static_cast<const uint16_t*>(base) + at);
+struct Raw8 {
+    u32x4_any_t u[BF16 ? 1 : 2];
+
+    __device__ __forceinline__ void load(const void* row, int at)
+    {
+        const char* p = static_cast<const char*>(row) + (size_t)at * (BF16 ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(u[i]), f[2 * i + 1] = bf16_hi(u[i]);
-    } else {
-        const u32x4_any_t* p = reinterpret_cast<const u32x4_any_t*>(static_cast<const float*>(base) + at);
-        const u32x4_any_t u = p[0], v = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(u[i]), f[4 + i] = __uint_as_float(v[i]);
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) u[i] = reinterpret_cast<const u32x4_any_t*>(p)[i];
     }
+    // of a row of fewer than eight: the last one again and again
+    __device__ __forceinline__ void load_few(const void* row, int V)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int at = min(e, V - 1);
+            if constexpr (BF16) {
+                const uint32_t h = static_cast<const uint16_t*>(row)[at];
+                u[0][e >> 1] = e & 1 ? u[0][e >> 1] | h << 16 : h;
+            } else {
+                u[e >> 2][e & 3] = static_cast<const uint32_t*>(row)[at];
+            }
+        }
+    }
+    __device__ __forceinline__ void floats(float* f) const
+    {
+        if constexpr (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(u[0][i]), f[2 * i + 1] = bf16_hi(u[0][i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i >> 2][i & 3]);
+        }
+    }
+};
+
+// the last m < 8 of eight to the front
+__device__ __forceinline__ void to_front(float* f, int m)
+{
+#pragma unroll
+    for (int d = 4; d; d >>= 1)
+        if ((8 - m) & d) {
+#pragma unroll
+            for (int e = 0; e + d < 8; ++e) f[e] = f[e + d];
+        }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void* base, size_t at, const float* f)
+__device__ __forceinline__ void store8(void* row, int at, const float* f)
 {
+    char* p = static_cast<char*>(row) + (size_t)at * (BF16 ? 2 : 4);
     u32x4_any_t u;
     if constexpr (BF16) {
 #pragma unroll
@@ -56,40 +90,66 @@ __device__ __forceinline__ void store8(void* base, size_t at, const float* f)
             const bf16x2_t h = {(__bf16)f[2 * i], (__bf16)f[2 * i + 1]};
             u[i] = __builtin_bit_cast(uint32_t, h);
         }
-        *reinterpret_cast<u32x4_any_t*>(static_cast<uint16_t*>(base) + at) = u;
+        __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any_t*>(p));
     } else {
-        u32x4_any_t* p = reinterpret_cast<u32x4_any_t*>(static_cast<float*>(base) + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[i]);
-        p[0] = u;
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[4 + i]);
-        p[1] = u;
+            for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[4 * h + i]);
+            __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any_t*>(p) + h);
+        }
     }
 }
 
-// the larger score, the lower token where they are equal; no token: INT_MAX
-struct Best {
-    float score;
-    int token;
-
-    __device__ __forceinline__ void take(float s, int t)
-    {
-        if (s > score || (s == score && t < token)) score = s, token = t;
-    }
-};
-
-__device__ __forceinline__ Best none() { return Best{-__builtin_huge_valf(), 0x7fffffff}; }
-
-__device__ __forceinline__ Best wave_best(Best b)
+// the largest over a wave (NaN is passed over)
+__device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const float s = __shfl_xor(b.score, d, 64);
-        const int t = __shfl_xor(b.token, d, 64);
-        b.take(s, t);
-    }
-    return b;
+    v = fmaxf(v, dpp_mov<kDppQuadXor1>(v));
+    v = fmaxf(v, dpp_mov<kDppQuadXor2>(v));
+    v = fmaxf(v, dpp_mov<kDppRowHalfMirror>(v));
+    v = fmaxf(v, dpp_mov<kDppRowMirror>(v));
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+
+// A score and its token as one number: the larger score is the larger number, the lower token where they are equal; 0
+// is none.  (Scores that are NaN or -inf have none.)
+__device__ __forceinline__ unsigned long long key_of(float score, int token)
+{
+    const uint32_t u = __float_as_uint(score + 0.0f);   // (-0 is 0)
+    const uint32_t up = u & 0x80000000u ? ~u : u | 0x80000000u;
+    return (unsigned long long)up << 32 | (0xffffffffu - (uint32_t)token);
+}
+
+__device__ __forceinline__ int token_of(unsigned long long key)
+{
+    return key ? (int)(0xffffffffu - (uint32_t)key) : -1;
+}
+
+// the smallest over a wave
+__device__ __forceinline__ int wave_min(int v)
+{
+    auto with = [&](int u) { v = min(v, u); };
+    with(__builtin_amdgcn_update_dpp(0, v, kDppQuadXor1, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, v, kDppQuadXor2, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, v, kDppRowHalfMirror, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, v, kDppRowMirror, 0xF, 0xF, false));
+    with(__shfl_xor(v, 16, 64));
+    with(__shfl_xor(v, 32, 64));
+    return v;
+}
+
+// the largest over a wave of numbers without a sign
+__device__ __forceinline__ uint32_t wave_most(uint32_t v)
+{
+    auto with = [&](int u) { v = max(v, (uint32_t)u); };
+    with(__builtin_amdgcn_update_dpp(0, (int)v, kDppQuadXor1, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, (int)v, kDppQuadXor2, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, (int)v, kDppRowHalfMirror, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(0, (int)v, kDppRowMirror, 0xF, 0xF, false));
+    with(__shfl_xor((int)v, 16, 64));
+    with(__shfl_xor((int)v, 32, 64));
+    return v;
 }
 
 // the nodes on the path root..i as a bit mask, in lane i, by doubling (a whole wave)
@@ -102,8 +162,7 @@ __device__ __forceinline__ unsigned long long node_paths(const int32_t* parent, 
         up = p >= 0 && p < lane ? p : -1;
     }
     unsigned long long path = 1ull << lane;
-#pragma unroll
-    for (int d = 1; d < kKvWindowMax; d <<= 1) {
+    for (int d = 1; d < N; d <<= 1) {
         const unsigned long long more = __shfl(path, max(up, 0), 64);
         const int far = __shfl(up, max(up, 0), 64);
         if (up >= 0) {
@@ -119,159 +178,349 @@ __device__ __forceinline__ int clamp_count(const int32_t* count, int b, int K)
     return count ? min(max(count[b], 0), K) : K;
 }
 
-template <bool XBF16, bool OBF16>
+// What a thread reads of a row: eight logits, their noise and whether they are allowed.  Eight that would pass the
+// row's end are its last eight instead (to_front): no load depends on a lane's place.
+template <bool XBF16, bool NOISE>
+struct Row8 {
+    Raw8<XBF16> x;
+    Raw8<false> z;
+    uint32_t allow;
+};
+
+// where a row starts: its logits, its noise and its mask
+template <bool XBF16, bool NOISE>
+struct Rows {
+    const char* x;
+    const float* z;
+    const uint8_t* allow;
+    int V, allow_bytes;
+    size_t x_step;
+
+    __device__ __forceinline__ Rows(const LogitsArgs& a, size_t row)
+        : V(a.V), allow_bytes((a.V + 31) / 32 * 4), x_step(a.x_stride * (XBF16 ? 2 : 4))
+    {
+        x = static_cast<const char*>(a.x) + row * x_step;
+        z = NOISE ? a.noise + row * a.V : nullptr;
+        allow = a.mask ? reinterpret_cast<const uint8_t*>(a.mask) + row * allow_bytes : nullptr;
+    }
+    __device__ __forceinline__ void next()
+    {
+        x += x_step;
+        if constexpr (NOISE) z += V;
+        if (allow) allow += allow_bytes;
+    }
+    __device__ __forceinline__ void load(Row8<XBF16, NOISE>& r, int v) const
+    {
+        if (V >= 8) {
+            r.x.load(x, min(v, V - 8));
+            if constexpr (NOISE) r.z.load(z, min(v, V - 8));
+        } else {
+            r.x.load_few(x, V);
+            if constexpr (NOISE) r.z.load_few(z, V);
+        }
+        if (allow) r.allow = allow[min(v >> 3, allow_bytes - 1)];
+    }
+};
+
+struct Params {
+    float rep, less, presence, frequency, cool;   // less, cool: the reciprocals of repetition and temperature
+
+    __device__ __forceinline__ Params(const float* p, int b)
+        : rep(1.0f), less(1.0f), presence(0.0f), frequency(0.0f), cool(1.0f)
+    {
+        if (!p) return;
+        p += (size_t)b * 4;
+        rep = p[0], less = 1.0f / rep, presence = p[1], frequency = p[2];
+        if (p[3] >= 0x1p-126f) cool = 1.0f / p[3];
+    }
+};
+
+// f where bit e of `bits` is set, -inf elsewhere
+__device__ __forceinline__ float only(float f, uint32_t bits, int e)
+{
+    const int m = __builtin_amdgcn_sbfe((int)bits, e, 1);
+    return __int_as_float(__builtin_amdgcn_bitop3_b32(__float_as_int(f), (int)0xff800000, m, 0xe4));   // m ? f : -inf
+}
+
+// What is known of the tokens of a slice, in LDS.  Narrow: 16 bits a token (14 of the count, one for a bias, one for
+// a place in the text before `start`), and a list of the slice's biases.  Wide: 32 bits a token, and a bias's
+// entry for each.
+constexpr int kNarrowText = 16000;   // the longest text (with a window's drafts below 2^14)
+constexpr int kNarrowBias = kThreads;
+
+template <bool WIDE, int TOKENS>
+struct Known;
+
+template <int TOKENS>
+struct Known<false, TOKENS> {
+    static constexpr uint32_t kCount = 0x3fffu, kBias = 0x4000u, kSeen = 0x8000u, kAnyBias = 0x40004000u;
+    uint32_t cnt[TOKENS / 2];
+    uint16_t bias_token[kNarrowBias];
+    float bias_value[kNarrowBias];
+    int biases[kWaves];
+
+    __device__ __forceinline__ void clear()
+    {
+        for (int i = threadIdx.x; i < TOKENS / 8; i += kThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void add(int u, int n) { atomicAdd(&cnt[u >> 1], (uint32_t)n << 16 * (u & 1)); }
+    __device__ __forceinline__ void mark(int u, uint32_t bit) { atomicOr(&cnt[u >> 1], bit << 16 * (u & 1)); }
+    // the eight from k on; returns their bits together
+    __device__ __forceinline__ uint32_t get8(int k, uint32_t* c) const
+    {
+        const uint4 w = *reinterpret_cast<const uint4*>(cnt + (k >> 1));
+        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[2 * i] = p[i] & 0xffffu, c[2 * i + 1] = p[i] >> 16;
+        return w.x | w.y | w.z | w.w;
+    }
+    // the biases of the slice in their order (a thread an entry; every thread calls it, one barrier inside)
+    __device__ __forceinline__ int list_biases(const LogitsArgs& a, int b, int v0, int nv)
+    {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+        const size_t at = (size_t)b * a.n_bias + tid;
+        const uint32_t u = tid < a.n_bias ? (uint32_t)a.bias_ids[at] - (uint32_t)v0 : 0xffffffffu;
+        const bool mine = u < (uint32_t)nv;
+        const float w = mine ? a.bias_values[at] : 0.0f;
+        const unsigned long long which = __ballot(mine);
+        if (lane == 0) biases[wave] = (int)__popcll(which);
+        __syncthreads();
+        int base = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            base += i < wave ? biases[i] : 0;
+            all += biases[i];
+        }
+        if (mine) {
+            base += (int)__popcll(which & ((1ull << lane) - 1));
+            bias_token[base] = (uint16_t)u;
+            bias_value[base] = w;
+            mark(u, kBias);
+        }
+        return all;
+    }
+    __device__ __forceinline__ float bias_of(const LogitsArgs&, int, int u, int listed) const
+    {
+        int i = listed - 1;   // (a token named twice: its last entry)
+        while (bias_token[i] != u) --i;
+        return bias_value[i];
+    }
+};
+
+template <int TOKENS>
+struct Known<true, TOKENS> {
+    static constexpr uint32_t kCount = 0x3fffffffu, kBias = 0x40000000u, kSeen = 0x80000000u, kAnyBias = kBias;
+    uint32_t cnt[TOKENS];
+    int entry[TOKENS];
+
+    __device__ __forceinline__ void clear()
+    {
+        for (int i = threadIdx.x; i < TOKENS; i += kThreads) cnt[i] = 0, entry[i] = -1;
+    }
+    __device__ __forceinline__ void add(int u, int n) { atomicAdd(&cnt[u], (uint32_t)n); }
+    __device__ __forceinline__ void mark(int u, uint32_t bit) { atomicOr(&cnt[u], bit); }
+    __device__ __forceinline__ uint32_t get8(int k, uint32_t* c) const
+    {
+        const uint4 w = *reinterpret_cast<const uint4*>(cnt + k), z = *reinterpret_cast<const uint4*>(cnt + k + 4);
+        c[0] = w.x, c[1] = w.y, c[2] = w.z, c[3] = w.w, c[4] = z.x, c[5] = z.y, c[6] = z.z, c[7] = z.w;
+        return w.x | w.y | w.z | w.w | z.x | z.y | z.z | z.w;
+    }
+    __device__ __forceinline__ int list_biases(const LogitsArgs& a, int b, int v0, int nv)
+    {
+        const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
+        for (int i = threadIdx.x; i < a.n_bias; i += kThreads) {
+            const uint32_t u = (uint32_t)ids[i] - (uint32_t)v0;
+            if (u < (uint32_t)nv) {
+                atomicMax(&entry[u], i);   // (a token named twice: its last entry)
+                mark(u, kBias);
+            }
+        }
+        return 0;
+    }
+    __device__ __forceinline__ float bias_of(const LogitsArgs& a, int b, int u, int) const
+    {
+        return a.bias_values[(size_t)b * a.n_bias + entry[u]];
+    }
+};
+
+// 2048 VECTORS tokens of the vocabulary, for some rows of one sequence: a thread has eight of each 2048.
+template <int VECTORS, bool WIDE, bool XBF16, bool OBF16, bool NOISE>
 __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
 {
-    extern __shared__ uint32_t lds[];   // counts, their bit map, and where there are biases their entries
-    __shared__ unsigned long long paths[kKvWindowMax], inside_s;
+    constexpr int kTokens = 8 * kThreads * VECTORS;
+    using K = Known<WIDE, kTokens>;
+    __shared__ alignas(16) K known;
+    __shared__ unsigned long long best[kKvWindowMax], paths[kKvWindowMax], inside_s;
     __shared__ int draft[kKvWindowMax];
-    __shared__ Best part[kKvWindowMax][kWaves];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int groups = (a.K + a.rows - 1) / a.rows;
-    const int b = blockIdx.y / groups, t0 = (blockIdx.y - b * groups) * a.rows;
-    const int t1 = min(t0 + a.rows, clamp_count(a.count, b, a.K));
+    // Rows g * a.rows on of sequence b.  Windows differ in length, so the later g are the emptier; a CU gets workgroups that
+    // lie a fixed number apart, and with the sequences shifted from one g to the next these are of different sequences.
+    const int g = blockIdx.y / a.B, b = (blockIdx.y - g * a.B + 5 * g) % a.B;
+    const int t0 = g * a.rows, t1 = min(t0 + a.rows, clamp_count(a.count, b, a.K));
     if (t0 >= t1) return;
-    const int v0 = blockIdx.x * a.slice, nv = min(a.slice, a.V - v0);
-    uint32_t *cnt = lds, *bits = lds + a.slice;
-    int* entry = reinterpret_cast<int*>(bits + a.slice / 32);
-    const bool counted = a.params != nullptr, biased = a.n_bias > 0;
+    const size_t row0 = (size_t)b * a.K;
+    const int v0 = blockIdx.x * kTokens, nv = min(kTokens, a.V - v0);
 
-    float rep = 1.0f, presence = 0.0f, frequency = 0.0f, temp = 1.0f;
-    if (counted) {
-        const float* p = a.params + (size_t)b * 4;
-        rep = p[0], presence = p[1], frequency = p[2], temp = p[3];
-        if (!(temp > 0.0f)) temp = 1.0f;
-    }
-
-    if (counted)
-        for (int i = tid; i < a.slice; i += kThreads) cnt[i] = 0;
-    if (biased)
-        for (int i = tid; i < a.slice; i += kThreads) entry[i] = -1;
-    for (int i = tid; i < a.slice / 32; i += kThreads) bits[i] = 0;
-    if (wave == 0) {
-        // the path to each node, and the drafted tokens of this slice
-        const bool drafts = counted && a.tokens;
-        unsigned long long path = 0;
-        if (drafts) path = node_paths(a.parent ? a.parent + (size_t)b * a.K : nullptr, a.K);
-        int u = -1;
-        if (drafts && lane < a.K) {
-            const int d = a.tokens[(size_t)b * a.K + lane];
-            if (d >= v0 && d - v0 < nv) u = d - v0;
+    // the first two vectors of eight are on their way while the text is counted, later ones two ahead
+    const int vectors = (nv + 8 * kThreads - 1) / (8 * kThreads);
+    Row8<XBF16, NOISE> even, odd;
+    Rows<XBF16, NOISE> ahead(a, row0 + t0);
+    int ahead_t = t0, ahead_j = 0;
+    auto load = [&](Row8<XBF16, NOISE>& r) {
+        if (ahead_t < t1) ahead.load(r, v0 + (ahead_j * kThreads + tid) * 8);
+        if (++ahead_j == vectors) {
+            ahead_j = 0;
+            ++ahead_t;
+            ahead.next();
         }
-        paths[lane] = path;
-        draft[lane] = u;
-        const unsigned long long inside = __ballot(u >= 0);
-        if (lane == 0) inside_s = inside;
-    }
+    };
+    load(even);
+    load(odd);
+
+    const Params p(a.params, b);
+    const bool marks = a.marks;
+    unsigned long long inside = 0;
+    int listed = 0;
+    if (tid < kKvWindowMax) best[tid] = 0;
+    if (marks) known.clear();
     __syncthreads();
-    if (counted && a.history) {
-        const int32_t* h = a.history + (size_t)b * a.capacity;
-        const int len = min(max(a.history_lens[b], 0), a.capacity);
-        const int start = a.history_start ? a.history_start[b] : 0;
-#pragma unroll 4
-        for (int i = tid; i < len; i += kThreads) {
-            const int u = h[i] - v0;
-            if ((unsigned)u < (unsigned)nv) {
-                if (i >= start) atomicAdd(&cnt[u], 1u);
-                else atomicOr(&cnt[u], kSeen);
-                atomicOr(&bits[u >> 5], 1u << (u & 31));
+    if (marks) {
+        if (a.params && a.history) {
+            const int32_t* h = a.history + (size_t)b * a.capacity;
+            const int len = min(max(a.history_lens[b], 0), a.capacity);
+            const int start = a.history_start ? a.history_start[b] : 0;
+            auto count = [&](int token, int i) {
+                const uint32_t u = (uint32_t)token - (uint32_t)v0;
+                if (u < (uint32_t)nv) {
+                    if (i >= start) known.add(u, 1);
+                    else known.mark(u, K::kSeen);
+                }
+            };
+            const int whole = len & ~3;
+            for (int i = tid * 4; i < whole; i += kThreads * 4) {
+                const u32x4_any_t t = *reinterpret_cast<const u32x4_any_t*>(h + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) count((int)t[e], i + e);
             }
+            if (tid < len - whole) count(h[whole + tid], whole + tid);
         }
+        if (wave == kWaves - 1) {   // the path to each node, and the drafted tokens of this slice
+            const bool drafts = a.params && a.tokens;
+            const int d = drafts && lane < a.K ? a.tokens[row0 + lane] : -1;
+            const bool here = d >= v0 && d - v0 < nv;
+            paths[lane] = drafts ? node_paths(a.parent ? a.parent + row0 : nullptr, a.K) : 0;
+            draft[lane] = d - v0;
+            const unsigned long long which = __ballot(here);
+            if (lane == 0) inside_s = which;
+        }
+        if (a.n_bias > 0) listed = known.list_biases(a, b, v0, nv);
+        __syncthreads();
+        inside = inside_s;
     }
-    if (biased)
-        for (int i = tid; i < a.n_bias; i += kThreads) {
-            const int u = a.bias_ids[(size_t)b * a.n_bias + i] - v0;
-            if ((unsigned)u < (unsigned)nv) {
-                atomicMax(&entry[u], i);   // (a token named twice: its last entry)
-                atomicOr(&bits[u >> 5], 1u << (u & 31));
-            }
-        }
-    const unsigned long long inside = inside_s;
-    if (tid < 64 && (inside >> tid & 1)) atomicOr(&bits[draft[tid] >> 5], 1u << (draft[tid] & 31));
-    __syncthreads();
 
-    const unsigned char* touched = reinterpret_cast<const unsigned char*>(bits);
-    const float* bias = biased ? a.bias_values + (size_t)b * a.n_bias : nullptr;
-    for (int t = t0; t < t1; ++t) {
-        const size_t row = (size_t)b * a.K + t;
-        // the drafted tokens of this slice on the path to the node count for this row alone
+    const size_t out_step = a.out_stride * (OBF16 ? 2 : 4);
+    char* out = static_cast<char*>(a.out) + (row0 + t0) * out_step;
+    int t = t0, j = 0;
+    float top = -__builtin_huge_valf();
+    int token = 0x7fffffff;
+    // the drafted tokens of this slice on the path to the node count for its row alone
+    auto drafts_count = [&](int n) {
         const unsigned long long mine = paths[t] & inside;
-        if (mine) {
-            __syncthreads();
-            if (tid < 64 && (mine >> tid & 1)) atomicAdd(&cnt[draft[tid]], 1u);
-            __syncthreads();
-        }
-        const size_t x_at = row * a.x_stride + v0, o_at = row * a.out_stride + v0, n_at = row * a.V + v0;
-        const unsigned char* allow =
-            a.mask ? reinterpret_cast<const unsigned char*>(a.mask + row * ((a.V + 31) / 32) + (v0 >> 5)) : nullptr;
-        Best best = none();
-        for (int k = tid * 8; k < nv; k += kThreads * 8) {
-            const int m = min(8, nv - k);
-            float f[8];
-            if (m == 8) load8<XBF16>(a.x, x_at + k, f);
-            else
-                for (int e = 0; e < 8; ++e) f[e] = e < m ? load1<XBF16>(a.x, x_at + k + e) : 0.0f;
-            if (touched[k >> 3]) {
-                for (int e = 0; e < 8; ++e) {
-                    if (e >= m) break;
-                    float x = f[e];
-                    if (counted) {
-                        const uint32_t c = cnt[k + e], n = c & ~kSeen;
-                        if (c) x = x > 0.0f ? x / rep : x * rep;
-                        if (n) x = (x - frequency * (float)n) - presence;
+        if (mine == 0) return;
+        __syncthreads();
+        if (tid < 64 && (mine >> tid & 1)) known.add(draft[tid], n);
+        __syncthreads();
+    };
+    // one vector of eight: the j-th of row t
+    auto take = [&](Row8<XBF16, NOISE>& r) {
+        const int k = (j * kThreads + tid) * 8, m = min(nv - k, 8);
+        const bool whole = m == 8 || a.V < 8;
+        const uint32_t allow = a.mask ? r.allow : 0xffu;
+        float f[8], z[8];
+        r.x.floats(f);
+        if constexpr (NOISE) r.z.floats(z);
+        load(r);
+        if (j == 0 && inside) drafts_count(1);
+        if (m > 0) {
+            if (!whole) {
+                to_front(f, m);
+                if constexpr (NOISE) to_front(z, m);
+            }
+            if (marks) {
+                uint32_t c[8];
+                const uint32_t any = known.get8(k, c);
+                if (any) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t n = c[e] & K::kCount;
+                        f[e] *= c[e] & ~K::kBias ? (f[e] > 0.0f ? p.less : p.rep) : 1.0f;
+                        f[e] -= n ? p.frequency * (float)n + p.presence : 0.0f;
                     }
-                    if (biased && entry[k + e] >= 0) x += bias[entry[k + e]];
-                    f[e] = x;
+                    if (any & K::kAnyBias) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c[e] & K::kBias) f[e] += known.bias_of(a, b, k + e, listed);
+                    }
                 }
             }
-            if (allow) {
-                const unsigned char w = allow[k >> 3];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (!(w >> e & 1)) f[e] = -__builtin_huge_valf();
-            }
-            if (temp != 1.0f) {
+            for (int e = 0; e < 8; ++e) f[e] *= p.cool;
+            if (a.mask) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] /= temp;
+                for (int e = 0; e < 8; ++e) f[e] = only(f[e], allow, e);
             }
             if (a.out) {
-                if (m == 8) store8<OBF16>(a.out, o_at + k, f);
-                else
-                    for (int e = 0; e < m; ++e) store1<OBF16>(a.out, o_at + k + e, f[e]);
+                if (m == 8) {
+                    store8<OBF16>(out, v0 + k, f);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (e < m) store1<OBF16>(out, v0 + k + e, f[e]);
+                }
             }
             if (a.best) {
-                if (a.noise) {
-                    float z[8];
-                    if (m == 8) load8<false>(a.noise, n_at + k, z);
-                    else
-                        for (int e = 0; e < 8; ++e) z[e] = e < m ? a.noise[n_at + k + e] : 0.0f;
+                if constexpr (NOISE) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] += z[e];
                 }
+                if (m < 8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < m && f[e] > best.score) best = Best{f[e], v0 + k + e};
+                    for (int e = 0; e < 8; ++e) f[e] = only(f[e], 0xffu >> (8 - m), e);
+                }
+                float most = f[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) most = fmaxf(most, f[e]);
+                if (most > top) {
+                    int e = 7;
+#pragma unroll
+                    for (int i = 6; i >= 0; --i) e = f[i] == most ? i : e;
+                    top = most;
+                    token = v0 + k + e;
+                }
             }
         }
+        if (++j < vectors) return;
         if (a.best) {
-            best = wave_best(best);
-            if (lane == 0) part[t - t0][wave] = best;
+            const float most = wave_max(top);
+            const int lowest = wave_min(top == most ? token : 0x7fffffff);
+            if (lane == 0 && most > -__builtin_huge_valf()) atomicMax(&best[t - t0], key_of(most, lowest));
+            top = -__builtin_huge_valf();
         }
-        if (mine) {
-            __syncthreads();
-            if (tid < 64 && (mine >> tid & 1)) atomicSub(&cnt[draft[tid]], 1u);
-            __syncthreads();   // the next row may look at the counts without a barrier of its own
-        }
+        if (inside) drafts_count(-1);
+        j = 0;
+        ++t;
+        out += out_step;
+    };
+    for (;;) {
+        take(even);
+        if (t == t1) break;
+        take(odd);
+        if (t == t1) break;
     }
     if (a.best) {
         __syncthreads();
-        if (tid < t1 - t0) {
-            Best r = part[tid][0];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) r.take(part[tid][w].score, part[tid][w].token);
-            a.work[((size_t)b * a.K + t0 + tid) * a.slices + blockIdx.x] = make_int2(__float_as_int(r.score), r.token);
-        }
+        if (tid < t1 - t0) a.work[(row0 + t0 + tid) * a.slices + blockIdx.x] = best[tid];
     }
 }
 
@@ -281,15 +530,11 @@ __global__ __launch_bounds__(kThreads) void logits_best_kernel(LogitsArgs a)
     const long long row = (long long)blockIdx.x * kWaves + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (row >= (long long)a.B * a.K) return;
+    unsigned long long key = 0;
+    for (int i = lane; i < a.slices; i += 64) key = max(key, a.work[row * a.slices + i]);
+    const uint32_t hi = (uint32_t)(key >> 32), most = wave_most(hi), low = wave_most(hi == most ? (uint32_t)key : 0);
     const int b = (int)(row / a.K), t = (int)(row - (long long)b * a.K);
-    if (t >= clamp_count(a.count, b, a.K)) return;
-    Best best = none();
-    for (int i = lane; i < a.slices; i += 64) {
-        const int2 w = a.work[row * a.slices + i];
-        best.take(__int_as_float(w.x), w.y);
-    }
-    best = wave_best(best);
-    if (lane == 0) a.best[row] = best.token == 0x7fffffff ? -1 : best.token;
+    if (lane == 0 && t < clamp_count(a.count, b, a.K)) a.best[row] = token_of((unsigned long long)most << 32 | low);
 }
 
 // ---------------------------------------------------------------- the accepted node
@@ -335,36 +580,44 @@ __global__ __launch_bounds__(kThreads) void accept_kernel(AcceptArgs a)
 
 // The vocabulary is cut so that a launch has about four workgroups for each of the 256 CUs; a slice of 512 tokens still
 // has eight logits for each of 64 lanes.
-int slice_of(int B, int V)
+int vectors_of(int B, int V)
 {
-    int slice = kSliceMax;
-    while (slice > 512 && (long long)B * ((V + slice - 1) / slice) < 512) slice /= 2;
-    return slice;
+    return (long long)B * ((V + 8 * kThreads * 4 - 1) / (8 * kThreads * 4)) >= 256 ? 4 : 1;
+}
+
+template <int VECTORS, bool WIDE, bool XBF16, bool OBF16>
+void launch(const LogitsArgs& a, dim3 grid, hipStream_t s)
+{
+    if (a.noise) logits_kernel<VECTORS, WIDE, XBF16, OBF16, true><<<grid, dim3(kThreads), 0, s>>>(a);
+    else logits_kernel<VECTORS, WIDE, XBF16, OBF16, false><<<grid, dim3(kThreads), 0, s>>>(a);
+}
+
+template <int VECTORS, bool WIDE>
+void launch(LogitsArgs& a, bool x_bf16, bool out_bf16, hipStream_t s)
+{
+    const int slice = 8 * kThreads * VECTORS;
+    a.slices = (a.V + slice - 1) / slice;
+    const long long units = (long long)a.B * a.slices;
+    const int groups = (int)min((long long)a.K, max(1LL, 2048 / units));
+    a.rows = (a.K + groups - 1) / groups;
+    const dim3 grid(a.slices, a.B * ((a.K + a.rows - 1) / a.rows));
+    if (x_bf16) out_bf16 ? launch<VECTORS, WIDE, true, true>(a, grid, s) : launch<VECTORS, WIDE, true, false>(a, grid, s);
+    else out_bf16 ? launch<VECTORS, WIDE, false, true>(a, grid, s) : launch<VECTORS, WIDE, false, false>(a, grid, s);
 }
 
 }  // namespace
 
-int logits_slices(int B, int V)
-{
-    const int slice = slice_of(B, V);
-    return (V + slice - 1) / slice;
-}
+// (as many as the smallest slices make: the workspace fits whichever are taken)
+int logits_slices(int V) { return (V + 8 * kThreads - 1) / (8 * kThreads); }
 
 hipError_t launch_logits(const LogitsArgs& args, bool x_bf16, bool out_bf16, hipStream_t s)
 {
     LogitsArgs a = args;
-    a.slice = slice_of(a.B, a.V);
-    a.slices = (a.V + a.slice - 1) / a.slice;
-    a.rows = a.K;
-    const dim3 grid(a.slices, a.B * ((a.K + a.rows - 1) / a.rows));
-    const size_t lds = ((size_t)a.slice + a.slice / 32 + (a.n_bias > 0 ? a.slice : 0)) * 4;
-    if (x_bf16) {
-        if (out_bf16) logits_kernel<true, true><<<grid, dim3(kThreads), lds, s>>>(a);
-        else logits_kernel<true, false><<<grid, dim3(kThreads), lds, s>>>(a);
-    } else {
-        if (out_bf16) logits_kernel<false, true><<<grid, dim3(kThreads), lds, s>>>(a);
-        else logits_kernel<false, false><<<grid, dim3(kThreads), lds, s>>>(a);
-    }
+    a.marks = a.n_bias > 0 || (a.params && (a.history || a.tokens));
+    const bool wide = (a.params && a.history && a.capacity > kNarrowText) || a.n_bias > kNarrowBias;
+    if (a.marks && wide) launch<1, true>(a, x_bf16, out_bf16, s);
+    else if (vectors_of(a.B, a.V) == 4) launch<4, false>(a, x_bf16, out_bf16, s);
+    else launch<1, false>(a, x_bf16, out_bf16, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.best) return e;
     const long long rows = (long long)a.B * a.K;

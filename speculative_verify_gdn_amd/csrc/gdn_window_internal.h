@@ -53,11 +53,11 @@ struct LogitsArgs {
     const float* bias_values;
     const uint32_t* mask;
     const float* noise;
-    int2* work;  // [rows][slices] the best of each slice: its score's bits and its token
+    unsigned long long* work;  // [rows][slices] the best of each slice, score and token as one number
     int B, K, V, capacity, n_bias;
     // set at the launch
-    int slice;   // tokens of the vocabulary of a workgroup
-    int slices;
+    int marks;   // some tokens may need more than the mask and the temperature
+    int slices;  // of the vocabulary
     int rows;    // rows of a window of a workgroup
 };
 
@@ -69,7 +69,7 @@ struct AcceptArgs {
     int B, K, capacity;
 };
 
-int logits_slices(int B, int V);   // of the vocabulary
+int logits_slices(int V);   // of the vocabulary, at most
 
 hipError_t launch_rope(const RopeArgs& a, bool bf16, bool interleaved, hipStream_t s);
 hipError_t launch_logits(const LogitsArgs& a, bool x_bf16, bool out_bf16, hipStream_t s);

@@ -75,8 +75,8 @@ def logits(x, history=None, lens=None, start=None, tokens=None, parent=None, par
                                 s[v] += 1
                                 n[v] += 1
                 y = x[b, t].to(dt)
-                y = torch.where(s > 0, torch.where(y > 0, y / rep.to(dt), y * rep.to(dt)), y)
-                y = torch.where(n > 0, y - frequency.to(dt) * n.to(dt) - presence.to(dt), y)
+                y = torch.where(s > 0, torch.where(y > 0, y * (1 / rep.to(dt)), y * rep.to(dt)), y)
+                y = torch.where(n > 0, y - (frequency.to(dt) * n.to(dt) + presence.to(dt)), y)
                 if ids is not None:
                     last = {int(v): i for i, v in enumerate(ids[b])}
                     for v, i in last.items():
@@ -85,8 +85,8 @@ def logits(x, history=None, lens=None, start=None, tokens=None, parent=None, par
                 if mask is not None:
                     v = torch.arange(V)
                     y = torch.where((mask[b, t][v // 32] >> (v % 32)) & 1 > 0, y, torch.tensor(-math.inf, dtype=dt))
-                if float(temp) > 0:
-                    y = y / temp.to(dt)
+                if float(temp) >= 2.0 ** -126:
+                    y = y * (1 / temp.to(dt))
                 out[b, t] = y
         both.append(out)
     return both
