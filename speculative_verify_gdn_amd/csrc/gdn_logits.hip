@@ -242,104 +242,92 @@ __device__ __forceinline__ float only(float f, uint32_t bits, int e)
     return __int_as_float(__builtin_amdgcn_bitop3_b32(__float_as_int(f), (int)0xff800000, m, 0xe4));   // m ? f : -inf
 }
 
-// What is known of the tokens of a slice, in LDS.  Narrow: 16 bits a token (14 of the count, one for a bias, one for
-// a place in the text before `start`), and a list of the slice's biases.  Wide: 32 bits a token, and a bias's
-// entry for each.
+// What is known of the tokens of a slice, in LDS: a bit map of those that need more than the mask and the temperature,
+// and their counts.  Narrow: 16 bits a token (14 of the count, one for a bias, one for a place in the text before
+// `start`), and a list of the slice's biases.  Wide: 32 bits a token, and a bias's entry for each.
 constexpr int kNarrowText = 16000;   // the longest text (with a window's drafts below 2^14)
 constexpr int kNarrowBias = kThreads;
 
 template <bool WIDE, int TOKENS>
-struct Known;
-
-template <int TOKENS>
-struct Known<false, TOKENS> {
-    static constexpr uint32_t kCount = 0x3fffu, kBias = 0x4000u, kSeen = 0x8000u, kAnyBias = 0x40004000u;
-    uint32_t cnt[TOKENS / 2];
-    uint16_t bias_token[kNarrowBias];
-    float bias_value[kNarrowBias];
+struct Known {
+    static constexpr int kBits = WIDE ? 32 : 16;
+    static constexpr uint32_t kCount = (1u << (kBits - 2)) - 1, kBias = 1u << (kBits - 2), kSeen = 1u << (kBits - 1);
+    uint32_t cnt[WIDE ? TOKENS : TOKENS / 2];
+    uint32_t bits[TOKENS / 32];
+    int entry[WIDE ? TOKENS : 1];
+    float bias_value[WIDE ? 1 : kNarrowBias];
+    uint16_t bias_token[WIDE ? 1 : kNarrowBias];
     int biases[kWaves];
 
     __device__ __forceinline__ void clear()
     {
-        for (int i = threadIdx.x; i < TOKENS / 8; i += kThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < (int)(sizeof(cnt) / 16); i += kThreads)
+            reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < TOKENS / 32; i += kThreads) bits[i] = 0;
+        if constexpr (WIDE)
+            for (int i = threadIdx.x; i < TOKENS; i += kThreads) entry[i] = -1;
     }
-    __device__ __forceinline__ void add(int u, int n) { atomicAdd(&cnt[u >> 1], (uint32_t)n << 16 * (u & 1)); }
-    __device__ __forceinline__ void mark(int u, uint32_t bit) { atomicOr(&cnt[u >> 1], bit << 16 * (u & 1)); }
-    // the eight from k on; returns their bits together
-    __device__ __forceinline__ uint32_t get8(int k, uint32_t* c) const
+    __device__ __forceinline__ void touch(int u) { atomicOr(&bits[u >> 5], 1u << (u & 31)); }
+    __device__ __forceinline__ void add(int u, int n)
     {
-        const uint4 w = *reinterpret_cast<const uint4*>(cnt + (k >> 1));
-        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[2 * i] = p[i] & 0xffffu, c[2 * i + 1] = p[i] >> 16;
-        return w.x | w.y | w.z | w.w;
+        if constexpr (WIDE) atomicAdd(&cnt[u], (uint32_t)n);
+        else atomicAdd(&cnt[u >> 1], (uint32_t)n << 16 * (u & 1));
     }
-    // the biases of the slice in their order (a thread an entry; every thread calls it, one barrier inside)
-    __device__ __forceinline__ int list_biases(const LogitsArgs& a, int b, int v0, int nv)
+    __device__ __forceinline__ void mark(int u, uint32_t bit)
+    {
+        if constexpr (WIDE) atomicOr(&cnt[u], bit);
+        else atomicOr(&cnt[u >> 1], bit << 16 * (u & 1));
+    }
+    __device__ __forceinline__ uint32_t get(int u) const
+    {
+        if constexpr (WIDE) return cnt[u];
+        else return reinterpret_cast<const uint16_t*>(cnt)[u];
+    }
+    // the biases of the slice; narrow: listed in their order, a thread an entry, and their number is returned.  Every
+    // thread calls it.
+    __device__ __forceinline__ int take_biases(const LogitsArgs& a, int b, int v0, int nv)
     {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        const size_t at = (size_t)b * a.n_bias + tid;
-        const uint32_t u = tid < a.n_bias ? (uint32_t)a.bias_ids[at] - (uint32_t)v0 : 0xffffffffu;
-        const bool mine = u < (uint32_t)nv;
-        const float w = mine ? a.bias_values[at] : 0.0f;
-        const unsigned long long which = __ballot(mine);
-        if (lane == 0) biases[wave] = (int)__popcll(which);
-        __syncthreads();
-        int base = 0, all = 0;
+        const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
+        if constexpr (WIDE) {
+            for (int i = tid; i < a.n_bias; i += kThreads) {
+                const uint32_t u = (uint32_t)ids[i] - (uint32_t)v0;
+                if (u < (uint32_t)nv) {
+                    atomicMax(&entry[u], i);   // (a token named twice: its last entry)
+                    mark(u, kBias);
+                    touch(u);
+                }
+            }
+            return 0;
+        } else {
+            const uint32_t u = tid < a.n_bias ? (uint32_t)ids[tid] - (uint32_t)v0 : 0xffffffffu;
+            const bool mine = u < (uint32_t)nv;
+            const float w = mine ? a.bias_values[(size_t)b * a.n_bias + tid] : 0.0f;
+            const unsigned long long which = __ballot(mine);
+            if (lane == 0) biases[wave] = (int)__popcll(which);
+            __syncthreads();
+            int base = 0, all = 0;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-            base += i < wave ? biases[i] : 0;
-            all += biases[i];
+            for (int i = 0; i < kWaves; ++i) {
+                base += i < wave ? biases[i] : 0;
+                all += biases[i];
+            }
+            if (mine) {
+                base += (int)__popcll(which & ((1ull << lane) - 1));
+                bias_token[base] = (uint16_t)u;
+                bias_value[base] = w;
+                mark(u, kBias);
+                touch(u);
+            }
+            return all;
         }
-        if (mine) {
-            base += (int)__popcll(which & ((1ull << lane) - 1));
-            bias_token[base] = (uint16_t)u;
-            bias_value[base] = w;
-            mark(u, kBias);
-        }
-        return all;
     }
-    __device__ __forceinline__ float bias_of(const LogitsArgs&, int, int u, int listed) const
+    __device__ __forceinline__ float bias_of(const LogitsArgs& a, int b, int u, int listed) const
     {
+        if constexpr (WIDE) return a.bias_values[(size_t)b * a.n_bias + entry[u]];
         int i = listed - 1;   // (a token named twice: its last entry)
         while (bias_token[i] != u) --i;
         return bias_value[i];
-    }
-};
-
-template <int TOKENS>
-struct Known<true, TOKENS> {
-    static constexpr uint32_t kCount = 0x3fffffffu, kBias = 0x40000000u, kSeen = 0x80000000u, kAnyBias = kBias;
-    uint32_t cnt[TOKENS];
-    int entry[TOKENS];
-
-    __device__ __forceinline__ void clear()
-    {
-        for (int i = threadIdx.x; i < TOKENS; i += kThreads) cnt[i] = 0, entry[i] = -1;
-    }
-    __device__ __forceinline__ void add(int u, int n) { atomicAdd(&cnt[u], (uint32_t)n); }
-    __device__ __forceinline__ void mark(int u, uint32_t bit) { atomicOr(&cnt[u], bit); }
-    __device__ __forceinline__ uint32_t get8(int k, uint32_t* c) const
-    {
-        const uint4 w = *reinterpret_cast<const uint4*>(cnt + k), z = *reinterpret_cast<const uint4*>(cnt + k + 4);
-        c[0] = w.x, c[1] = w.y, c[2] = w.z, c[3] = w.w, c[4] = z.x, c[5] = z.y, c[6] = z.z, c[7] = z.w;
-        return w.x | w.y | w.z | w.w | z.x | z.y | z.z | z.w;
-    }
-    __device__ __forceinline__ int list_biases(const LogitsArgs& a, int b, int v0, int nv)
-    {
-        const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
-        for (int i = threadIdx.x; i < a.n_bias; i += kThreads) {
-            const uint32_t u = (uint32_t)ids[i] - (uint32_t)v0;
-            if (u < (uint32_t)nv) {
-                atomicMax(&entry[u], i);   // (a token named twice: its last entry)
-                mark(u, kBias);
-            }
-        }
-        return 0;
-    }
-    __device__ __forceinline__ float bias_of(const LogitsArgs& a, int b, int u, int) const
-    {
-        return a.bias_values[(size_t)b * a.n_bias + entry[u]];
     }
 };
 
@@ -393,6 +381,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
             auto count = [&](int token, int i) {
                 const uint32_t u = (uint32_t)token - (uint32_t)v0;
                 if (u < (uint32_t)nv) {
+                    known.touch(u);
                     if (i >= start) known.add(u, 1);
                     else known.mark(u, K::kSeen);
                 }
@@ -411,10 +400,11 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
             const bool here = d >= v0 && d - v0 < nv;
             paths[lane] = drafts ? node_paths(a.parent ? a.parent + row0 : nullptr, a.K) : 0;
             draft[lane] = d - v0;
+            if (here) known.touch(d - v0);
             const unsigned long long which = __ballot(here);
             if (lane == 0) inside_s = which;
         }
-        if (a.n_bias > 0) listed = known.list_biases(a, b, v0, nv);
+        if (a.n_bias > 0) listed = known.take_biases(a, b, v0, nv);
         __syncthreads();
         inside = inside_s;
     }
@@ -448,20 +438,18 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
                 if constexpr (NOISE) to_front(z, m);
             }
             if (marks) {
-                uint32_t c[8];
-                const uint32_t any = known.get8(k, c);
-                if (any) {
+                // one known token of each lane at a time: most have none, few have two
+                for (uint32_t left = reinterpret_cast<const uint8_t*>(known.bits)[k >> 3]; left; left &= left - 1) {
+                    const int e = __ffs(left) - 1;
+                    const uint32_t c = known.get(k + e), n = c & K::kCount;
+                    float x = f[0];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t n = c[e] & K::kCount;
-                        f[e] *= c[e] & ~K::kBias ? (f[e] > 0.0f ? p.less : p.rep) : 1.0f;
-                        f[e] -= n ? p.frequency * (float)n + p.presence : 0.0f;
-                    }
-                    if (any & K::kAnyBias) {
+                    for (int i = 1; i < 8; ++i) x = i == e ? f[i] : x;
+                    if (c & ~K::kBias) x *= x > 0.0f ? p.less : p.rep;
+                    if (n) x -= p.frequency * (float)n + p.presence;
+                    if (c & K::kBias) x += known.bias_of(a, b, k + e, listed);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c[e] & K::kBias) f[e] += known.bias_of(a, b, k + e, listed);
-                    }
+                    for (int i = 0; i < 8; ++i) f[i] = i == e ? x : f[i];
                 }
             }
 #pragma unroll
