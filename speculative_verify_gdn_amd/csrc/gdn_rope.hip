@@ -26,45 +26,47 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTileMax = kWaves;    // tokens of a workgroup
+constexpr int kTileMax = 32;        // tokens of a workgroup
 constexpr int kAngles = 1024;       // sines (and cosines) of a workgroup
-constexpr long long kStreamBytes = 32 << 20;
+// Reads of more than this go past the caches (tokens of 32 heads of 256, by their number: 2048, 33.5 MB read, 17.9 us past
+// them and 14.7 through them; 4096 31.1 and 31.8; 8192 59.5 and 61.4).
+constexpr long long kStreamBytes = 48 << 20;
 constexpr double kInv2Pi = 0.15915494309189533577;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-// E elements of one piece: as they lie in memory, and as floats
+// E elements of one piece, 16 or 8 bytes or a single one: as they lie in memory, and as floats
 template <bool BF16, int E, bool STREAM>
 struct Piece {
-    u32x4_t raw;   // (16 bytes, or the one element in x)
+    static constexpr int kWords = E * (BF16 ? 2 : 4) / 4;   // (a single bf16: 0)
+    static_assert(kWords == 4 || kWords == 2 || E == 1, "a piece is 16 or 8 bytes or one element");
+    typedef uint32_t words_t __attribute__((ext_vector_type(E == 1 ? 1 : kWords)));
+    words_t raw;
 
     __device__ __forceinline__ void load(const char* p)
     {
-        if constexpr (E > 1 && STREAM) raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
-        else if constexpr (E > 1) raw = *reinterpret_cast<const u32x4_t*>(p);
-        else if constexpr (BF16) raw[0] = *reinterpret_cast<const uint16_t*>(p);
-        else raw[0] = *reinterpret_cast<const uint32_t*>(p);
+        if constexpr (E == 1 && BF16) raw[0] = *reinterpret_cast<const uint16_t*>(p);
+        else if constexpr (STREAM) raw = __builtin_nontemporal_load(reinterpret_cast<const words_t*>(p));
+        else raw = *reinterpret_cast<const words_t*>(p);
     }
     __device__ __forceinline__ void floats(float* f) const
     {
-        if constexpr (BF16 && E == 8) {
+        if constexpr (BF16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(raw[i]), f[2 * i + 1] = bf16_hi(raw[i]);
-        } else if constexpr (!BF16 && E == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(raw[i]);
+            for (int i = 0; i < E; ++i) f[i] = i & 1 ? bf16_hi(raw[i >> 1]) : bf16_lo(raw[i >> 1]);
         } else {
-            static_assert(E == 1, "pieces are 16 bytes or one element");
-            f[0] = BF16 ? bf16_lo(raw[0]) : __uint_as_float(raw[0]);
+#pragma unroll
+            for (int i = 0; i < E; ++i) f[i] = __uint_as_float(raw[i]);
         }
     }
     static __device__ __forceinline__ void store(char* p, const float* f)
     {
-        if constexpr (E > 1) {
-            u32x4_t w;
+        if constexpr (E == 1) {
+            store1<BF16>(p, 0, f[0]);
+        } else {
+            words_t w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kWords; ++i) {
                 if constexpr (BF16) {
                     const bf16x2_t h = {(__bf16)f[2 * i], (__bf16)f[2 * i + 1]};
                     w[i] = __builtin_bit_cast(uint32_t, h);
@@ -72,10 +74,8 @@ struct Piece {
                     w[i] = __float_as_uint(f[i]);
                 }
             }
-            if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
-            else *reinterpret_cast<u32x4_t*>(p) = w;
-        } else {
-            store1<BF16>(p, 0, f[0]);
+            if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<words_t*>(p));
+            else *reinterpret_cast<words_t*>(p) = w;
         }
     }
 };
@@ -131,13 +131,7 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
     const int n = (int)min((uint32_t)a.tile, tokens - first);
     const int half = a.rot >> 1;
 
-    // A wave looks after one token, or several waves where there are fewer: what it has to know of it is asked for first.
-    const int share = kWaves / a.tile, mine = wave / share, sub = wave - mine * share;
-    const uint32_t tok = min(first + mine, tokens - 1);
-    const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
-    const int32_t parent = a.parent && lane < a.K ? a.parent[(size_t)b * a.K + lane] : -1;
-    const int j0 = lane + 64 * sub;
-    const double freq = j0 < half ? a.freqs[j0] : 0.0;
+    // the norms' weights are asked for first
     float w[2][kRopeHeadMax / kThreads];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -188,8 +182,14 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
                 v[k].load(x + bt[k] * ES);
             }
     };
-    // where the token stands and goes, and its sines
-    if (mine < n) {
+    // where each token stands and goes, and its sines: a wave a token, or several waves where there are fewer tokens
+    const int share = max(kWaves / a.tile, 1), sub = wave % share;
+    for (int i = wave / share; i < n; i += kWaves / share) {
+        const uint32_t tok = first + i;
+        const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
+        const int32_t parent = a.parent && lane < a.K ? a.parent[(size_t)b * a.K + lane] : -1;
+        const int j0 = lane + 64 * sub;
+        const double freq = j0 < half ? a.freqs[j0] : 0.0;
         const long long len = a.lens ? max(a.lens[b], 0) : 0;
         const bool there = !a.count || t < a.count[b];
         if (sub == 0) {
@@ -203,8 +203,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
             }
             if (lane < 3) {
                 const RopePart& r = a.part[lane];
-                info[mine].from[lane] = b * r.xs[0] + t * r.xs[1];
-                info[mine].to[lane] = !there ? -1 : r.paged ? page_at : b * r.ys[0] + t * r.ys[1];
+                info[i].from[lane] = b * r.xs[0] + t * r.xs[1];
+                info[i].to[lane] = !there ? -1 : r.paged ? page_at : b * r.ys[0] + t * r.ys[1];
             }
         }
         const long long p = a.pos      ? (long long)a.pos[tok]
@@ -214,8 +214,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
             const double turns = (double)p * (j == j0 ? freq : a.freqs[j]) * kInv2Pi;
             float s, c;
             sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-            cs[mine * half + j] = a.mscale * c;
-            sn[mine * half + j] = a.mscale * s;
+            cs[i * half + j] = a.mscale * c;
+            sn[i * half + j] = a.mscale * s;
         }
     }
 #pragma unroll
@@ -296,11 +296,12 @@ __global__ __launch_bounds__(kThreads, 8) void rope_kernel(RopeArgs a)
     rope_heads<BF16, BF16 ? 8 : 4, 1, INTERLEAVED, STREAM>(a);
 }
 
-// element by element
-template <bool BF16, bool INTERLEAVED>
+// Pieces of 8 bytes, and element by element: for turned parts that no whole pairs of 16 bytes make up (8192 tokens of
+// 32 heads of 96, bf16: 32 elements of each turned 27 us, 24 of them 42, 22 102).
+template <bool BF16, int E, int NP, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void rope_narrow_kernel(RopeArgs a)
 {
-    rope_heads<BF16, 1, 4, INTERLEAVED, false>(a);
+    rope_heads<BF16, E, NP, INTERLEAVED, false>(a);
 }
 
 int log2_up(int n)
@@ -314,21 +315,29 @@ template <bool BF16, bool INTERLEAVED>
 void launch(RopeArgs& a, hipStream_t s)
 {
     constexpr int E = BF16 ? 8 : 4;
-    // 16-byte pieces where the turned part is made of whole pairs of them, single elements otherwise
-    const bool wide = a.rot % (2 * E) == 0;
-    a.lanes_log2 = min(log2_up(a.D / (wide ? 2 * E : 2)), 6);
+    const int e = a.rot % (2 * E) == 0 ? E : a.rot % E == 0 ? E / 2 : 1;   // elements of a piece
+    a.lanes_log2 = min(log2_up(a.D / (2 * e)), 6);
     a.heads = a.part[0].H + a.part[1].H + a.part[2].H;
     const long long tokens = (long long)a.B * a.K;
     const int half = a.rot / 2, pass = kThreads >> a.lanes_log2;
+    // Tokens of a workgroup: as many as give its groups a head each (tokens of 6 heads of 64, 65536 of them: 100 us with
+    // one a workgroup, 43 with four), and three where there are many workgroups left (4096 x 4 tokens of 32 heads of 128:
+    // 58.6 us with one, 52.1 with four; 8192 of 32 heads of 256: 56.3 with one, 57.2 with two).
     a.tile = 1;
-    while (a.tile < 4 && tokens / a.tile > 2048 && 2 * a.tile * half <= kAngles) a.tile *= 2;
+    while (2 * a.tile <= kTileMax && 2 * a.tile * half <= kAngles &&
+           ((a.tile * a.heads < pass && tokens / (2 * a.tile) >= 1024) ||
+            (a.tile * a.heads < 3 * pass && tokens / (2 * a.tile) >= 2048)))
+        a.tile *= 2;
     const long long tiles = (tokens + a.tile - 1) / a.tile;
-    int chunks = (a.heads * a.tile + pass - 1) / pass;   // one head a group of lanes
-    while (chunks > 1 && tiles * chunks > 2048) chunks = (chunks + 1) / 2;
+    // A head a group, and several for each where that makes more workgroups than four a CU (128 windows of 16 tokens of 32
+    // heads of 256: 14.8 us, with one head a group 16.8).
+    int chunks = (a.heads * a.tile + pass - 1) / pass;
+    while (chunks > 1 && tiles * chunks > 1024) chunks = (chunks + 1) / 2;
     a.chunk = (a.heads + chunks - 1) / chunks;
     const dim3 grid((unsigned)tiles, (a.heads + a.chunk - 1) / a.chunk);
     const bool stream = (long long)tokens * a.heads * a.D * (BF16 ? 2 : 4) > kStreamBytes;
-    if (!wide) rope_narrow_kernel<BF16, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
+    if (e == 1) rope_narrow_kernel<BF16, 1, 4, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
+    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
     else if (stream) rope_kernel<BF16, INTERLEAVED, true><<<grid, dim3(kThreads), 0, s>>>(a);
     else rope_kernel<BF16, INTERLEAVED, false><<<grid, dim3(kThreads), 0, s>>>(a);
 }

@@ -53,7 +53,7 @@ def check(got, want, off, dtype, there):
 
 # heads of every kind: whole, part, pairs that fill no 16 bytes, the largest
 HEADS = [(64, 64), (128, 32), (256, 64), (256, 256), (80, 80), (96, 24), (192, 192), (16, 2), (16, 16), (512, 512), (112, 38),
-         (512, 6), (48, 46)]
+         (512, 6), (48, 46), (512, 20), (80, 40), (256, 12)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
