@@ -152,16 +152,19 @@ __device__ __forceinline__ uint32_t wave_most(uint32_t v)
     return v;
 }
 
-// the nodes on the path root..i as a bit mask, in lane i, by doubling (a whole wave)
-__device__ __forceinline__ unsigned long long node_paths(const int32_t* parent, int N)
+// the node above lane's of a tree (parent: its entry) or of a chain, below 0: none
+__device__ __forceinline__ int node_above(const int32_t* parent, int N)
 {
     const int lane = threadIdx.x & 63;
-    int up = -1;
-    if (lane < N) {
-        const int p = parent ? parent[lane] : lane - 1;
-        up = p >= 0 && p < lane ? p : -1;
-    }
-    unsigned long long path = 1ull << lane;
+    if (lane >= N) return -1;
+    const int p = parent ? parent[lane] : lane - 1;
+    return p >= 0 && p < lane ? p : -1;
+}
+
+// the nodes on the path root..i as a bit mask, in lane i, from the node above each, by doubling (a whole wave)
+__device__ __forceinline__ unsigned long long node_paths(int up, int N)
+{
+    unsigned long long path = 1ull << (threadIdx.x & 63);
     for (int d = 1; d < N; d <<= 1) {
         const unsigned long long more = __shfl(path, max(up, 0), 64);
         const int far = __shfl(up, max(up, 0), 64);
@@ -283,13 +286,13 @@ struct Known {
         if constexpr (WIDE) return cnt[u];
         else return reinterpret_cast<const uint16_t*>(cnt)[u];
     }
-    // the biases of the slice; narrow: listed in their order, a thread an entry, and their number is returned.  Every
-    // thread calls it.
-    __device__ __forceinline__ int take_biases(const LogitsArgs& a, int b, int v0, int nv)
+    // the biases of the slice; narrow: listed in their order, a thread an entry (id, value), and their number is
+    // returned.  Every thread calls it.
+    __device__ __forceinline__ int take_biases(const LogitsArgs& a, int b, int v0, int nv, int id, float value)
     {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
         if constexpr (WIDE) {
+            const int32_t* ids = a.bias_ids + (size_t)b * a.n_bias;
             for (int i = tid; i < a.n_bias; i += kThreads) {
                 const uint32_t u = (uint32_t)ids[i] - (uint32_t)v0;
                 if (u < (uint32_t)nv) {
@@ -300,9 +303,8 @@ struct Known {
             }
             return 0;
         } else {
-            const uint32_t u = tid < a.n_bias ? (uint32_t)ids[tid] - (uint32_t)v0 : 0xffffffffu;
-            const bool mine = u < (uint32_t)nv;
-            const float w = mine ? a.bias_values[(size_t)b * a.n_bias + tid] : 0.0f;
+            const uint32_t u = (uint32_t)id - (uint32_t)v0;
+            const bool mine = tid < a.n_bias && u < (uint32_t)nv;
             const unsigned long long which = __ballot(mine);
             if (lane == 0) biases[wave] = (int)__popcll(which);
             __syncthreads();
@@ -315,7 +317,7 @@ struct Known {
             if (mine) {
                 base += (int)__popcll(which & ((1ull << lane) - 1));
                 bias_token[base] = (uint16_t)u;
-                bias_value[base] = w;
+                bias_value[base] = value;
                 mark(u, kBias);
                 touch(u);
             }
@@ -350,6 +352,26 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     const size_t row0 = (size_t)b * a.K;
     const int v0 = blockIdx.x * kTokens, nv = min(kTokens, a.V - v0);
 
+    // What the counting needs is asked for first: reads come back in their order, and those of the logits take longer
+    // (64 rows of 131072, fp32: 22.5 to 22.1 us).
+    const Params p(a.params, b);
+    const bool marks = a.marks, texts = marks && a.params && a.history, drafts = marks && a.params && a.tokens;
+    const int32_t* h = a.history + (size_t)b * a.capacity;
+    // four tokens of the text from index i on, or its last four where there are fewer behind i
+    auto four = [&](int i) { return *reinterpret_cast<const u32x4_any_t*>(h + min(i, a.capacity - 4)); };
+    u32x4_any_t text = {0, 0, 0, 0};
+    int drafted = -1, above = -1, id = -1;
+    float value = 0.0f;
+    if (texts && a.capacity >= 4) text = four(tid * 4);
+    if (drafts && wave == kWaves - 1) {
+        drafted = lane < a.K ? a.tokens[row0 + lane] : -1;
+        above = node_above(a.parent ? a.parent + row0 : nullptr, a.K);
+    }
+    if (!WIDE && tid < a.n_bias) {
+        id = a.bias_ids[(size_t)b * a.n_bias + tid];
+        value = a.bias_values[(size_t)b * a.n_bias + tid];
+    }
+
     // the first two vectors of eight are on their way while the text is counted, later ones two ahead
     const int vectors = (nv + 8 * kThreads - 1) / (8 * kThreads);
     Row8<XBF16, NOISE> even, odd;
@@ -366,16 +388,13 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     load(even);
     load(odd);
 
-    const Params p(a.params, b);
-    const bool marks = a.marks;
     unsigned long long inside = 0;
     int listed = 0;
     if (tid < kKvWindowMax) best[tid] = 0;
     if (marks) known.clear();
     __syncthreads();
     if (marks) {
-        if (a.params && a.history) {
-            const int32_t* h = a.history + (size_t)b * a.capacity;
+        if (texts) {
             const int len = min(max(a.history_lens[b], 0), a.capacity);
             const int start = a.history_start ? a.history_start[b] : 0;
             auto count = [&](int token, int i) {
@@ -386,25 +405,27 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
                     else known.mark(u, K::kSeen);
                 }
             };
-            const int whole = len & ~3;
-            for (int i = tid * 4; i < whole; i += kThreads * 4) {
-                const u32x4_any_t t = *reinterpret_cast<const u32x4_any_t*>(h + i);
+            if (a.capacity >= 4) {
+                for (int i = tid * 4; i < len; i += kThreads * 4) {
+                    if (i >= kThreads * 4) text = four(i);
+                    const int from = min(i, a.capacity - 4);   // (see four)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) count((int)t[e], i + e);
+                    for (int e = 0; e < 4; ++e)
+                        if (from + e >= i && from + e < len) count((int)text[e], from + e);
+                }
+            } else if (tid < len) {
+                count(h[tid], tid);
             }
-            if (tid < len - whole) count(h[whole + tid], whole + tid);
         }
         if (wave == kWaves - 1) {   // the path to each node, and the drafted tokens of this slice
-            const bool drafts = a.params && a.tokens;
-            const int d = drafts && lane < a.K ? a.tokens[row0 + lane] : -1;
-            const bool here = d >= v0 && d - v0 < nv;
-            paths[lane] = drafts ? node_paths(a.parent ? a.parent + row0 : nullptr, a.K) : 0;
-            draft[lane] = d - v0;
-            if (here) known.touch(d - v0);
+            const bool here = drafted >= v0 && drafted - v0 < nv;
+            paths[lane] = drafts ? node_paths(above, a.K) : 0;
+            draft[lane] = drafted - v0;
+            if (here) known.touch(drafted - v0);
             const unsigned long long which = __ballot(here);
             if (lane == 0) inside_s = which;
         }
-        if (a.n_bias > 0) listed = known.take_biases(a, b, v0, nv);
+        if (a.n_bias > 0) listed = known.take_biases(a, b, v0, nv, id, value);
         __syncthreads();
         inside = inside_s;
     }
@@ -538,12 +559,8 @@ __global__ __launch_bounds__(kThreads) void accept_kernel(AcceptArgs a)
     const int token = node ? a.tokens[(size_t)b * a.K + lane] : -1;
     const int target = node ? a.target[(size_t)b * a.K + lane] : -1;
     const int root = a.root ? a.root[b] : -1;
-    int up = -1;
-    if (node) {
-        const int p = parent ? parent[lane] : lane - 1;
-        up = p >= 0 && p < lane ? p : -1;
-    }
-    const unsigned long long path = node_paths(parent, a.K);
+    const int up = node_above(parent, a.K);
+    const unsigned long long path = node_paths(up, a.K);
     const int above = __shfl(target, max(up, 0), 64);
     const bool good = lane < live && (up >= 0 ? token >= 0 && token == above : root < 0 || token == root);
     const unsigned long long bad = __ballot(!good);

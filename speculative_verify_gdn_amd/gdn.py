@@ -59,7 +59,7 @@ def load(path: str = LIB_PATH):
 
 def _L():
     """The library the calls of this thread go to: load()'s, or the one a `using` block names."""
-    lib = getattr(_using, "lib", None)
+    lib = getattr(_using, "lib", None) or _lib
     return lib if lib is not None else load()
 
 
