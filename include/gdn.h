@@ -34,7 +34,8 @@
  * S is dv x dk (row i is value index i, columns are key dims), fp32.
  *
  * Conventions shared by every entry point
- *   - Every pointer argument is a DEVICE pointer owned by the caller; the
+ *   - Every pointer argument is a DEVICE pointer owned by the caller (but where
+ *     it is called a HOST pointer: strides, sizes and frequencies); the
  *     library never allocates, frees or keeps device memory, never
  *     synchronises, and launches only on `stream` (a hipStream_t; NULL is the
  *     default stream).  Calls are stream-ordered; two calls that write the
@@ -712,7 +713,7 @@ int gdn_kv_append_rope(const void *q, const long long *q_strides, const void *k,
  *   best is a sample of softmax(x)
  *   workspace (with best): gdn_logits_workspace bytes, its contents not kept
  *   between calls (calls on different streams need one each)
- *   B <= 65535, K <= 64, V <= 2^24, n_bias <= 2^20, capacity <= 2^30; logits, out, noise and
+ *   B <= 65535, K <= 64, V <= 2^24, n_bias <= 2^20, capacity <= 2^29; logits, out, noise and
  *   workspace 16-byte aligned, the others 4
  */
 int gdn_logits_adjust(const void *logits, long long logits_stride, void *out, long long out_stride, int32_t *best,
@@ -738,7 +739,7 @@ int gdn_logits_workspace(int B, int K, int V, size_t *bytes);
  *   path go to history[b][lens[b] ..] (those past capacity nowhere), lens_out[b] <- the
  *   new length (capacity at most); lens clamped into 0..capacity; lens_out may be lens
  *   target, tokens [B][K] (target: gdn_logits_adjust's best); parent [B][K] or NULL (a
- *   chain); count, root [B] or NULL; K <= 64, B <= 2^20, capacity <= 2^30
+ *   chain); count, root [B] or NULL; K <= 64, B <= 2^20, capacity <= 2^29
  */
 int gdn_accept_tree(const int32_t *target, const int32_t *tokens, const int32_t *parent, const int32_t *count,
                     const int32_t *root, int32_t *node, int32_t *next, int32_t *history, const int32_t *lens,

@@ -1175,7 +1175,7 @@ int gdn_logits_adjust(const void* logits, long long logits_stride, void* out, lo
             GDN_EINVAL, "%s: int32 and float pointers must be 4-byte aligned", fn);
     if (history) {
         REQUIRE(history_lens, GDN_EINVAL, "%s: history without history_lens", fn);
-        REQUIRE(capacity >= 1 && capacity <= 1 << 30, GDN_EINVAL, "%s: capacity = %d is not in 1..2^30", fn, capacity);
+        REQUIRE(capacity >= 1 && capacity <= 1 << 29, GDN_EINVAL, "%s: capacity = %d is not in 1..2^29", fn, capacity);
     }
     REQUIRE(n_bias == 0 || (bias_ids && bias_values), GDN_EINVAL, "%s: biases without bias_ids or bias_values", fn);
     REQUIRE(!noise || best, GDN_EINVAL, "%s: noise is for finding best", fn);
@@ -1219,7 +1219,7 @@ int gdn_accept_tree(const int32_t* target, const int32_t* tokens, const int32_t*
     REQUIRE((history != nullptr) == (lens != nullptr) && (history != nullptr) == (lens_out != nullptr), GDN_EINVAL,
             "%s: history, lens and lens_out are all given or all NULL", fn);
     if (history)
-        REQUIRE(capacity >= 1 && capacity <= 1 << 30, GDN_EINVAL, "%s: capacity = %d is not in 1..2^30", fn, capacity);
+        REQUIRE(capacity >= 1 && capacity <= 1 << 29, GDN_EINVAL, "%s: capacity = %d is not in 1..2^29", fn, capacity);
     REQUIRE(aligned4(target) && aligned4(tokens) && aligned4(parent) && aligned4(count) && aligned4(root) &&
                 aligned4(node) && aligned4(next) && aligned4(history) && aligned4(lens) && aligned4(lens_out),
             GDN_EINVAL, "%s: pointers must be 4-byte aligned", fn);

@@ -11,13 +11,17 @@
 // One read of the logits and one write: memory bound, if the counts cost
 // little.  So a workgroup takes a slice of the vocabulary for some rows of one
 // sequence: it walks the text once, counts the tokens of its slice in LDS (16
-// bits each, 16 KB for 8192 tokens), and then streams.  Eight logits whose eight counts are 0,
-// which is nearly all of them, take the short way.
+// bits each, 16 KB for 8192 tokens), and then streams; a bit map says which tokens have a
+// count or a bias, and a lane looks up those of its eight alone.
 // Every operation is one rounding of 32 bits in the order above, so that equal
 // logits stay equal and the best is the lowest of them.
 //
-// Measured apart: with the logits of the counted tokens left to a second kernel (a hash table
-// a sequence), that kernel's scattered reads and writes took 13 us behind a window of 32 x 8 rows of 131072.
+// Measured: 64 rows of 131072, fp32, with noise and output (101 MB) 22.2 us, of which the stream 19.6 (5.1 TB/s);
+// 32 ragged windows of 8 rows of 131072, bf16, masks, biases and texts of 4000 (78 MB)
+// 24.4 us, and without text, biases, masks and best 14.0: the counting takes 4 us, the mask and the biases 2 each, the
+// search for the best 2.5, joining it 3.
+// With the logits of the counted tokens left to a second kernel (a hash table a sequence) the stream was 1 us shorter, and
+// that kernel's scattered reads and writes took 13.
 #include "gdn_device.h"
 #include "gdn_window_internal.h"
 

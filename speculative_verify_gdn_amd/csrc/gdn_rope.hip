@@ -12,12 +12,17 @@
 //     that many rows would not fit), reduced to turns and only then rounded to
 //     32 bits; a workgroup forms the sines of its tokens once, into LDS, and
 //     every head of a token reads them from there.
-//   - a group of lanes holds one head, a lane the two 16-byte pieces whose
-//     elements are pairs of one another: (j, j + rot/2) for the two halves, the
-//     neighbouring pieces for neighbours.  So no element crosses lanes, and the norm is
-//     a sum over the group.
+//   - a group of lanes holds one head, a lane two 16-byte pieces of it: for the
+//     two halves those whose elements are pairs of one another, for neighbours
+//     any two, taken half the turned part apart so that the lanes of a group lie side
+//     by side.  So no element crosses lanes, and the norm is a sum over the group.
 //   - where the head goes (dense rows, or a page of the cache) is an offset a
-//     token, found while the first heads are on their way.
+//     token.
+// Measured: 16384 tokens of 48 heads of 128 (bf16, into the cache, 403 MB) 76.8 us, 5.2 TB/s; 8193 of 40
+// heads of 128 (fp32, normed, 336 MB) 66.7 us; 16384 of 32 (bf16, 268 MB) 51.3 us: 93 to 97% of a copy of the same
+// bytes.  1024 tokens in trees of 16, 32 heads of 256 (34 MB) 10.2 us: a workgroup's chain of reads, 9 us from its
+// start to its last store.  Heads asked for before that chain, or a head ahead, took longer in every case (waves
+// then hold more registers, or reads come back in an order that the chain waits for).
 #include "gdn_device.h"
 #include "gdn_window_internal.h"
 

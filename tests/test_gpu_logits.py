@@ -101,6 +101,47 @@ def test_adjust_a_large_vocabulary(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kw", [dict(tree=True, ragged=True, n_bias=40, mask=True, noise=True), dict(n_bias=256), dict(params=False)])
+def test_adjust_in_large_slices(kw, dtype):
+    """Enough rows that a workgroup takes 8192 tokens of the vocabulary, and one that ends inside a slice."""
+    say("logits large slices", kw, dtype)
+    c = case(11, 5, 8, 100003, 150, dtype, **kw)
+    check(c, *run(c, dtype), dtype)
+
+
+@pytest.mark.parametrize("capacity,seen,n_bias", [(16000, 16000, 3), (16001, 16001, 3), (20000, 700, 0), (20000, 20000, 257), (3, 3, 0), (5, 4, 257),
+                                                  (1030, 1029, 1), (4, 4, 256)])
+def test_texts_of_every_length(capacity, seen, n_bias):
+    """Counts of 16 bits and of 32, on both sides of where they change, one token for nearly all of a text; texts that
+    end inside a read of four; biases listed and not."""
+    say("logits texts", capacity, seen, n_bias)
+    c = case(12, 2, 2, 5000, capacity, F32, n_bias=n_bias)
+    c["history"][:, :capacity - 1] = torch.tensor([[17], [4999]], dtype=I32)
+    c["lens"] = torch.tensor([seen, seen - 1], dtype=I32)
+    c["start"] = torch.tensor([1, seen // 2], dtype=I32)
+    c["tokens"][:] = 17
+    if n_bias:
+        c["ids"][:, 0] = 17
+    check(c, *run(c, F32), F32)
+
+
+def test_logits_past_2_31():
+    """More than 2^31 logits: the last row is right, and the first."""
+    say("logits past 2^31")
+    B, K, V = 257, 64, 131072
+    x = torch.zeros(B, K, V, dtype=BF, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    rows = torch.randn(2, V, generator=g).to(BF)
+    x[0, 0], x[-1, -1] = rows[0].cuda(), rows[1].cuda()
+    params = torch.tensor([1.0, 0.0, 0.0, 0.5]).repeat(B, 1).cuda()
+    best = torch.empty(B, K, dtype=I32, device="cuda")
+    gdn.logits_adjust(x, out=x, best=best, params=params, workspace=gdn.logits_workspace(x))
+    assert torch.equal(x[0, 0].cpu(), (rows[0].float() * 2).to(BF)) and torch.equal(x[-1, -1].cpu(), (rows[1].float() * 2).to(BF))
+    assert best[0, 0].item() == ref.best(rows[:1].float())[0].item() and best[-1, -1].item() == ref.best(rows[1:].float())[0].item()
+    assert int(best[100, 7]) == 0 and float(x[100, 7].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_one_of_the_outputs_and_in_place(dtype):
     say("logits outputs", dtype)
     c = case(6, 2, 3, 1234, 60, dtype, n_bias=4)

@@ -323,6 +323,49 @@ def test_append_past_4_gb():
     assert torch.equal(planes[1][n_pages - 1, :, page - 1], v[0, 0]) and torch.equal(planes[1][n_pages - 2, :, 0], v[0, 1])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,D,rot,K", [(24, 4, 256, 64, 3001), (3, 1, 64, 64, 40001), (32, 8, 128, 128, 4100), (5, 2, 64, 24, 9000)])
+def test_one_call_and_many(Hq, Hkv, D, rot, K, dtype):
+    """A long window in one call and in pieces: the same bits, however a launch is cut."""
+    say("one call and many", Hq, Hkv, D, rot, K, dtype)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    page = 64
+    row = torch.randn(1, K, (Hq + 2 * Hkv) * D, generator=g, device="cuda").to(dtype)
+    q, k, v = (x.unflatten(-1, (-1, D)) for x in row.split((Hq * D, Hkv * D, Hkv * D), -1))
+    w, f = 1 + 0.2 * torch.randn(D, generator=g, device="cuda"), freqs_of(rot).cuda()
+    P = K // page + 2
+    table = torch.randperm(P, generator=g, device="cuda").to(I32)[None].contiguous()
+    got = []
+    for step in (K, 337, 29):
+        pool, qo = torch.zeros(2, P, Hkv, page, D, dtype=dtype, device="cuda"), torch.zeros(1, K, Hq, D, dtype=dtype, device="cuda")
+        for at in range(0, min(K, 100 * step), step):
+            n = min(step, K - at)
+            gdn.kv_append_rope(k[:, at:at + n], v[:, at:at + n], pool[0], pool[1], dev([at + 7]), table, f, q=q[:, at:at + n],
+                               q_out=qo[:, at:at + n], wq=w, wk=w)
+        got.append((pool, qo, min(K, 100 * step)))
+    for pool, qo, n in got[1:]:
+        assert torch.equal(qo[:, :n], got[0][1][:, :n])
+        rows = torch.arange(7, n + 7, device="cuda")
+        ids = table[0, rows // page].long()
+        assert torch.equal(pool[:, ids, :, rows % page], got[0][0][:, ids, :, rows % page])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_more_than_4_gb(interleaved):
+    """A window of more than 2^32 bytes: its last token is right."""
+    say("rope past 2^32", interleaved)
+    g = torch.Generator().manual_seed(6)
+    B, K, H, D = 9, 16384, 64, 256
+    x = torch.zeros(B, K, H, D, dtype=BF, device="cuda")
+    last = randn(g, 1, 1, H, D, dtype=BF)
+    x[-1, -1] = last[0, 0].cuda()
+    f = freqs_of(64)
+    gdn.rope(x, x, f.cuda(), interleaved=interleaved)
+    want, off = ref.turned(last, [[K - 1]], f, interleaved)
+    check(x[-1:, -1:].cpu(), want, off, BF, torch.ones(1, 1, dtype=torch.bool))
+    assert float(x[:-1].abs().max()) == 0.0
+
+
 def test_captured_and_on_two_streams():
     """A window's calls in a graph, replayed with other inputs in the same buffers and eager work between, and the same calls
     on two streams at once."""

@@ -92,7 +92,7 @@ BAD = {
                           (dict(out=None, best=None, noise=None), E), (dict(out=None, best=None), E), (dict(best=None), E),
                           (dict(logits_stride=999), E), (dict(out_stride=10), E), (dict(logits=p(1, 8)), E),
                           (dict(noise=p(14, 4)), E), (dict(workspace=p(15, 8)), E), (dict(best=p(3, 2)), E),
-                          (dict(history_lens=None), E), (dict(capacity=0), E), (dict(capacity=(1 << 30) + 1), E),
+                          (dict(history_lens=None), E), (dict(capacity=0), E), (dict(capacity=(1 << 29) + 1), E),
                           (dict(n_bias=-1), E), (dict(n_bias=(1 << 20) + 1), E), (dict(bias_ids=None), E),
                           (dict(bias_values=None), E), (dict(workspace=None), E), (dict(workspace_bytes=8), E),
                           (dict(out=p(1)), E), (dict(out=p(1, 16)), E), (dict(best=p(1, 64)), E), (dict(workspace=p(2)), E),
