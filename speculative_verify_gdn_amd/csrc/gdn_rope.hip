@@ -33,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTileMax = 32;        // tokens of a workgroup
 constexpr int kAngles = 1024;       // sines (and cosines) of a workgroup
+constexpr long long kGridX = 1 << 23;   // workgroups in x (a launch's threads there stay below 2^32)
 // Reads of more than this go past the caches (tokens of 32 heads of 256, by their number: 2048, 33.5 MB read, 17.9 us past
 // them and 14.7 through them; 4096 31.1 and 31.8; 8192 59.5 and 61.4).
 constexpr long long kStreamBytes = 48 << 20;
@@ -63,6 +64,13 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < E; ++i) f[i] = __uint_as_float(raw[i]);
         }
+    }
+    // as it came, to the bit (a conversion makes a signalling NaN a quiet one)
+    __device__ __forceinline__ void keep(char* p) const
+    {
+        if constexpr (E == 1 && BF16) *reinterpret_cast<uint16_t*>(p) = (uint16_t)raw[0];
+        else if constexpr (STREAM) __builtin_nontemporal_store(raw, reinterpret_cast<words_t*>(p));
+        else *reinterpret_cast<words_t*>(p) = raw;
     }
     static __device__ __forceinline__ void store(char* p, const float* f)
     {
@@ -132,7 +140,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
     __shared__ float weight[2][kRopeHeadMax];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t tokens = (uint32_t)a.B * a.K, first = blockIdx.x * a.tile;
+    const uint32_t tokens = (uint32_t)a.B * a.K, first = (blockIdx.x + blockIdx.z * gridDim.x) * a.tile;
+    if (first >= tokens) return;
     const int n = (int)min((uint32_t)a.tile, tokens - first);
     const int half = a.rot >> 1;
 
@@ -269,7 +278,13 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
         for (int k = 0; k < NP; ++k) {
             const int j = l + (k << a.lanes_log2);
             if (j >= pairs) continue;
-            if (part.turned && j < turned) {
+            const bool turns = part.turned && j < turned;
+            if (!turns && !part.w) {
+                u[k].keep(y + at[k] * ES);
+                v[k].keep(y + bt[k] * ES);
+                continue;
+            }
+            if (turns) {
                 auto turn = [](float& p, float& q, float c, float s) {
                     const float p0 = p, q0 = q;
                     p = fmaf(p0, c, -(q0 * s));
@@ -339,7 +354,7 @@ void launch(RopeArgs& a, hipStream_t s)
     int chunks = (a.heads * a.tile + pass - 1) / pass;
     while (chunks > 1 && tiles * chunks > 1024) chunks = (chunks + 1) / 2;
     a.chunk = (a.heads + chunks - 1) / chunks;
-    const dim3 grid((unsigned)tiles, (a.heads + a.chunk - 1) / a.chunk);
+    const dim3 grid((unsigned)min(tiles, kGridX), (a.heads + a.chunk - 1) / a.chunk, (unsigned)((tiles + kGridX - 1) / kGridX));
     const bool stream = (long long)tokens * a.heads * a.D * (BF16 ? 2 : 4) > kStreamBytes;
     if (e == 1) rope_narrow_kernel<BF16, 1, 4, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
     else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);

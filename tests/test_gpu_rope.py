@@ -324,6 +324,54 @@ def test_append_past_4_gb():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [5, 50001])
+def test_bits_that_stay(K, dtype):
+    """Values, what does not turn and keys without a turn keep every bit pattern, signalling NaNs among them."""
+    say("bits", K, dtype)
+    g = torch.Generator().manual_seed(K)
+    H, D, page, word = 4, 64, 16, torch.int16 if dtype == BF else I32
+    info = torch.iinfo(word)
+    bits = torch.randint(info.min, info.max + 1, (1, K, 2 * H, D), generator=g).to(word)
+    bits[0, :, :, 33], bits[0, :, :, 62] = (0x7f81, -127) if dtype == BF else (0x7f800001, -8388607)   # signalling
+    x = bits.view(dtype).cuda()
+    k, v = x[:, :, :H], x[:, :, H:]
+    P = (K + page - 1) // page
+    table = torch.arange(P, dtype=I32).view(1, P).cuda()
+
+    def rows(plane):
+        return plane.cpu().view(word).transpose(1, 2).reshape(-1, H, D)[:K]
+
+    for rot in (0, 32, 24, 22):
+        pool = torch.zeros(2, P, H, page, D, dtype=dtype, device="cuda")
+        gdn.kv_append_rope(k, v, pool[0], pool[1], dev([0]), table, freqs_of(rot).cuda() if rot else None)
+        assert torch.equal(rows(pool[1]), bits[0, :, H:])
+        assert torch.equal(rows(pool[0])[..., rot:], bits[0, :, :H, rot:])
+    y = torch.empty_like(x)
+    gdn.rope(x, y, freqs_of(32).cuda(), interleaved=True)
+    assert torch.equal(y.cpu().view(word)[..., 32:], bits[..., 32:])
+
+
+def test_more_tokens_than_a_grid_has_threads():
+    """2^30 tokens, of which only the last sequence's are there."""
+    say("2^30 tokens")
+    g = torch.Generator().manual_seed(12)
+    B, K, D, page = 65535, 16384, 64, 1024
+    k, v = (randn(g, 1, 1, 1, D, dtype=BF).cuda() for _ in range(2))
+    f, P = freqs_of(D).cuda(), K // page
+    count = torch.zeros(B, dtype=I32, device="cuda")
+    count[-1] = K
+    table = torch.full((B, P), -1, dtype=I32, device="cuda")
+    table[-1] = torch.arange(P - 1, -1, -1, dtype=I32)
+    pool = torch.zeros(2, P, 1, page, D, dtype=BF, device="cuda")
+    gdn.kv_append_rope(k.expand(B, K, 1, D), v.expand(B, K, 1, D), pool[0], pool[1], torch.zeros(B, dtype=I32, device="cuda"),
+                       table, f, count=count)
+    want = torch.empty(1, K, 1, D, dtype=BF, device="cuda")
+    gdn.rope(k.expand(1, K, 1, D), want, f)
+    assert torch.equal(pool[0].flip(0).view(K, D), want.view(K, D))
+    assert torch.equal(pool[1].view(K, D), v.view(1, D).expand(K, D))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("Hq,Hkv,D,rot,K", [(24, 4, 256, 64, 3001), (3, 1, 64, 64, 40001), (32, 8, 128, 128, 4100), (5, 2, 64, 24, 9000)])
 def test_one_call_and_many(Hq, Hkv, D, rot, K, dtype):
     """A long window in one call and in pieces: the same bits, however a launch is cut."""
