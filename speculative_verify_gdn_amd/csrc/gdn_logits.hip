@@ -11,15 +11,15 @@
 // One read of the logits and one write: memory bound, if the counts cost
 // little.  So a workgroup takes a slice of the vocabulary for some rows of one
 // sequence: it walks the text once, counts the tokens of its slice in LDS (16
-// bits each, 16 KB for 8192 tokens), and then streams; a bit map says which tokens have a
-// count or a bias, and a lane looks up those of its eight alone.
+// bits each, 16 KB for 8192 tokens), and then streams; a lane knows which of its tokens have a
+// count or a bias, and looks up those alone.
 // Every operation is one rounding of 32 bits in the order above, so that equal
 // logits stay equal and the best is the lowest of them.
 //
 // Measured: 64 rows of 131072, fp32, with noise and output (101 MB) 22.2 us, of which the stream 19.6 (5.1 TB/s);
 // 32 ragged windows of 8 rows of 131072, bf16, masks, biases and texts of 4000 (78 MB)
-// 24.4 us, and without text, biases, masks and best 14.0: the counting takes 4 us, the mask and the biases 2 each, the
-// search for the best 2.5, joining it 3.
+// 23.1 us: the counting and what it makes the stream look up take 2 us each, joining the best 2.5, a workgroup's reads before its
+// stream 3; without texts, biases, masks and best 14.0.
 // With the logits of the counted tokens left to a second kernel (a hash table a sequence) the stream was 1 us shorter, and
 // that kernel's scattered reads and writes took 13.
 #include "gdn_device.h"
@@ -249,11 +249,12 @@ __device__ __forceinline__ float only(float f, uint32_t bits, int e)
     return __int_as_float(__builtin_amdgcn_bitop3_b32(__float_as_int(f), (int)0xff800000, m, 0xe4));   // m ? f : -inf
 }
 
-// What is known of the tokens of a slice, in LDS: a bit map of those that need more than the mask and the temperature,
-// and their counts.  Narrow: 16 bits a token (14 of the count, one for a bias, one for a place in the text before
-// `start`), and a list of the slice's biases.  Wide: 32 bits a token, and a bias's entry for each; where a count may pass
-// 14 bits or the biases are more than a thread each (64 rows of 131072, fp32, texts of 1000: 20.1 us wide, 18.5
-// narrow; of 15000 36.5 and 25.0; 8 rows 7.8 and 7.5, 12.3 and 12.2).
+// What is known of the tokens of a slice, in LDS: their counts, and whether they stand in the text before `start` or have
+// a bias; a bit map of the drafted ones.  Narrow: 16 bits a token (14 of the count, one for a bias, one for the text before
+// `start`), and a list of the slice's biases; a token with a bias has its place in that list instead, and its count
+// there.  Wide: 32 bits a token, and a bias's entry for each; where a count may pass 14 bits or the biases are more
+// than a thread each (64 rows of 131072, fp32, texts of 1000: 20.1 us wide, 18.5 narrow; of 15000 36.5 and 25.0; 8
+// rows 7.8 and 7.5, 12.3 and 12.2).
 constexpr int kNarrowText = 16000;   // the longest text (with a window's drafts below 2^14)
 constexpr int kNarrowBias = kThreads;
 
@@ -262,9 +263,10 @@ struct Known {
     static constexpr int kBits = WIDE ? 32 : 16;
     static constexpr uint32_t kCount = (1u << (kBits - 2)) - 1, kBias = 1u << (kBits - 2), kSeen = 1u << (kBits - 1);
     uint32_t cnt[WIDE ? TOKENS : TOKENS / 2];
-    uint32_t bits[TOKENS / 32];
+    uint32_t drafted[TOKENS / 32];
     int entry[WIDE ? TOKENS : 1];
     float bias_value[WIDE ? 1 : kNarrowBias];
+    uint32_t bias_cnt[WIDE ? 1 : kNarrowBias];
     uint16_t bias_token[WIDE ? 1 : kNarrowBias];
     int biases[kWaves];
 
@@ -272,11 +274,11 @@ struct Known {
     {
         for (int i = threadIdx.x; i < (int)(sizeof(cnt) / 16); i += kThreads)
             reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < TOKENS / 32; i += kThreads) bits[i] = 0;
+        for (int i = threadIdx.x; i < TOKENS / 32; i += kThreads) drafted[i] = 0;
         if constexpr (WIDE)
             for (int i = threadIdx.x; i < TOKENS; i += kThreads) entry[i] = -1;
     }
-    __device__ __forceinline__ void touch(int u) { atomicOr(&bits[u >> 5], 1u << (u & 31)); }
+    __device__ __forceinline__ void draft(int u) { atomicOr(&drafted[u >> 5], 1u << (u & 31)); }
     __device__ __forceinline__ void add(int u, int n)
     {
         if constexpr (WIDE) atomicAdd(&cnt[u], (uint32_t)n);
@@ -287,14 +289,17 @@ struct Known {
         if constexpr (WIDE) atomicOr(&cnt[u], bit);
         else atomicOr(&cnt[u >> 1], bit << 16 * (u & 1));
     }
-    __device__ __forceinline__ uint32_t get(int u) const
+    __device__ __forceinline__ uint16_t& narrow(int u) { return reinterpret_cast<uint16_t*>(cnt)[u]; }
+    // the biases of the slice, in three steps with a barrier between each and the next; narrow: a thread has an entry, id
+    // and value
+    __device__ __forceinline__ unsigned long long ask_biases(const LogitsArgs& a, int v0, int nv, int id)
     {
-        if constexpr (WIDE) return cnt[u];
-        else return reinterpret_cast<const uint16_t*>(cnt)[u];
+        const unsigned long long which = __ballot((int)threadIdx.x < a.n_bias && (uint32_t)id - (uint32_t)v0 < (uint32_t)nv);
+        if (!WIDE && (threadIdx.x & 63) == 0) biases[threadIdx.x >> 6] = (int)__popcll(which);
+        return which;
     }
-    // the biases of the slice; narrow: listed in their order, a thread an entry (id, value), and their number is
-    // returned.  Every thread calls it.
-    __device__ __forceinline__ int take_biases(const LogitsArgs& a, int b, int v0, int nv, int id, float value)
+    __device__ __forceinline__ void take_biases(const LogitsArgs& a, int b, int v0, int nv, int id, float value,
+                                                unsigned long long which)
     {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
         if constexpr (WIDE) {
@@ -304,40 +309,127 @@ struct Known {
                 if (u < (uint32_t)nv) {
                     atomicMax(&entry[u], i);   // (a token named twice: its last entry)
                     mark(u, kBias);
-                    touch(u);
                 }
             }
-            return 0;
         } else {
-            const uint32_t u = (uint32_t)id - (uint32_t)v0;
-            const bool mine = tid < a.n_bias && u < (uint32_t)nv;
-            const unsigned long long which = __ballot(mine);
-            if (lane == 0) biases[wave] = (int)__popcll(which);
-            __syncthreads();
-            int base = 0, all = 0;
+            int at = 0;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
-                base += i < wave ? biases[i] : 0;
-                all += biases[i];
+            for (int i = 0; i < kWaves; ++i) at += i < wave ? biases[i] : 0;
+            if (which >> lane & 1) {
+                at += (int)__popcll(which & ((1ull << lane) - 1));
+                bias_token[at] = (uint16_t)(id - v0);
+                bias_value[at] = value;
             }
-            if (mine) {
-                base += (int)__popcll(which & ((1ull << lane) - 1));
-                bias_token[base] = (uint16_t)u;
-                bias_value[base] = value;
-                mark(u, kBias);
-                touch(u);
-            }
-            return all;
         }
     }
-    __device__ __forceinline__ float bias_of(const LogitsArgs& a, int b, int u, int listed) const
+    __device__ __forceinline__ void place_biases()
     {
-        if constexpr (WIDE) return a.bias_values[(size_t)b * a.n_bias + entry[u]];
-        int i = listed - 1;   // (a token named twice: its last entry)
-        while (bias_token[i] != u) --i;
-        return bias_value[i];
+        if constexpr (!WIDE) {
+            const int tid = threadIdx.x;
+            int all = 0;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) all += biases[i];
+            if (tid >= all) return;
+            const int u = bias_token[tid];
+            for (int i = tid + 1; i < all; ++i)
+                if (bias_token[i] == u) return;   // (a token named twice: its last entry)
+            bias_cnt[tid] = narrow(u);
+            narrow(u) = (uint16_t)(kBias | tid);
+        }
+    }
+    // n more of a token, once the biases are in place
+    __device__ __forceinline__ void add_later(int u, int n)
+    {
+        if constexpr (!WIDE) {
+            const uint32_t c = narrow(u);
+            if (c & kBias) {
+                atomicAdd(&bias_cnt[c & (kNarrowBias - 1)], (uint32_t)n);
+                return;
+            }
+        }
+        add(u, n);
+    }
+    // which of eight tokens from u on need more than the mask and the temperature
+    __device__ __forceinline__ uint32_t which(int u) const
+    {
+        uint32_t some = reinterpret_cast<const uint8_t*>(drafted)[u >> 3];
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) some |= min(cnt[u + e], 1u) << e;
+        } else {
+            uint32_t two = 0;   // bits 0 and 16: the first two, ...
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = cnt[(u >> 1) + i];
+                two |= (min(w & 0xffffu, 1u) | min(w >> 16, 1u) << 1) << 2 * i;
+            }
+            some |= two;
+        }
+        return some;
+    }
+    // what is known of a token: its count with kSeen, and its bias (if it has one)
+    __device__ __forceinline__ uint32_t look(const LogitsArgs& a, int b, int u, bool& biased, float& bias) const
+    {
+        uint32_t c;
+        if constexpr (WIDE) c = cnt[u];
+        else c = reinterpret_cast<const uint16_t*>(cnt)[u];
+        biased = c & kBias;
+        if (biased) {
+            if constexpr (WIDE) {
+                c &= ~kBias;
+                bias = a.bias_values[(size_t)b * a.n_bias + entry[u]];
+            } else {
+                const int i = c & (kNarrowBias - 1);
+                c = bias_cnt[i];
+                bias = bias_value[i];
+            }
+        }
+        return c;
     }
 };
+
+// The i-th workgroup's sequence and rows t0 to t1, at most a.rows of them; false: there are none.  Windows differ in length;
+// where the sequences are few, those with all their rows come first and the shorter ones behind them, so that each CU gets
+// about the same number of rows (32 windows of 1 to 8 rows of 131072: 7 to 10 rows a CU where it was 4 to 14, 24.6 to 23.2
+// us).
+__device__ __forceinline__ bool rows_of(const LogitsArgs& a, int i, int& b, int& t0, int& t1)
+{
+    if (a.count && a.B <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int count = lane < a.B ? clamp_count(a.count, lane, a.K) : 0;
+        const int full = count / a.rows, rest = count - full * a.rows;
+        int upto = full;   // of this and the sequences before
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int before = __shfl_up(upto, d, 64);
+            upto += lane >= d ? before : 0;
+        }
+        const int all = __shfl(upto, 63, 64);
+        int g;
+        if (i < all) {
+            b = (int)__popcll(__ballot(upto <= i));
+            g = i - __shfl(upto - full, b, 64);
+        } else {
+            const unsigned long long rests = __ballot(rest > 0);
+            const int rank = (int)__popcll(rests & ((1ull << lane) - 1));
+            const unsigned long long it = __ballot(rest > 0 && rank == i - all);
+            if (it == 0) return false;
+            b = __ffsll((long long)it) - 1;
+            g = __shfl(full, b, 64);
+        }
+        b = __builtin_amdgcn_readfirstlane(b);
+        t0 = __builtin_amdgcn_readfirstlane(g * a.rows);
+        t1 = min(t0 + a.rows, __builtin_amdgcn_readfirstlane(__shfl(count, b, 64)));
+        return true;
+    }
+    // (a CU gets workgroups that lie a fixed number apart: with the sequences shifted from one g to the next these are of
+    // different sequences)
+    const int g = i / a.B;
+    b = (i - g * a.B + 5 * g) % a.B;
+    t0 = g * a.rows;
+    t1 = min(t0 + a.rows, clamp_count(a.count, b, a.K));
+    return t0 < t1;
+}
 
 // 2048 VECTORS tokens of the vocabulary, for some rows of one sequence: a thread has eight of each 2048.
 template <int VECTORS, bool WIDE, bool XBF16, bool OBF16, bool NOISE>
@@ -350,24 +442,24 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     __shared__ int draft[kKvWindowMax];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    // Rows g * a.rows on of sequence b.  Windows differ in length, so the later g are the emptier; a CU gets workgroups that
-    // lie a fixed number apart, and with the sequences shifted from one g to the next these are of different sequences.
-    const int g = blockIdx.y / a.B, b = (blockIdx.y - g * a.B + 5 * g) % a.B;
-    const int t0 = g * a.rows, t1 = min(t0 + a.rows, clamp_count(a.count, b, a.K));
-    if (t0 >= t1) return;
+    int b, t0, t1;
+    if (!rows_of(a, blockIdx.y, b, t0, t1)) return;
     const size_t row0 = (size_t)b * a.K;
     const int v0 = blockIdx.x * kTokens, nv = min(kTokens, a.V - v0);
 
     // What the counting needs is asked for first: reads come back in their order, and those of the logits take longer
     // (64 rows of 131072, fp32: 22.5 to 22.1 us).
-    const Params p(a.params, b);
     const bool marks = a.marks, texts = marks && a.params && a.history, drafts = marks && a.params && a.tokens;
     const int32_t* h = a.history + (size_t)b * a.capacity;
     // four tokens of the text from index i on, or its last four where there are fewer behind i
     auto four = [&](int i) { return *reinterpret_cast<const u32x4_any_t*>(h + min(i, a.capacity - 4)); };
     u32x4_any_t text = {0, 0, 0, 0};
-    int drafted = -1, above = -1, id = -1;
+    int drafted = -1, above = -1, id = -1, len = 0, start = 0;
     float value = 0.0f;
+    if (texts) {
+        len = min(max(a.history_lens[b], 0), a.capacity);
+        if (a.history_start) start = a.history_start[b];
+    }
     if (texts && a.capacity >= 4) text = four(tid * 4);
     if (drafts && wave == kWaves - 1) {
         drafted = lane < a.K ? a.tokens[row0 + lane] : -1;
@@ -393,47 +485,60 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     };
     load(even);
     load(odd);
+    const Params p(a.params, b);
 
     unsigned long long inside = 0;
-    int listed = 0;
+    uint32_t some = 0;   // a byte for each of the thread's vectors: the tokens of which something is known
     if (tid < kKvWindowMax) best[tid] = 0;
-    if (marks) known.clear();
+    unsigned long long biased_here = 0;
+    if (marks) {
+        known.clear();
+        if (a.n_bias > 0) biased_here = known.ask_biases(a, v0, nv, id);
+    }
     __syncthreads();
     if (marks) {
+        if (a.n_bias > 0) known.take_biases(a, b, v0, nv, id, value, biased_here);
         if (texts) {
-            const int len = min(max(a.history_lens[b], 0), a.capacity);
-            const int start = a.history_start ? a.history_start[b] : 0;
-            auto count = [&](int token, int i) {
+            auto count = [&](int token, bool since) {
                 const uint32_t u = (uint32_t)token - (uint32_t)v0;
                 if (u < (uint32_t)nv) {
-                    known.touch(u);
-                    if (i >= start) known.add(u, 1);
+                    if (since) known.add(u, 1);
                     else known.mark(u, K::kSeen);
                 }
             };
             if (a.capacity >= 4) {
                 for (int i = tid * 4; i < len; i += kThreads * 4) {
                     if (i >= kThreads * 4) text = four(i);
-                    const int from = min(i, a.capacity - 4);   // (see four)
+                    if (i >= start && i + 4 <= len) {   // (nearly all)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (from + e >= i && from + e < len) count((int)text[e], from + e);
+                        for (int e = 0; e < 4; ++e) count((int)text[e], true);
+                    } else {
+                        const int from = min(i, a.capacity - 4);   // (see four)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (from + e >= i && from + e < len) count((int)text[e], from + e >= start);
+                    }
                 }
             } else if (tid < len) {
-                count(h[tid], tid);
+                count(h[tid], tid >= start);
             }
         }
         if (wave == kWaves - 1) {   // the path to each node, and the drafted tokens of this slice
             const bool here = drafted >= v0 && drafted - v0 < nv;
             paths[lane] = drafts ? node_paths(above, a.K) : 0;
             draft[lane] = drafted - v0;
-            if (here) known.touch(drafted - v0);
+            if (here) known.draft(drafted - v0);
             const unsigned long long which = __ballot(here);
             if (lane == 0) inside_s = which;
         }
-        if (a.n_bias > 0) listed = known.take_biases(a, b, v0, nv, id, value);
         __syncthreads();
+        if (!WIDE && a.n_bias > 0) {
+            known.place_biases();
+            __syncthreads();
+        }
         inside = inside_s;
+#pragma unroll
+        for (int i = 0; i < VECTORS; ++i) some |= known.which((i * kThreads + tid) * 8) << 8 * i;
     }
 
     const size_t out_step = a.out_stride * (OBF16 ? 2 : 4);
@@ -446,7 +551,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
         const unsigned long long mine = paths[t] & inside;
         if (mine == 0) return;
         __syncthreads();
-        if (tid < 64 && (mine >> tid & 1)) known.add(draft[tid], n);
+        if (tid < 64 && (mine >> tid & 1)) known.add_later(draft[tid], n);
         __syncthreads();
     };
     // one vector of eight: the j-th of row t
@@ -466,15 +571,17 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
             }
             if (marks) {
                 // one known token of each lane at a time: most have none, few have two
-                for (uint32_t left = reinterpret_cast<const uint8_t*>(known.bits)[k >> 3]; left; left &= left - 1) {
+                for (uint32_t left = some >> 8 * j & 0xffu; left; left &= left - 1) {
                     const int e = __ffs(left) - 1;
-                    const uint32_t c = known.get(k + e), n = c & K::kCount;
+                    bool biased;
+                    float bias = 0.0f;
+                    const uint32_t c = known.look(a, b, k + e, biased, bias), n = c & K::kCount;
                     float x = f[0];
 #pragma unroll
                     for (int i = 1; i < 8; ++i) x = i == e ? f[i] : x;
-                    if (c & ~K::kBias) x *= x > 0.0f ? p.less : p.rep;
+                    if (c) x *= x > 0.0f ? p.less : p.rep;
                     if (n) x -= p.frequency * (float)n + p.presence;
-                    if (c & K::kBias) x += known.bias_of(a, b, k + e, listed);
+                    if (biased) x += bias;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = i == e ? x : f[i];
                 }

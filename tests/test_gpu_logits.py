@@ -141,6 +141,39 @@ def test_logits_past_2_31():
     assert int(best[100, 7]) == 0 and float(x[100, 7].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("B,K,V", [(64, 8, 9000), (65, 8, 9000), (33, 64, 2500), (5, 64, 33000), (64, 3, 2048), (1, 64, 140000)])
+@pytest.mark.parametrize("counts", ["any", "none", "last", "one"])
+def test_windows_of_every_length(B, K, V, counts):
+    """Which rows a workgroup takes goes by the windows' lengths: every row that is there is right, no other is touched."""
+    say("windows", B, K, V, counts)
+    r = random.Random(B * K)
+    c = case(B, B, K, V, 20, BF, tree=True, mask=False)
+    c["count"] = torch.tensor({"any": [r.randint(-1, K + 1) for _ in range(B)], "none": [0] * B, "last": [0] * (B - 1) + [K],
+                               "one": [1] * B}[counts], dtype=I32)
+    out, b = run(c, BF)
+    del c["params"]                                      # (the adjusting itself is tested above)
+    plain, pb = run({k: v for k, v in c.items() if k != "count"}, BF)
+    there = torch.arange(K)[None] < c["count"][:, None]
+    assert bool((out.cpu()[~there] == 9.0).all()) and bool((b.cpu()[~there] == -7).all())
+    assert not bool((out.cpu()[there] == 9.0).all(-1).any()) and bool((b.cpu()[there] >= 0).all())
+    out, b = run(c, BF)
+    assert torch.equal(out.cpu()[there], plain.cpu()[there]) and torch.equal(b.cpu()[there], pb.cpu()[there])
+    assert bool((out.cpu()[~there] == 9.0).all()) and bool((b.cpu()[~there] == -7).all())
+
+
+@pytest.mark.parametrize("B,K,V,n_bias", [(2, 5, 300, 256), (1, 16, 70, 256), (3, 2, 300, 257), (2, 9, 9000, 200)])
+def test_biases_of_many_tokens(B, K, V, n_bias):
+    """Most tokens have a bias, many ids are named twice or more, and the drafted tokens and the text's have one too."""
+    say("biases", B, K, V, n_bias)
+    for seed in range(4):
+        c = case(seed, B, K, V, 90, F32, tree=bool(seed & 1), n_bias=n_bias)
+        c["ids"][:, ::3] = torch.randint(0, min(V, 40), c["ids"][:, ::3].shape).to(I32)
+        c["tokens"] = c["ids"][:, torch.arange(K) % n_bias].clone()
+        c["history"][:, ::2] = c["ids"][:, torch.arange(45) % n_bias]
+        out, b = run(c, F32)
+        check(c, out, b, F32)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_one_of_the_outputs_and_in_place(dtype):
     say("logits outputs", dtype)
