@@ -253,10 +253,11 @@ __device__ __forceinline__ float only(float f, uint32_t bits, int e)
 // a bias; a bit map of the drafted ones.  Narrow: 16 bits a token (14 of the count, one for a bias, one for the text before
 // `start`), and a list of the slice's biases; a token with a bias has its place in that list instead, and its count
 // there.  Wide: 32 bits a token, and a bias's entry for each; where a count may pass 14 bits or the biases are more
-// than a thread each (64 rows of 131072, fp32, texts of 1000: 20.1 us wide, 18.5 narrow; of 15000 36.5 and 25.0; 8
+// than two a thread (64 rows of 131072, fp32, texts of 1000: 20.1 us wide, 18.5 narrow; of 15000 36.5 and 25.0; 8
 // rows 7.8 and 7.5, 12.3 and 12.2).
 constexpr int kNarrowText = 16000;   // the longest text (with a window's drafts below 2^14)
-constexpr int kNarrowBias = kThreads;
+constexpr int kNarrowBias = 2 * kThreads;
+constexpr int kEach = kNarrowBias / kThreads;   // biases of a thread
 
 template <bool WIDE, int TOKENS>
 struct Known {
@@ -266,9 +267,9 @@ struct Known {
     uint32_t drafted[TOKENS / 32];
     int entry[WIDE ? TOKENS : 1];
     float bias_value[WIDE ? 1 : kNarrowBias];
-    uint32_t bias_cnt[WIDE ? 1 : kNarrowBias];
+    uint32_t bias_cnt[WIDE ? 1 : kNarrowBias / 2];   // (16 bits each)
     uint16_t bias_token[WIDE ? 1 : kNarrowBias];
-    int biases[kWaves];
+    int biases[kEach * kWaves];
 
     __device__ __forceinline__ void clear()
     {
@@ -278,28 +279,33 @@ struct Known {
         if constexpr (WIDE)
             for (int i = threadIdx.x; i < TOKENS; i += kThreads) entry[i] = -1;
     }
+    static __device__ __forceinline__ void add16(uint32_t* p, int i, int n) { atomicAdd(&p[i >> 1], (uint32_t)n << 16 * (i & 1)); }
+    static __device__ __forceinline__ uint16_t& at16(uint32_t* p, int i) { return reinterpret_cast<uint16_t*>(p)[i]; }
     __device__ __forceinline__ void draft(int u) { atomicOr(&drafted[u >> 5], 1u << (u & 31)); }
     __device__ __forceinline__ void add(int u, int n)
     {
         if constexpr (WIDE) atomicAdd(&cnt[u], (uint32_t)n);
-        else atomicAdd(&cnt[u >> 1], (uint32_t)n << 16 * (u & 1));
+        else add16(cnt, u, n);
     }
     __device__ __forceinline__ void mark(int u, uint32_t bit)
     {
         if constexpr (WIDE) atomicOr(&cnt[u], bit);
         else atomicOr(&cnt[u >> 1], bit << 16 * (u & 1));
     }
-    __device__ __forceinline__ uint16_t& narrow(int u) { return reinterpret_cast<uint16_t*>(cnt)[u]; }
-    // the biases of the slice, in three steps with a barrier between each and the next; narrow: a thread has an entry, id
-    // and value
-    __device__ __forceinline__ unsigned long long ask_biases(const LogitsArgs& a, int v0, int nv, int id)
+    // The biases of the slice, in three steps with a barrier between each and the next; narrow: entries tid, tid + kThreads,
+    // ... are the thread's, id and value.
+    __device__ __forceinline__ void ask_biases(const LogitsArgs& a, int v0, int nv, const int* id, unsigned long long* which)
     {
-        const unsigned long long which = __ballot((int)threadIdx.x < a.n_bias && (uint32_t)id - (uint32_t)v0 < (uint32_t)nv);
-        if (!WIDE && (threadIdx.x & 63) == 0) biases[threadIdx.x >> 6] = (int)__popcll(which);
-        return which;
+        const int tid = threadIdx.x;
+        if constexpr (!WIDE)
+#pragma unroll
+            for (int r = 0; r < kEach; ++r) {
+                which[r] = __ballot(tid + r * kThreads < a.n_bias && (uint32_t)id[r] - (uint32_t)v0 < (uint32_t)nv);
+                if ((tid & 63) == 0) biases[r * kWaves + (tid >> 6)] = (int)__popcll(which[r]);
+            }
     }
-    __device__ __forceinline__ void take_biases(const LogitsArgs& a, int b, int v0, int nv, int id, float value,
-                                                unsigned long long which)
+    __device__ __forceinline__ void take_biases(const LogitsArgs& a, int b, int v0, int nv, const int* id, const float* value,
+                                                const unsigned long long* which)
     {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
         if constexpr (WIDE) {
@@ -312,38 +318,41 @@ struct Known {
                 }
             }
         } else {
-            int at = 0;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) at += i < wave ? biases[i] : 0;
-            if (which >> lane & 1) {
-                at += (int)__popcll(which & ((1ull << lane) - 1));
-                bias_token[at] = (uint16_t)(id - v0);
-                bias_value[at] = value;
+            for (int r = 0; r < kEach; ++r) {
+                int at = (int)__popcll(which[r] & ((1ull << lane) - 1));
+#pragma unroll
+                for (int i = 0; i < kEach * kWaves; ++i) at += i < r * kWaves + wave ? biases[i] : 0;
+                if (which[r] >> lane & 1) {
+                    bias_token[at] = (uint16_t)(id[r] - v0);
+                    bias_value[at] = value[r];
+                }
             }
         }
     }
     __device__ __forceinline__ void place_biases()
     {
         if constexpr (!WIDE) {
-            const int tid = threadIdx.x;
             int all = 0;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) all += biases[i];
-            if (tid >= all) return;
-            const int u = bias_token[tid];
-            for (int i = tid + 1; i < all; ++i)
-                if (bias_token[i] == u) return;   // (a token named twice: its last entry)
-            bias_cnt[tid] = narrow(u);
-            narrow(u) = (uint16_t)(kBias | tid);
+            for (int i = 0; i < kEach * kWaves; ++i) all += biases[i];
+            for (int i = threadIdx.x; i < all; i += kThreads) {
+                const int u = bias_token[i];
+                int j = i + 1;
+                while (j < all && bias_token[j] != u) ++j;
+                if (j < all) continue;   // (a token named twice: its last entry)
+                at16(bias_cnt, i) = at16(cnt, u);
+                at16(cnt, u) = (uint16_t)(kBias | i);
+            }
         }
     }
     // n more of a token, once the biases are in place
     __device__ __forceinline__ void add_later(int u, int n)
     {
         if constexpr (!WIDE) {
-            const uint32_t c = narrow(u);
+            const uint32_t c = at16(cnt, u);
             if (c & kBias) {
-                atomicAdd(&bias_cnt[c & (kNarrowBias - 1)], (uint32_t)n);
+                add16(bias_cnt, c & (kNarrowBias - 1), n);
                 return;
             }
         }
@@ -380,7 +389,7 @@ struct Known {
                 bias = a.bias_values[(size_t)b * a.n_bias + entry[u]];
             } else {
                 const int i = c & (kNarrowBias - 1);
-                c = bias_cnt[i];
+                c = reinterpret_cast<const uint16_t*>(bias_cnt)[i];
                 bias = bias_value[i];
             }
         }
@@ -454,8 +463,8 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     // four tokens of the text from index i on, or its last four where there are fewer behind i
     auto four = [&](int i) { return *reinterpret_cast<const u32x4_any_t*>(h + min(i, a.capacity - 4)); };
     u32x4_any_t text = {0, 0, 0, 0};
-    int drafted = -1, above = -1, id = -1, len = 0, start = 0;
-    float value = 0.0f;
+    int drafted = -1, above = -1, id[kEach] = {}, len = 0, start = 0;
+    float value[kEach] = {};
     if (texts) {
         len = min(max(a.history_lens[b], 0), a.capacity);
         if (a.history_start) start = a.history_start[b];
@@ -465,10 +474,13 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
         drafted = lane < a.K ? a.tokens[row0 + lane] : -1;
         above = node_above(a.parent ? a.parent + row0 : nullptr, a.K);
     }
-    if (!WIDE && tid < a.n_bias) {
-        id = a.bias_ids[(size_t)b * a.n_bias + tid];
-        value = a.bias_values[(size_t)b * a.n_bias + tid];
-    }
+    if constexpr (!WIDE)
+#pragma unroll
+        for (int r = 0; r < kEach; ++r)
+            if (tid + r * kThreads < a.n_bias) {
+                id[r] = a.bias_ids[(size_t)b * a.n_bias + tid + r * kThreads];
+                value[r] = a.bias_values[(size_t)b * a.n_bias + tid + r * kThreads];
+            }
 
     // the first two vectors of eight are on their way while the text is counted, later ones two ahead
     const int vectors = (nv + 8 * kThreads - 1) / (8 * kThreads);
@@ -490,10 +502,10 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     unsigned long long inside = 0;
     uint32_t some = 0;   // a byte for each of the thread's vectors: the tokens of which something is known
     if (tid < kKvWindowMax) best[tid] = 0;
-    unsigned long long biased_here = 0;
+    unsigned long long biased_here[kEach];
     if (marks) {
         known.clear();
-        if (a.n_bias > 0) biased_here = known.ask_biases(a, v0, nv, id);
+        if (a.n_bias > 0) known.ask_biases(a, v0, nv, id, biased_here);
     }
     __syncthreads();
     if (marks) {

@@ -161,7 +161,7 @@ def test_windows_of_every_length(B, K, V, counts):
     assert bool((out.cpu()[~there] == 9.0).all()) and bool((b.cpu()[~there] == -7).all())
 
 
-@pytest.mark.parametrize("B,K,V,n_bias", [(2, 5, 300, 256), (1, 16, 70, 256), (3, 2, 300, 257), (2, 9, 9000, 200)])
+@pytest.mark.parametrize("B,K,V,n_bias", [(2, 5, 300, 256), (1, 16, 70, 256), (3, 2, 300, 257), (2, 9, 9000, 200), (2, 5, 300, 512), (3, 2, 300, 513)])
 def test_biases_of_many_tokens(B, K, V, n_bias):
     """Most tokens have a bias, many ids are named twice or more, and the drafted tokens and the text's have one too."""
     say("biases", B, K, V, n_bias)
