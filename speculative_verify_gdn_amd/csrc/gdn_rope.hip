@@ -129,13 +129,15 @@ struct Token {
     long long to[3];    // the same where it goes; below 0: nowhere
 };
 
-// E: elements of a piece; NP: pairs of pieces of a lane; STREAM: past the caches
-template <bool BF16, int E, int NP, bool INTERLEAVED, bool STREAM>
+// E: elements of a piece; NP: pairs of pieces of a lane; STREAM: past the caches; LANES: the tokens are looked after by a
+// lane each, not by a wave
+template <bool BF16, int E, int NP, bool INTERLEAVED, bool STREAM, bool LANES>
 __device__ __forceinline__ void rope_heads(const RopeArgs& a)
 {
     constexpr int ES = BF16 ? 2 : 4;
     constexpr int PE = E > 1 ? E / 2 : 1;   // pairs within a piece (neighbours)
     __shared__ Token info[kTileMax];
+    __shared__ long long where[LANES ? kTileMax : 1];
     __shared__ float cs[kAngles], sn[kAngles];
     __shared__ float weight[2][kRopeHeadMax];
 
@@ -196,40 +198,62 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
                 v[k].load(x + bt[k] * ES);
             }
     };
-    // where each token stands and goes, and its sines: a wave a token, or several waves where there are fewer tokens
-    const int share = max(kWaves / a.tile, 1), sub = wave % share;
-    for (int i = wave / share; i < n; i += kWaves / share) {
-        const uint32_t tok = first + i;
-        const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
-        const int32_t parent = a.parent && lane < a.K ? a.parent[(size_t)b * a.K + lane] : -1;
-        const int j0 = lane + 64 * sub;
-        const double freq = j0 < half ? a.freqs[j0] : 0.0;
-        const long long len = a.lens ? max(a.lens[b], 0) : 0;
-        const bool there = !a.count || t < a.count[b];
-        if (sub == 0) {
-            long long page_at = -1;
-            if (a.table) {
-                const long long at = len + t, slot = at >> a.g.page_log2;
-                const int id = slot < a.P ? a.table[(size_t)b * a.P + slot] : -1;
-                if ((unsigned)id < (unsigned)a.g.n_pages)
-                    page_at = ((((long long)id * a.g.Hkv) << a.g.page_log2) + (at & ((1 << a.g.page_log2) - 1))) *
-                              a.g.row_bytes;
-            }
-            if (lane < 3) {
-                const RopePart& r = a.part[lane];
-                info[i].from[lane] = b * r.xs[0] + t * r.xs[1];
-                info[i].to[lane] = !there ? -1 : r.paged ? page_at : b * r.ys[0] + t * r.ys[1];
-            }
+    // the byte offset of a sequence's place `at` in a plane of the cache, below 0: it has no page
+    auto page_of = [&](int b, long long at) -> long long {
+        const long long slot = at >> a.g.page_log2;
+        const int id = slot < a.P ? a.table[(size_t)b * a.P + slot] : -1;
+        if ((unsigned)id >= (unsigned)a.g.n_pages) return -1;
+        return ((((long long)id * a.g.Hkv) << a.g.page_log2) + (at & ((1 << a.g.page_log2) - 1))) * a.g.row_bytes;
+    };
+    // the i-th token of the workgroup, token t of sequence b, in a part
+    auto place = [&](int i, int part, int b, int t, bool there, long long page_at) {
+        const RopePart& r = a.part[part];
+        info[i].from[part] = b * r.xs[0] + t * r.xs[1];
+        info[i].to[part] = !there ? -1 : r.paged ? page_at : b * r.ys[0] + t * r.ys[1];
+    };
+    // the sine and cosine of its pair j
+    auto angle = [&](int i, int j, long long p, double freq) {
+        const double turns = (double)p * freq * kInv2Pi;
+        float s, c;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        cs[i * half + j] = a.mscale * c;
+        sn[i * half + j] = a.mscale * s;
+    };
+    if constexpr (LANES) {   // a lane a token, then its pairs side by side with those of other tokens
+        const int j = threadIdx.x & ((1 << a.half_log2) - 1);
+        const double freq = j < half ? a.freqs[j] : 0.0;
+        if (threadIdx.x < n) {
+            const int i = threadIdx.x;
+            const uint32_t tok = first + i;
+            const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
+            const long long len = a.lens ? max(a.lens[b], 0) : 0;
+            const bool there = !a.count || t < a.count[b];
+            where[i] = a.pos ? (long long)a.pos[tok] : len + t;
+            const long long page_at = a.table ? page_of(b, len + t) : -1;
+#pragma unroll
+            for (int part = 0; part < 3; ++part) place(i, part, b, t, there, page_at);
         }
-        const long long p = a.pos      ? (long long)a.pos[tok]
-                            : a.parent ? len + node_depth(parent, a.K, t)
-                                       : len + t;
-        for (int j = j0; j < half; j += 64 * share) {
-            const double turns = (double)p * (j == j0 ? freq : a.freqs[j]) * kInv2Pi;
-            float s, c;
-            sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-            cs[i * half + j] = a.mscale * c;
-            sn[i * half + j] = a.mscale * s;
+        __syncthreads();
+        if (j < half)
+            for (int i = threadIdx.x >> a.half_log2; i < n; i += kThreads >> a.half_log2) angle(i, j, where[i], freq);
+    } else {   // a wave a token, or several waves where there are fewer tokens
+        const int share = max(kWaves / a.tile, 1), sub = wave % share;
+        for (int i = wave / share; i < n; i += kWaves / share) {
+            const uint32_t tok = first + i;
+            const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
+            const int32_t parent = a.parent && lane < a.K ? a.parent[(size_t)b * a.K + lane] : -1;
+            const int j0 = lane + 64 * sub;
+            const double freq = j0 < half ? a.freqs[j0] : 0.0;
+            const long long len = a.lens ? max(a.lens[b], 0) : 0;
+            const bool there = !a.count || t < a.count[b];
+            if (sub == 0) {
+                const long long page_at = a.table ? page_of(b, len + t) : -1;
+                if (lane < 3) place(i, lane, b, t, there, page_at);
+            }
+            const long long p = a.pos      ? (long long)a.pos[tok]
+                                : a.parent ? len + node_depth(parent, a.K, t)
+                                           : len + t;
+            for (int j = j0; j < half; j += 64 * share) angle(i, j, p, j == j0 ? freq : a.freqs[j]);
         }
     }
 #pragma unroll
@@ -310,18 +334,28 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
 }
 
 // Eight waves a SIMD: with six (ten registers more) the large windows took 3 to 6% longer.
-template <bool BF16, bool INTERLEAVED, bool STREAM>
+template <bool BF16, bool INTERLEAVED, bool STREAM, bool LANES>
 __global__ __launch_bounds__(kThreads, 8) void rope_kernel(RopeArgs a)
 {
-    rope_heads<BF16, BF16 ? 8 : 4, 1, INTERLEAVED, STREAM>(a);
+    rope_heads<BF16, BF16 ? 8 : 4, 1, INTERLEAVED, STREAM, LANES>(a);
 }
 
 // Pieces of 8 bytes, and element by element: for turned parts that no whole pairs of 16 bytes make up (8192 tokens of
 // 32 heads of 96, bf16: 32 elements of each turned 27 us, 24 of them 42, 22 102).
-template <bool BF16, int E, int NP, bool INTERLEAVED>
+template <bool BF16, int E, int NP, bool INTERLEAVED, bool LANES>
 __global__ __launch_bounds__(kThreads) void rope_narrow_kernel(RopeArgs a)
 {
-    rope_heads<BF16, E, NP, INTERLEAVED, false>(a);
+    rope_heads<BF16, E, NP, INTERLEAVED, false, LANES>(a);
+}
+
+template <bool BF16, bool INTERLEAVED, bool LANES>
+void launch(const RopeArgs& a, int e, bool stream, dim3 grid, hipStream_t s)
+{
+    constexpr int E = BF16 ? 8 : 4;
+    if (e == 1) rope_narrow_kernel<BF16, 1, 4, INTERLEAVED, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
+    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, INTERLEAVED, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
+    else if (stream) rope_kernel<BF16, INTERLEAVED, true, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
+    else rope_kernel<BF16, INTERLEAVED, false, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
 }
 
 int log2_up(int n)
@@ -355,11 +389,16 @@ void launch(RopeArgs& a, hipStream_t s)
     while (chunks > 1 && tiles * chunks > 1024) chunks = (chunks + 1) / 2;
     a.chunk = (a.heads + chunks - 1) / chunks;
     const dim3 grid((unsigned)min(tiles, kGridX), (a.heads + a.chunk - 1) / a.chunk, (unsigned)((tiles + kGridX - 1) / kGridX));
-    const bool stream = (long long)tokens * a.heads * a.D * (BF16 ? 2 : 4) > kStreamBytes;
-    if (e == 1) rope_narrow_kernel<BF16, 1, 4, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
-    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, INTERLEAVED><<<grid, dim3(kThreads), 0, s>>>(a);
-    else if (stream) rope_kernel<BF16, INTERLEAVED, true><<<grid, dim3(kThreads), 0, s>>>(a);
-    else rope_kernel<BF16, INTERLEAVED, false><<<grid, dim3(kThreads), 0, s>>>(a);
+    a.half_log2 = log2_up(half);
+    // Past the caches go accesses of whole lines, or of runs of 64 bytes and at least 128: parts of lines are joined in the
+    // caches (13278 tokens of 30 heads of 128, bf16, 32 elements turned: 69 us past them, 53 through them; 40562 of 24 of 64
+    // 74 and 58; but 16384 of 32 of 256, 64 turned, runs of 64 and 192, 45.8 and 48.7).
+    const int es = BF16 ? 2 : 4, run = half * es, rest = (a.D - a.rot) / 2 * es;
+    const bool stream = (long long)tokens * a.heads * a.D * es > kStreamBytes && (run | rest) % 64 == 0 && max(run, rest) >= 128;
+    // A lane a token where a workgroup has more of them than waves (110304 tokens of 4 heads of 96: 67 us with a wave a token,
+    // 48 with a lane); the depth in a tree takes a wave.
+    if (a.tile > kWaves && (a.pos || !a.parent)) launch<BF16, INTERLEAVED, true>(a, e, stream, grid, s);
+    else launch<BF16, INTERLEAVED, false>(a, e, stream, grid, s);
 }
 
 }  // namespace

@@ -39,6 +39,7 @@ struct RopeArgs {
     int tile;        // tokens of a workgroup
     int chunk;       // heads of a workgroup
     int lanes_log2;  // lanes of one head
+    int half_log2;   // lanes of one token's pairs
 };
 
 struct LogitsArgs {

@@ -351,6 +351,33 @@ def test_bits_that_stay(K, dtype):
     assert torch.equal(y.cpu().view(word)[..., 32:], bits[..., 32:])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mode", ["pos", "lens", "chain", "tree"])
+@pytest.mark.parametrize("B,K,H,D,rot", [(40, 600, 2, 64, 64), (301, 41, 3, 96, 24), (1, 9001, 1, 48, 22), (700, 13, 1, 512, 512), (5000, 3, 1, 16, 2)])
+def test_many_tokens_of_few_heads(B, K, H, D, rot, mode, dtype):
+    """Workgroups of many tokens, across the ends of sequences."""
+    say("few heads", B, K, H, D, rot, mode, dtype)
+    if mode == "tree" and K > 64:
+        B, K = B * K // 50 + 1, 50
+    g, r = torch.Generator().manual_seed(B), random.Random(K)
+    x, f = randn(g, B, K, H, D, dtype=dtype), freqs_of(rot)
+    kw = {}
+    if mode == "pos":
+        kw["pos"] = [[r.randint(-5000, 100000) for _ in range(K)] for _ in range(B)]
+    if mode != "chain":
+        kw["lens"] = [r.choice([0, -3, 77, 200000]) for _ in range(B)]
+    if mode == "tree":
+        kw["parent"] = trees(B, K, D)
+    count = [r.choice([0, 1, K, K + 7]) for _ in range(B)]
+    y = torch.full((B, K, H, D), 9.0, dtype=dtype).cuda()
+    gdn.rope(x.cuda(), y, f.cuda(), count=dev(count), **{k: dev(v) for k, v in kw.items()})
+    where = kw["pos"] if mode == "pos" else ref.positions(B, K, **kw)
+    want, off = ref.turned(x, where, f)
+    there = torch.arange(K)[None] < torch.tensor(count)[:, None]
+    check(y.cpu(), want, off, dtype, there)
+    assert bool((y.cpu()[~there] == 9.0).all())
+
+
 def test_more_tokens_than_a_grid_has_threads():
     """2^30 tokens, of which only the last sequence's are there."""
     say("2^30 tokens")
