@@ -292,7 +292,7 @@ struct Known {
         if constexpr (WIDE) atomicOr(&cnt[u], bit);
         else atomicOr(&cnt[u >> 1], bit << 16 * (u & 1));
     }
-    // The biases of the slice, in three steps with a barrier between each and the next; narrow: entries tid, tid + kThreads,
+    // The biases of the slice, in four steps with a barrier between each and the next; narrow: entries tid, tid + kThreads,
     // ... are the thread's, id and value.
     __device__ __forceinline__ void ask_biases(const LogitsArgs& a, int v0, int nv, const int* id, unsigned long long* which)
     {
@@ -330,21 +330,35 @@ struct Known {
             }
         }
     }
+    // (a token named twice: all of its entries have its count, and its word the last one's place)
+    __device__ __forceinline__ int listed() const
+    {
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < kEach * kWaves; ++i) all += biases[i];
+        return all;
+    }
+    __device__ __forceinline__ void count_biases()
+    {
+        if constexpr (!WIDE)
+            for (int i = threadIdx.x, all = listed(); i < all; i += kThreads) at16(bias_cnt, i) = at16(cnt, bias_token[i]);
+    }
     __device__ __forceinline__ void place_biases()
     {
-        if constexpr (!WIDE) {
-            int all = 0;
-#pragma unroll
-            for (int i = 0; i < kEach * kWaves; ++i) all += biases[i];
-            for (int i = threadIdx.x; i < all; i += kThreads) {
-                const int u = bias_token[i];
-                int j = i + 1;
-                while (j < all && bias_token[j] != u) ++j;
-                if (j < all) continue;   // (a token named twice: its last entry)
-                at16(bias_cnt, i) = at16(cnt, u);
-                at16(cnt, u) = (uint16_t)(kBias | i);
+        if constexpr (!WIDE)
+            for (int i = threadIdx.x, all = listed(); i < all; i += kThreads) {
+                const int u = bias_token[i], shift = 16 * (u & 1);
+                uint32_t* const word = &cnt[u >> 1];
+                const uint32_t mine = kBias | i;
+                for (uint32_t was = *word;;) {
+                    const uint32_t half = was >> shift & 0xffffu;
+                    // (a count has kBias nowhere; with kSeen alone it is no place either)
+                    if ((half & kBias) && half > mine) break;
+                    const uint32_t now = atomicCAS(word, was, (was & ~(0xffffu << shift)) | mine << shift);
+                    if (now == was) break;
+                    was = now;
+                }
             }
-        }
     }
     // n more of a token, once the biases are in place
     __device__ __forceinline__ void add_later(int u, int n)
@@ -519,17 +533,28 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
                 }
             };
             if (a.capacity >= 4) {
-                for (int i = tid * 4; i < len; i += kThreads * 4) {
-                    if (i >= kThreads * 4) text = four(i);
+                auto count4 = [&](const u32x4_any_t& text, int i) {
                     if (i >= start && i + 4 <= len) {   // (nearly all)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) count((int)text[e], true);
-                    } else {
+                    } else if (i < len) {
                         const int from = min(i, a.capacity - 4);   // (see four)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (from + e >= i && from + e < len) count((int)text[e], from + e >= start);
                     }
+                };
+                constexpr int kStep = kThreads * 4;
+                count4(text, tid * 4);
+                // (four reads at a time)
+                for (int i0 = kStep; i0 < len; i0 += 4 * kStep) {
+                    u32x4_any_t more[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i0 + r * kStep < len) more[r] = four(i0 + r * kStep + tid * 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i0 + r * kStep < len) count4(more[r], i0 + r * kStep + tid * 4);
                 }
             } else if (tid < len) {
                 count(h[tid], tid >= start);
@@ -545,6 +570,8 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
         }
         __syncthreads();
         if (!WIDE && a.n_bias > 0) {
+            known.count_biases();
+            __syncthreads();
             known.place_biases();
             __syncthreads();
         }
@@ -728,10 +755,12 @@ void launch(LogitsArgs& a, bool x_bf16, bool out_bf16, hipStream_t s)
 {
     const int slice = 8 * kThreads * VECTORS;
     a.slices = (a.V + slice - 1) / slice;
-    // Rows of a workgroup: each walks its sequence's text anew, so few workgroups (about 2048) take many rows (32 windows of 8
-    // rows of 131072 with texts of 4000: 24.7 us, with half as many workgroups 30.8, with twice as many 26.5).
+    // Rows of a workgroup: each walks its sequence's text anew, so few workgroups take many rows: about 1024, and twice that
+    // where windows may be short (32 ragged windows of 8 rows of 131072 with texts of 4000: 23.1 us, with half as many
+    // workgroups 26.2, with twice as many 27.3; whole windows, 16 of 32 rows of 32000: 20.4 with 1024, 22.5 with 2048, 25.0
+    // with 512).
     const long long units = (long long)a.B * a.slices;
-    const int groups = (int)min((long long)a.K, max(1LL, 2048 / units));
+    const int groups = (int)min((long long)a.K, max(1LL, (a.count ? 2048 : 1024) / units));
     a.rows = (a.K + groups - 1) / groups;
     const dim3 grid(a.slices, a.B * ((a.K + a.rows - 1) / a.rows));
     if (x_bf16) out_bf16 ? launch<VECTORS, WIDE, true, true>(a, grid, s) : launch<VECTORS, WIDE, true, false>(a, grid, s);
