@@ -252,15 +252,24 @@ __device__ __forceinline__ float only(float f, uint32_t bits, int e)
 // What is known of the tokens of a slice, in LDS: their counts, and whether they stand in the text before `start` or have
 // a bias; a bit map of the drafted ones.  Narrow: 16 bits a token (14 of the count, one for a bias, one for the text before
 // `start`), and a list of the slice's biases; a token with a bias has its place in that list instead, and its count
-// there.  Wide: 32 bits a token, and a bias's entry for each; where a count may pass 14 bits or the biases are more
-// than two a thread (64 rows of 131072, fp32, texts of 1000: 20.1 us wide, 18.5 narrow; of 15000 36.5 and 25.0; 8
-// rows 7.8 and 7.5, 12.3 and 12.2).
-constexpr int kNarrowText = 16000;   // the longest text (with a window's drafts below 2^14)
+// there.  Long, for texts that may be of more than 16000 tokens: the same, and such a text is counted in parts, between
+// which counts of 3000 and more go to a list of their own (all but one).  Wide: 32 bits a token, and a bias's entry for
+// each; where that list could overflow or the biases are more than two a thread.  (64 rows of 131072, fp32, texts of
+// 1000: 20.1 us wide, 18.5 narrow; of 15000 36.5 and 25.0.)
+constexpr int kStep = kThreads * 4;   // tokens of a text that a workgroup reads at once
+constexpr int kPart = 12 * kStep;     // those of a part (the first has a step more)
+constexpr int kMuch = 3000, kNarrowText = 16000;
+static_assert(kNarrowText + kKvWindowMax < 1 << 14 && kMuch + kPart + kKvWindowMax < 1 << 14 &&
+                  kPart + kStep + kKvWindowMax < 1 << 14, "a count with a window's drafts has 14 bits");
+constexpr int kSpills = 128;
+constexpr int kLongText = kSpills * (kMuch - 1);
+enum Size { kNarrow, kLong, kWide };
 constexpr int kNarrowBias = 2 * kThreads;
 constexpr int kEach = kNarrowBias / kThreads;   // biases of a thread
 
-template <bool WIDE, int TOKENS>
+template <Size SIZE, int TOKENS>
 struct Known {
+    static constexpr bool WIDE = SIZE == kWide, LONG = SIZE == kLong;
     static constexpr int kBits = WIDE ? 32 : 16;
     static constexpr uint32_t kCount = (1u << (kBits - 2)) - 1, kBias = 1u << (kBits - 2), kSeen = 1u << (kBits - 1);
     uint32_t cnt[WIDE ? TOKENS : TOKENS / 2];
@@ -270,6 +279,8 @@ struct Known {
     uint32_t bias_cnt[WIDE ? 1 : kNarrowBias / 2];   // (16 bits each)
     uint16_t bias_token[WIDE ? 1 : kNarrowBias];
     int biases[kEach * kWaves];
+    int spill_token[LONG ? kSpills : 1];
+    uint32_t spill_cnt[LONG ? kSpills : 1];
 
     __device__ __forceinline__ void clear()
     {
@@ -278,6 +289,7 @@ struct Known {
         for (int i = threadIdx.x; i < TOKENS / 32; i += kThreads) drafted[i] = 0;
         if constexpr (WIDE)
             for (int i = threadIdx.x; i < TOKENS; i += kThreads) entry[i] = -1;
+        if (LONG && threadIdx.x < kSpills) spill_token[threadIdx.x] = -1, spill_cnt[threadIdx.x] = 0;
     }
     static __device__ __forceinline__ void add16(uint32_t* p, int i, int n) { atomicAdd(&p[i >> 1], (uint32_t)n << 16 * (i & 1)); }
     static __device__ __forceinline__ uint16_t& at16(uint32_t* p, int i) { return reinterpret_cast<uint16_t*>(p)[i]; }
@@ -286,6 +298,43 @@ struct Known {
     {
         if constexpr (WIDE) atomicAdd(&cnt[u], (uint32_t)n);
         else add16(cnt, u, n);
+    }
+    // much counted tokens to their list (there are seldom any)
+    __device__ __forceinline__ void spill()
+    {
+        if constexpr (LONG) {
+            constexpr int kEights = TOKENS / 8 / kThreads;   // a thread's
+            uint32_t most = 0;
+#pragma unroll
+            for (int r = 0; r < kEights; ++r) {
+                const uint4 w = reinterpret_cast<const uint4*>(cnt)[threadIdx.x + r * kThreads];
+                for (const uint32_t x : {w.x, w.y, w.z, w.w}) most = max(most, max(x & kCount, x >> 16 & kCount));
+            }
+            if (most < kMuch) return;
+#pragma clang loop unroll(disable)
+            for (int i = 0; i < 8 * kEights; ++i) {
+                const int u = (threadIdx.x + (i >> 3) * kThreads) * 8 + (i & 7);
+                const uint32_t c = at16(cnt, u), n = c & kCount;
+                if (n < kMuch) continue;
+                at16(cnt, u) = (uint16_t)(c - (n - 1));
+                int at = 0;
+                for (;;) {
+                    const int was = atomicCAS(&spill_token[at], -1, u);
+                    if (was == -1 || was == u || at == kSpills - 1) break;
+                    ++at;
+                }
+                atomicAdd(&spill_cnt[at], n - 1);
+            }
+        }
+    }
+    // what that list has of a token
+    __device__ __forceinline__ uint32_t spilled(int u) const
+    {
+        if constexpr (LONG)
+#pragma clang loop unroll(disable)
+            for (int i = 0; i < kSpills && spill_token[i] != -1; ++i)
+                if (spill_token[i] == u) return spill_cnt[i];
+        return 0;
     }
     __device__ __forceinline__ void mark(int u, uint32_t bit)
     {
@@ -380,13 +429,11 @@ struct Known {
 #pragma unroll
             for (int e = 0; e < 8; ++e) some |= min(cnt[u + e], 1u) << e;
         } else {
-            uint32_t two = 0;   // bits 0 and 16: the first two, ...
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t w = cnt[(u >> 1) + i];
-                two |= (min(w & 0xffffu, 1u) | min(w >> 16, 1u) << 1) << 2 * i;
+                some |= (min(w & 0xffffu, 1u) | min(w >> 16, 1u) << 1) << 2 * i;
             }
-            some |= two;
         }
         return some;
     }
@@ -455,11 +502,12 @@ __device__ __forceinline__ bool rows_of(const LogitsArgs& a, int i, int& b, int&
 }
 
 // 2048 VECTORS tokens of the vocabulary, for some rows of one sequence: a thread has eight of each 2048.
-template <int VECTORS, bool WIDE, bool XBF16, bool OBF16, bool NOISE>
+template <int VECTORS, Size SIZE, bool XBF16, bool OBF16, bool NOISE>
 __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
 {
     constexpr int kTokens = 8 * kThreads * VECTORS;
-    using K = Known<WIDE, kTokens>;
+    constexpr bool WIDE = SIZE == kWide, LONG = SIZE == kLong;
+    using K = Known<SIZE, kTokens>;
     __shared__ alignas(16) K known;
     __shared__ unsigned long long best[kKvWindowMax], paths[kKvWindowMax], inside_s;
     __shared__ int draft[kKvWindowMax];
@@ -479,9 +527,11 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
     u32x4_any_t text = {0, 0, 0, 0};
     int drafted = -1, above = -1, id[kEach] = {}, len = 0, start = 0;
     float value[kEach] = {};
+    bool longer = false;
     if (texts) {
         len = min(max(a.history_lens[b], 0), a.capacity);
         if (a.history_start) start = a.history_start[b];
+        longer = LONG && len - max(min(start, len), 0) > kNarrowText;
     }
     if (texts && a.capacity >= 4) text = four(tid * 4);
     if (drafts && wave == kWaves - 1) {
@@ -544,17 +594,24 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
                             if (from + e >= i && from + e < len) count((int)text[e], from + e >= start);
                     }
                 };
-                constexpr int kStep = kThreads * 4;
                 count4(text, tid * 4);
                 // (four reads at a time)
-                for (int i0 = kStep; i0 < len; i0 += 4 * kStep) {
-                    u32x4_any_t more[4];
+                u32x4_any_t more[4];
+                auto ask = [&](int i0) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (i0 + r * kStep < len) more[r] = four(i0 + r * kStep + tid * 4);
+                };
+                for (int i0 = kStep; i0 < len; i0 += 4 * kStep) {
+                    ask(i0);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (i0 + r * kStep < len) count4(more[r], i0 + r * kStep + tid * 4);
+                    if (LONG && longer && i0 % kPart == kPart - 3 * kStep) {
+                        __syncthreads();
+                        known.spill();
+                        __syncthreads();
+                    }
                 }
             } else if (tid < len) {
                 count(h[tid], tid >= start);
@@ -614,7 +671,9 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a)
                     const int e = __ffs(left) - 1;
                     bool biased;
                     float bias = 0.0f;
-                    const uint32_t c = known.look(a, b, k + e, biased, bias), n = c & K::kCount;
+                    const uint32_t c = known.look(a, b, k + e, biased, bias);
+                    uint32_t n = c & K::kCount;
+                    if (LONG && longer && n) n += known.spilled(k + e);
                     float x = f[0];
 #pragma unroll
                     for (int i = 1; i < 8; ++i) x = i == e ? f[i] : x;
@@ -743,14 +802,14 @@ int vectors_of(const LogitsArgs& a)
     return (long long)a.B * a.K * ((a.V + 8 * kThreads * 4 - 1) / (8 * kThreads * 4)) >= 384 ? 4 : 1;
 }
 
-template <int VECTORS, bool WIDE, bool XBF16, bool OBF16>
+template <int VECTORS, Size SIZE, bool XBF16, bool OBF16>
 void launch(const LogitsArgs& a, dim3 grid, hipStream_t s)
 {
-    if (a.noise) logits_kernel<VECTORS, WIDE, XBF16, OBF16, true><<<grid, dim3(kThreads), 0, s>>>(a);
-    else logits_kernel<VECTORS, WIDE, XBF16, OBF16, false><<<grid, dim3(kThreads), 0, s>>>(a);
+    if (a.noise) logits_kernel<VECTORS, SIZE, XBF16, OBF16, true><<<grid, dim3(kThreads), 0, s>>>(a);
+    else logits_kernel<VECTORS, SIZE, XBF16, OBF16, false><<<grid, dim3(kThreads), 0, s>>>(a);
 }
 
-template <int VECTORS, bool WIDE>
+template <int VECTORS, Size SIZE>
 void launch(LogitsArgs& a, bool x_bf16, bool out_bf16, hipStream_t s)
 {
     const int slice = 8 * kThreads * VECTORS;
@@ -763,8 +822,8 @@ void launch(LogitsArgs& a, bool x_bf16, bool out_bf16, hipStream_t s)
     const int groups = (int)min((long long)a.K, max(1LL, (a.count ? 2048 : 1024) / units));
     a.rows = (a.K + groups - 1) / groups;
     const dim3 grid(a.slices, a.B * ((a.K + a.rows - 1) / a.rows));
-    if (x_bf16) out_bf16 ? launch<VECTORS, WIDE, true, true>(a, grid, s) : launch<VECTORS, WIDE, true, false>(a, grid, s);
-    else out_bf16 ? launch<VECTORS, WIDE, false, true>(a, grid, s) : launch<VECTORS, WIDE, false, false>(a, grid, s);
+    if (x_bf16) out_bf16 ? launch<VECTORS, SIZE, true, true>(a, grid, s) : launch<VECTORS, SIZE, true, false>(a, grid, s);
+    else out_bf16 ? launch<VECTORS, SIZE, false, true>(a, grid, s) : launch<VECTORS, SIZE, false, false>(a, grid, s);
 }
 
 }  // namespace
@@ -776,10 +835,14 @@ hipError_t launch_logits(const LogitsArgs& args, bool x_bf16, bool out_bf16, hip
 {
     LogitsArgs a = args;
     a.marks = a.n_bias > 0 || (a.params && (a.history || a.tokens));
-    const bool wide = (a.params && a.history && a.capacity > kNarrowText) || a.n_bias > kNarrowBias;
-    if (a.marks && wide) launch<1, true>(a, x_bf16, out_bf16, s);
-    else if (vectors_of(a) == 4) launch<4, false>(a, x_bf16, out_bf16, s);
-    else launch<1, false>(a, x_bf16, out_bf16, s);
+    const int text = a.params && a.history ? a.capacity : 0;
+    const bool many = vectors_of(a) == 4;
+    // (Small slices have room for 32 bits, and no parts to wait for: a row of 131072 with a text of 32000 13.2 us wide, 15.6
+    // long; 8 rows, 100000 34.0 and 43.9; but 64 rows, 100000 in large slices 61 us long, 103 wide in small ones; 32 ragged
+    // windows of 8, texts of 4000 in rows of 131072 23.5 and 30.7.)
+    if (text > kLongText || a.n_bias > kNarrowBias || (text > kNarrowText && !many)) launch<1, kWide>(a, x_bf16, out_bf16, s);
+    else if (text > kNarrowText) launch<4, kLong>(a, x_bf16, out_bf16, s);
+    else many ? launch<4, kNarrow>(a, x_bf16, out_bf16, s) : launch<1, kNarrow>(a, x_bf16, out_bf16, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.best) return e;
     const long long rows = (long long)a.B * a.K;

@@ -37,6 +37,7 @@ constexpr long long kGridX = 1 << 23;   // workgroups in x (a launch's threads t
 // Reads of more than this go past the caches (tokens of 32 heads of 256, by their number: 2048, 33.5 MB read, 17.9 us past
 // them and 14.7 through them; 4096 31.1 and 31.8; 8192 59.5 and 61.4).
 constexpr long long kStreamBytes = 48 << 20;
+constexpr long long kNowhere = 1LL << 62;   // (no position: a token that is not there)
 constexpr double kInv2Pi = 0.15915494309189533577;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -228,14 +229,15 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
             const int b = (int)(tok / (uint32_t)a.K), t = (int)(tok - (uint32_t)b * a.K);
             const long long len = a.lens ? max(a.lens[b], 0) : 0;
             const bool there = !a.count || t < a.count[b];
-            where[i] = a.pos ? (long long)a.pos[tok] : len + t;
+            where[i] = !there ? kNowhere : a.pos ? (long long)a.pos[tok] : len + t;
             const long long page_at = a.table ? page_of(b, len + t) : -1;
 #pragma unroll
             for (int part = 0; part < 3; ++part) place(i, part, b, t, there, page_at);
         }
         __syncthreads();
         if (j < half)
-            for (int i = threadIdx.x >> a.half_log2; i < n; i += kThreads >> a.half_log2) angle(i, j, where[i], freq);
+            for (int i = threadIdx.x >> a.half_log2; i < n; i += kThreads >> a.half_log2)
+                if (where[i] != kNowhere) angle(i, j, where[i], freq);
     } else {   // a wave a token, or several waves where there are fewer tokens
         const int share = max(kWaves / a.tile, 1), sub = wave % share;
         for (int i = wave / share; i < n; i += kWaves / share) {

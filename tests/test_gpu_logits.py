@@ -161,6 +161,51 @@ def test_windows_of_every_length(B, K, V, counts):
     assert bool((out.cpu()[~there] == 9.0).all()) and bool((b.cpu()[~there] == -7).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("V,length,capacity,often", [
+    (100, 16001, 16001, [(7, 16001)]), (9000, 33000, 40000, [(8191, 16000), (8192, 17000)]), (5000, 40000, 1 << 17, [(2047, 39990)]),
+    (50, 120000, 120000, [(3, 16200), (4, 16300), (10, 40000), (49, 16255)]), (300, 900, 1 << 20, [(5, 800)]),
+    (40, 100000, 383872, [(0, 50000), (1, 50000)]), (40, 100000, 383873, [(0, 50000), (1, 50000)]),
+    (128, 383872, 383872, [(i, 2999) for i in range(128)]), (128, 383872, 383872, [(127 - i, 3022) for i in range(127)])])
+def test_tokens_that_stand_often(V, length, capacity, often, few, dtype):
+    """Long texts, tokens that stand in them more often than 14 bits count, with drafts and biases of the same ones."""
+    say("often", V, length, capacity, often, few, dtype)
+    g = torch.Generator().manual_seed(length)
+    B, K = (2, 3) if few else (6, 64)
+    c = case(1, B, K, V, 4, dtype, n_bias=3)
+    text = torch.randint(0, V, (length,), generator=g).to(I32)
+    at, i = torch.randperm(length, generator=g), 0
+    for token, n in often:
+        text[at[i:i + n]] = token
+        i += n
+    c["history"] = torch.zeros(B, capacity, dtype=I32)
+    c["history"][:, :length] = text
+    c["lens"] = torch.tensor([length, length - 1] * (B // 2), dtype=I32)
+    c["start"] = torch.tensor([0, length // 3] * (B // 2), dtype=I32)
+    c["tokens"][:] = often[0][0]
+    c["ids"][:, 1] = often[-1][0]
+    c["params"][:, 2] = torch.tensor([1e-4, -3e-5] * (B // 2))
+    out, b = run(c, F32)
+    # (the counts by torch, in place of the loops over texts)
+    want = c["x"].float()
+    for s in range(B):
+        n = int(c["lens"][s])
+        seen, since = (torch.bincount(c["history"][s, i:n].long(), minlength=V) for i in (0, int(c["start"][s])))
+        rep, presence, frequency, temp = c["params"][s]
+        for t in range(K):
+            path = torch.zeros(V, dtype=torch.int64)
+            path[often[0][0]] = t + 1
+            x = want[s, t]
+            x = torch.where(seen + path > 0, x * torch.where(x > 0, 1.0 / rep, rep), x)
+            x = torch.where(since + path > 0, x - (frequency * (since + path).float() + presence), x)
+            for i, v in {int(i): v for i, v in zip(c["ids"][s], c["values"][s]) if 0 <= i < V}.items():
+                x[i] += v
+            want[s, t] = x * (1.0 / temp)
+    assert torch.equal(out.cpu(), want)
+    assert torch.equal(b.cpu(), ref.best(want))
+
+
 @pytest.mark.parametrize("B,K,V,n_bias", [(2, 5, 300, 256), (1, 16, 70, 256), (3, 2, 300, 257), (2, 9, 9000, 200), (2, 5, 300, 512), (3, 2, 300, 513)])
 def test_biases_of_many_tokens(B, K, V, n_bias):
     """Most tokens have a bias, many ids are named twice or more, and the drafted tokens and the text's have one too."""
