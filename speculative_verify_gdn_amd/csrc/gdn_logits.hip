@@ -32,6 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 // 16 bytes at an element's own alignment (rows of an odd length start anywhere)
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -153,6 +154,18 @@ __device__ __forceinline__ uint32_t wave_most(uint32_t v)
     with(__builtin_amdgcn_update_dpp(0, (int)v, kDppRowMirror, 0xF, 0xF, false));
     with(__shfl_xor((int)v, 16, 64));
     with(__shfl_xor((int)v, 32, 64));
+    return v;
+}
+
+// the sums of the lanes up to each
+__device__ __forceinline__ int wave_sums(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // within a row: 1, 2, 4, 8 lanes before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // rows 1 and 3: the last of the row before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // rows 2 and 3: the last of row 1
     return v;
 }
 
@@ -429,11 +442,13 @@ struct Known {
 #pragma unroll
             for (int e = 0; e < 8; ++e) some |= min(cnt[u + e], 1u) << e;
         } else {
+            uint32_t two = 0;   // bits 0, 2, 4, 6: the even ones; 16, 18, ...: the odd ones
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t w = cnt[(u >> 1) + i];
-                some |= (min(w & 0xffffu, 1u) | min(w >> 16, 1u) << 1) << 2 * i;
+                const u16x2_t w = __builtin_elementwise_min(__builtin_bit_cast(u16x2_t, cnt[(u >> 1) + i]), (u16x2_t){1, 1});
+                two |= __builtin_bit_cast(uint32_t, w) << 2 * i;
             }
+            some |= (two | two >> 15) & 0xffu;
         }
         return some;
     }
@@ -468,12 +483,7 @@ __device__ __forceinline__ bool rows_of(const LogitsArgs& a, int i, int& b, int&
         const int lane = threadIdx.x & 63;
         const int count = lane < a.B ? clamp_count(a.count, lane, a.K) : 0;
         const int full = count / a.rows, rest = count - full * a.rows;
-        int upto = full;   // of this and the sequences before
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int before = __shfl_up(upto, d, 64);
-            upto += lane >= d ? before : 0;
-        }
+        const int upto = wave_sums(full);   // of this and the sequences before
         const int all = __shfl(upto, 63, 64);
         int g;
         if (i < all) {
