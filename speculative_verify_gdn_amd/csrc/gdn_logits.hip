@@ -16,9 +16,9 @@
 // Every operation is one rounding of 32 bits in the order above, so that equal
 // logits stay equal and the best is the lowest of them.
 //
-// Measured: 64 rows of 131072, fp32, with noise and output (101 MB) 22.2 us, of which the stream 19.6 (5.1 TB/s);
+// Measured: 64 rows of 131072, fp32, with noise and output (101 MB) 22.4 us, of which the stream 19.6 (5.1 TB/s);
 // 32 ragged windows of 8 rows of 131072, bf16, masks, biases and texts of 4000 (78 MB)
-// 23.1 us: the counting and what it makes the stream look up take 2 us each, joining the best 2.5, a workgroup's reads before its
+// 22.9 us: the counting and what it makes the stream look up take 2 us each, joining the best 2.5, a workgroup's reads before its
 // stream 3; without texts, biases, masks and best 14.0.
 // With the logits of the counted tokens left to a second kernel (a hash table a sequence) the stream was 1 us shorter, and
 // that kernel's scattered reads and writes took 13.
