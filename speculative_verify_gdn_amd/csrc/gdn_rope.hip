@@ -18,9 +18,9 @@
 //     by side.  So no element crosses lanes, and the norm is a sum over the group.
 //   - where the head goes (dense rows, or a page of the cache) is an offset a
 //     token.
-// Measured: 16384 tokens of 48 heads of 128 (bf16, into the cache, 403 MB) 76.8 us, 5.2 TB/s; 8193 of 40
-// heads of 128 (fp32, normed, 336 MB) 66.7 us; 16384 of 32 (bf16, 268 MB) 51.3 us: 93 to 97% of a copy of the same
-// bytes.  1024 tokens in trees of 16, 32 heads of 256 (34 MB) 10.2 us: a workgroup's chain of reads, 9 us from its
+// Measured: 16384 tokens of 48 heads of 128 (bf16, into the cache, 403 MB) 77.1 us, 5.2 TB/s; 8193 of 40
+// heads of 128 (fp32, normed, 336 MB) 66.2 us; 16384 of 32 (bf16, 268 MB) 51.4 us: 97 to 100% of a copy of the same
+// bytes.  1024 tokens in trees of 16, 32 heads of 256 (34 MB) 10.4 us: a workgroup's chain of reads, 9 us from its
 // start to its last store.  Heads asked for before that chain, or a head ahead, took longer in every case (waves
 // then hold more registers, or reads come back in an order that the chain waits for).
 #include "gdn_device.h"
@@ -145,6 +145,11 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t tokens = (uint32_t)a.B * a.K, first = (blockIdx.x + blockIdx.z * gridDim.x) * a.tile;
     if (first >= tokens) return;
+    if constexpr (LANES || STREAM)   // (many workgroups) done where none of the tokens is there
+        if (a.count) {
+            const uint32_t b = first / (uint32_t)a.K, t = first - b * a.K;
+            if (t + a.tile <= (uint32_t)a.K && (int)t >= a.count[b]) return;
+        }
     const int n = (int)min((uint32_t)a.tile, tokens - first);
     const int half = a.rot >> 1;
 
