@@ -626,8 +626,8 @@ int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, in
  *   head-major layout will do; a head's own elements are dense
  *   wq, wk [D] float; pos [B][K], lens, count [B], parent [B][K] int32, each or
  *   NULL; rows t >= count[b] (clamped into 0..K; NULL: K) are left untouched
- * rot in multiples of 32 bytes of elements (16 in bf16, 8 in fp32) is fastest, in
- * multiples of 16 bytes next; other rot go element by element.
+ * rot in multiples of 32 bytes of elements (16 in bf16, 8 in fp32; interleaved: half of that)
+ * is fastest, in multiples of half as many next; other rot go element by element.
  */
 enum gdn_rope_layout { GDN_ROPE_HALVES = 0, GDN_ROPE_INTERLEAVED = 1 };
 enum gdn_rope_scaling {

@@ -14,8 +14,8 @@
 //     every head of a token reads them from there.
 //   - a group of lanes holds one head, a lane two 16-byte pieces of it: for the
 //     two halves those whose elements are pairs of one another, for neighbours
-//     any two, taken half the turned part apart so that the lanes of a group lie side
-//     by side.  So no element crosses lanes, and the norm is a sum over the group.
+//     any two, taken half the turned part (or half the head, where not all of it turns)
+//     apart so that the lanes of a group lie side by side.  So no element crosses lanes, and the norm is a sum over the group.
 //   - where the head goes (dense rows, or a page of the cache) is an offset a
 //     token.
 // Measured: 16384 tokens of 48 heads of 128 (bf16, into the cache, 403 MB) 77.1 us, 5.2 TB/s; 8193 of 40
@@ -130,9 +130,15 @@ struct Token {
     long long to[3];    // the same where it goes; below 0: nowhere
 };
 
+// kPart: neighbours of heads that turn in part.  Their pieces turn or not each for itself, so that any whole number of
+// pieces may turn, and the two of a lane are half the head apart: accesses of whole lines.  (16384 tokens of 32 heads of
+// 80, bf16, 40 elements turned: 46 us, in pieces of half the size 76; 110304 of 4 heads of 128, 32 turned: 51.5 and 56.5.  With
+// whole heads it has more registers to hold than there are: 16384 of 32 heads of 128, 54.5 and 51.4.)
+enum Pairs { kHalves, kNeighbours, kPart };
+
 // E: elements of a piece; NP: pairs of pieces of a lane; STREAM: past the caches; LANES: the tokens are looked after by a
 // lane each, not by a wave
-template <bool BF16, int E, int NP, bool INTERLEAVED, bool STREAM, bool LANES>
+template <bool BF16, int E, int NP, Pairs PAIRS, bool STREAM, bool LANES>
 __device__ __forceinline__ void rope_heads(const RopeArgs& a)
 {
     constexpr int ES = BF16 ? 2 : 4;
@@ -164,7 +170,7 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
         }
 
     // A group of lanes holds a head; lane l of it the pieces l and l + turned of the part that turns, or l and l +
-    // (pairs - turned) of the rest.
+    // (pairs - turned) of the rest; kPart: l and l + pairs of the head.
     const int h0 = blockIdx.y * a.chunk, nh = min(a.chunk, a.heads - h0);
     const int group = threadIdx.x >> a.lanes_log2, step = kThreads >> a.lanes_log2;
     const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);
@@ -174,7 +180,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
         const int j = l + (k << a.lanes_log2);
-        if (INTERLEAVED && E == 1 && j < turned) at[k] = 2 * j, bt[k] = 2 * j + 1;
+        if (PAIRS == kPart) at[k] = j * E, bt[k] = (j + pairs) * E;
+        else if (PAIRS == kNeighbours && E == 1 && j < turned) at[k] = 2 * j, bt[k] = 2 * j + 1;
         else if (j < turned) at[k] = j * E, bt[k] = at[k] + half;
         else at[k] = a.rot + (j - turned) * E, bt[k] = at[k] + (pairs - turned) * E;
     }
@@ -309,60 +316,77 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
         for (int k = 0; k < NP; ++k) {
             const int j = l + (k << a.lanes_log2);
             if (j >= pairs) continue;
-            const bool turns = part.turned && j < turned;
-            if (!turns && !part.w) {
+            // (the second piece turns only where the first does)
+            const bool tu = part.turned && (PAIRS == kPart ? at[k] < a.rot : j < turned);
+            const bool tv = PAIRS == kPart ? part.turned && bt[k] < a.rot : tu;
+            if (!tu && !part.w) {
                 u[k].keep(y + at[k] * ES);
                 v[k].keep(y + bt[k] * ES);
                 continue;
             }
-            if (turns) {
-                auto turn = [](float& p, float& q, float c, float s) {
-                    const float p0 = p, q0 = q;
-                    p = fmaf(p0, c, -(q0 * s));
-                    q = fmaf(q0, c, p0 * s);
-                };
-                const float *c = cs + x.i * half, *s = sn + x.i * half;
-                if constexpr (!INTERLEAVED || E == 1) {   // the pair: an element of each piece
+            auto turn = [](float& p, float& q, float c, float s) {
+                const float p0 = p, q0 = q;
+                p = fmaf(p0, c, -(q0 * s));
+                q = fmaf(q0, c, p0 * s);
+            };
+            const float *c = cs + x.i * half, *s = sn + x.i * half;
+            if constexpr (PAIRS == kHalves || E == 1) {   // the pair: an element of each piece
+                if (tu)
 #pragma unroll
                     for (int e = 0; e < E; ++e) turn(f[k][e], g[k][e], c[j * E + e], s[j * E + e]);
-                } else {   // neighbours: the two pieces turn by themselves
+            } else if constexpr (PAIRS == kNeighbours) {   // the two pieces turn by themselves
+                if (tu)
 #pragma unroll
                     for (int e = 0; e < PE; ++e) {
                         const int i = j * PE + e, m = (turned + j) * PE + e;
                         turn(f[k][2 * e], f[k][2 * e + 1], c[i], s[i]);
                         turn(g[k][2 * e], g[k][2 * e + 1], c[m], s[m]);
                     }
-                }
+            } else {
+                if (tu)
+#pragma unroll
+                    for (int e = 0; e < PE; ++e) turn(f[k][2 * e], f[k][2 * e + 1], c[j * PE + e], s[j * PE + e]);
+                if (tv)
+#pragma unroll
+                    for (int e = 0; e < PE; ++e)
+                        turn(g[k][2 * e], g[k][2 * e + 1], c[(pairs + j) * PE + e], s[(pairs + j) * PE + e]);
             }
             Piece<BF16, E, STREAM>::store(y + at[k] * ES, f[k]);
-            Piece<BF16, E, STREAM>::store(y + bt[k] * ES, g[k]);
+            if (PAIRS == kPart && !tv && !part.w) v[k].keep(y + bt[k] * ES);
+            else Piece<BF16, E, STREAM>::store(y + bt[k] * ES, g[k]);
         }
     }
 }
 
 // Eight waves a SIMD: with six (ten registers more) the large windows took 3 to 6% longer.
-template <bool BF16, bool INTERLEAVED, bool STREAM, bool LANES>
+template <bool BF16, Pairs PAIRS, bool STREAM, bool LANES>
 __global__ __launch_bounds__(kThreads, 8) void rope_kernel(RopeArgs a)
 {
-    rope_heads<BF16, BF16 ? 8 : 4, 1, INTERLEAVED, STREAM, LANES>(a);
+    rope_heads<BF16, BF16 ? 8 : 4, 1, PAIRS, STREAM, LANES>(a);
 }
 
-// Pieces of 8 bytes, and element by element: for turned parts that no whole pairs of 16 bytes make up (8192 tokens of
-// 32 heads of 96, bf16: 32 elements of each turned 27 us, 24 of them 42, 22 102).
-template <bool BF16, int E, int NP, bool INTERLEAVED, bool LANES>
-__global__ __launch_bounds__(kThreads) void rope_narrow_kernel(RopeArgs a)
+// Pieces of 8 bytes, and element by element: for turned parts that no whole pieces (halves: pairs of them) of 16 bytes make
+// up (16384 tokens of 32 heads of 96, bf16, halves: 24 elements of each turned 74 us, 22 197).
+template <bool BF16, int E, int NP, Pairs PAIRS, bool LANES>
+__global__ __launch_bounds__(kThreads, 8) void rope_narrow_kernel(RopeArgs a)
 {
-    rope_heads<BF16, E, NP, INTERLEAVED, false, LANES>(a);
+    rope_heads<BF16, E, NP, PAIRS, false, LANES>(a);
 }
 
 template <bool BF16, bool INTERLEAVED, bool LANES>
 void launch(const RopeArgs& a, int e, bool stream, dim3 grid, hipStream_t s)
 {
     constexpr int E = BF16 ? 8 : 4;
-    if (e == 1) rope_narrow_kernel<BF16, 1, 4, INTERLEAVED, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
-    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, INTERLEAVED, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
-    else if (stream) rope_kernel<BF16, INTERLEAVED, true, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
-    else rope_kernel<BF16, INTERLEAVED, false, LANES><<<grid, dim3(kThreads), 0, s>>>(a);
+    constexpr Pairs kWhole = INTERLEAVED ? kNeighbours : kHalves, kSome = INTERLEAVED ? kPart : kHalves;
+    const dim3 block(kThreads);
+    if (e == 1) rope_narrow_kernel<BF16, 1, 4, kWhole, LANES><<<grid, block, 0, s>>>(a);
+    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, kSome, LANES><<<grid, block, 0, s>>>(a);
+    else if (INTERLEAVED && a.rot < a.D)
+        stream ? rope_kernel<BF16, kSome, true, LANES><<<grid, block, 0, s>>>(a)
+               : rope_kernel<BF16, kSome, false, LANES><<<grid, block, 0, s>>>(a);
+    else
+        stream ? rope_kernel<BF16, kWhole, true, LANES><<<grid, block, 0, s>>>(a)
+               : rope_kernel<BF16, kWhole, false, LANES><<<grid, block, 0, s>>>(a);
 }
 
 int log2_up(int n)
@@ -376,7 +400,8 @@ template <bool BF16, bool INTERLEAVED>
 void launch(RopeArgs& a, hipStream_t s)
 {
     constexpr int E = BF16 ? 8 : 4;
-    const int e = a.rot % (2 * E) == 0 ? E : a.rot % E == 0 ? E / 2 : 1;   // elements of a piece
+    const int whole = INTERLEAVED ? 1 : 2;   // pieces that the turned part has to be made of
+    const int e = a.rot % (whole * E) == 0 ? E : a.rot % (whole * E / 2) == 0 ? E / 2 : 1;   // elements of a piece
     a.lanes_log2 = min(log2_up(a.D / (2 * e)), 6);
     a.heads = a.part[0].H + a.part[1].H + a.part[2].H;
     const long long tokens = (long long)a.B * a.K;
@@ -400,7 +425,7 @@ void launch(RopeArgs& a, hipStream_t s)
     // Past the caches go accesses of whole lines, or of runs of 64 bytes and at least 128: parts of lines are joined in the
     // caches (13278 tokens of 30 heads of 128, bf16, 32 elements turned: 69 us past them, 53 through them; 40562 of 24 of 64
     // 74 and 58; but 16384 of 32 of 256, 64 turned, runs of 64 and 192, 45.8 and 48.7).
-    const int es = BF16 ? 2 : 4, run = half * es, rest = (a.D - a.rot) / 2 * es;
+    const int es = BF16 ? 2 : 4, run = (INTERLEAVED ? a.D / 2 : half) * es, rest = INTERLEAVED ? 0 : (a.D - a.rot) / 2 * es;
     const bool stream = (long long)tokens * a.heads * a.D * es > kStreamBytes && (run | rest) % 64 == 0 && max(run, rest) >= 128;
     // A lane a token where a workgroup has more of them than waves (110304 tokens of 4 heads of 96: 67 us with a wave a token,
     // 48 with a lane); the depth in a tree takes a wave.
