@@ -118,8 +118,9 @@ class Choice:
         before = dict(logits=logits, tokens=tokens, text=self.history.clone(), text_lens=self.lens.clone())
         gdn.logits_adjust(logits, best=self.best, history=self.history, history_lens=self.lens, history_start=self.start,
                           tokens=tokens, parent=parent, count=granted, params=self.params, workspace=self.workspace)
-        gdn.accept_tree(self.best, tokens, self.node, self.next, parent=parent, count=granted, history=self.history,
-                        lens=self.lens, lens_out=self.lens)
+        # (a sequence that got no room has no node to accept: its next token stays the one that it began with)
+        gdn.accept_tree(self.best, tokens, self.node, self.next, parent=parent, count=granted, root=tokens[:, 0].contiguous(),
+                        history=self.history, lens=self.lens, lens_out=self.lens)
         return dict(before, best=self.best.clone(), next=self.next.clone())
 
 
