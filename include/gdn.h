@@ -649,7 +649,8 @@ enum gdn_rope_scaling {
  *   YARN    the same with k = log(n_i / low) / log(high / low) in 0..1, and
  *           mscale = 0.1 log(factor) + 1 (Peng et al. 2023; low 1, high 32 there)
  *   freqs   HOST pointer, rot/2 doubles; mscale HOST pointer (1 except YARN)
- *   base > 1, 0 < low < high, rot even, 2..512
+ *   base > 1, 0 < low < high, rot even, 2..512; NTK's larger base and YARN's high / low (above 1)
+ *   have to fit a double
  */
 int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low, double high, double original,
                    double *freqs, float *mscale);

@@ -982,8 +982,13 @@ int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low,
     if (scaling == GDN_ROPE_BANDS || scaling == GDN_ROPE_YARN)
         REQUIRE(std::isfinite(original) && original > 0.0 && low > 0.0 && high > low && std::isfinite(high), GDN_EINVAL,
                 "%s: original = %g, low = %g, high = %g", fn, original, low, high);
+    if (scaling == GDN_ROPE_YARN)   // (its logarithm divides)
+        REQUIRE(high / low > 1.0 && std::isfinite(high / low), GDN_EUNSUPPORTED, "%s: high / low = %g", fn, high / low);
     const double two_pi = 6.283185307179586476925;
-    if (scaling == GDN_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+    if (scaling == GDN_ROPE_NTK) {
+        base *= std::pow(factor, (double)rot / (rot - 2));
+        REQUIRE(std::isfinite(base), GDN_EUNSUPPORTED, "%s: the enlarged base passes 64 bits", fn);
+    }
     for (int i = 0; i < rot / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / rot);
         const double turns = original * f / two_pi;   // over the original context
