@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define GDN_VERSION 5
+#define GDN_VERSION 6
 
 enum gdn_status {
     GDN_OK = 0,
@@ -635,7 +635,8 @@ enum gdn_rope_scaling {
     GDN_ROPE_LINEAR = 1,
     GDN_ROPE_NTK = 2,
     GDN_ROPE_BANDS = 3,
-    GDN_ROPE_YARN = 4
+    GDN_ROPE_YARN = 4,
+    GDN_ROPE_YARN_ROUNDED = 5
 };
 
 /*
@@ -647,8 +648,16 @@ enum gdn_rope_scaling {
  *   NTK     f_i with base * factor^(rot/(rot-2)) for the base (the same unused; rot > 2)
  *   BANDS   k f_i + (1-k) f_i / factor, k = (n_i - low) / (high - low) in 0..1
  *   YARN    the same with k = log(n_i / low) / log(high / low) in 0..1, and
- *           mscale = 0.1 log(factor) + 1 (Peng et al. 2023; low 1, high 32 there)
- *   freqs   HOST pointer, rot/2 doubles; mscale HOST pointer (1 except YARN)
+ *           mscale = 0.1 log(factor) + 1
+ *   YARN_ROUNDED  the same mscale, with k = 1 up to pair i = p, 0 from pair q on and linear in i between,
+ *           p = floor(d(high)) (0 at least), q = ceil(d(low)) (rot-1 at most),
+ *           d(n) = rot log(original / (2 pi n)) / (2 log base): the pair of n turns, unrounded
+ * YaRN (Peng et al. 2023; low 1, high 32) is published in three forms.  The paper's
+ * ramp is linear in the turns: BANDS, with YARN's mscale.  The authors' program has one that is linear in
+ * the pair's index between rounded bounds: YARN_ROUNDED, which most models scaled so were trained with.  YARN is the
+ * latter without the rounding (models that say that they do not truncate the bounds); against it a pair's frequency
+ * may be a third off.
+ *   freqs   HOST pointer, rot/2 doubles; mscale HOST pointer (1 except YARN and YARN_ROUNDED)
  *   base > 1, 0 < low < high, rot even, 2..512; NTK's larger base and YARN's high / low (above 1)
  *   have to fit a double
  */

@@ -974,12 +974,12 @@ int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low,
     REQUIRE(rot >= 2 && rot % 2 == 0, GDN_EINVAL, "%s: rot = %d is odd or below 2", fn, rot);
     REQUIRE(rot <= gdn::kRopeHeadMax, GDN_EUNSUPPORTED, "%s: rot = %d > %d", fn, rot, gdn::kRopeHeadMax);
     REQUIRE(std::isfinite(base) && base > 1.0, GDN_EINVAL, "%s: base = %g is not above 1", fn, base);
-    REQUIRE(scaling >= GDN_ROPE_PLAIN && scaling <= GDN_ROPE_YARN, GDN_EINVAL, "%s: bad scaling code %d", fn, scaling);
+    REQUIRE(scaling >= GDN_ROPE_PLAIN && scaling <= GDN_ROPE_YARN_ROUNDED, GDN_EINVAL, "%s: bad scaling code %d", fn, scaling);
     REQUIRE(freqs && mscale, GDN_EINVAL, "%s: null pointer", fn);
     if (scaling != GDN_ROPE_PLAIN)
         REQUIRE(std::isfinite(factor) && factor >= 1.0, GDN_EINVAL, "%s: factor = %g is below 1", fn, factor);
     if (scaling == GDN_ROPE_NTK) REQUIRE(rot > 2, GDN_EINVAL, "%s: one pair has no base to enlarge", fn);
-    if (scaling == GDN_ROPE_BANDS || scaling == GDN_ROPE_YARN)
+    if (scaling >= GDN_ROPE_BANDS)
         REQUIRE(std::isfinite(original) && original > 0.0 && low > 0.0 && high > low && std::isfinite(high), GDN_EINVAL,
                 "%s: original = %g, low = %g, high = %g", fn, original, low, high);
     if (scaling == GDN_ROPE_YARN)   // (its logarithm divides)
@@ -989,6 +989,13 @@ int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low,
         base *= std::pow(factor, (double)rot / (rot - 2));
         REQUIRE(std::isfinite(base), GDN_EUNSUPPORTED, "%s: the enlarged base passes 64 bits", fn);
     }
+    // the pair that turns n times over the original context, as a number between the pairs
+    auto pair_of = [&](double n) { return rot * std::log(original / (n * two_pi)) / (2.0 * std::log(base)); };
+    double first = 0.0, last = 0.0;
+    if (scaling == GDN_ROPE_YARN_ROUNDED) {
+        first = std::fmax(std::floor(pair_of(high)), 0.0);
+        last = std::fmin(std::ceil(pair_of(low)), rot - 1.0);
+    }
     for (int i = 0; i < rot / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / rot);
         const double turns = original * f / two_pi;   // over the original context
@@ -997,10 +1004,11 @@ int gdn_rope_freqs(int rot, double base, int scaling, double factor, double low,
         if (scaling == GDN_ROPE_BANDS) keep = (turns - low) / (high - low);
         // (the pair's index is linear in the logarithm of its turns)
         if (scaling == GDN_ROPE_YARN) keep = std::log(turns / low) / std::log(high / low);
+        if (scaling == GDN_ROPE_YARN_ROUNDED) keep = i <= first ? 1.0 : i >= last ? 0.0 : (last - i) / (last - first);
         keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
         freqs[i] = keep == 1.0 ? f : keep * f + (1.0 - keep) * f / factor;
     }
-    *mscale = scaling == GDN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    *mscale = scaling >= GDN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
     return ok();
 }
 

@@ -26,7 +26,7 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libgdn_debug.so")
 GDN_OK, GDN_EINVAL, GDN_EUNSUPPORTED, GDN_EHIP = 0, -1, -2, -3
 GDN_F32, GDN_BF16 = 0, 1
 GDN_ROPE_HALVES, GDN_ROPE_INTERLEAVED = 0, 1
-ROPE_SCALINGS = ("plain", "linear", "ntk", "bands", "yarn")   # gdn_rope_scaling, in order
+ROPE_SCALINGS = ("plain", "linear", "ntk", "bands", "yarn", "yarn_rounded")   # gdn_rope_scaling, in order
 EXPORTS = ("gdn_version", "gdn_last_error", "gdn_conv_step", "gdn_verify", "gdn_rollback", "gdn_prefill_chunked",
            "gdn_rollback_conv_step", "gdn_conv_step_ex", "gdn_verify_ex", "gdn_rollback_ex", "gdn_replay",
            "gdn_conv_tree", "gdn_verify_tree", "gdn_rollback_tree", "gdn_verify_step",
@@ -438,7 +438,7 @@ def attn_verify(q, k_pages, v_pages, lens, table, o, prefix_len=0, count=None, p
 # ---------------------------------------------------------------- positions and norms, logits and acceptance
 def rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, low=1.0, high=32.0, original=0.0, device="cuda"):
     """gdn_rope_freqs: the rot/2 frequencies as a float64 tensor on `device`, and mscale; scaling one of
-    ROPE_SCALINGS."""
+    ROPE_SCALINGS ("yarn_rounded" has the bounds of its ramp at whole pairs, as most models scaled by YaRN do, "yarn" not)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
     freqs, mscale = (ctypes.c_double * max(1, int(rot) // 2))(), ctypes.c_float(0.0)
