@@ -627,7 +627,7 @@ int gdn_attn_workspace(int B, int K, int Hq, int Hkv, int D, int page, int P, in
  *   wq, wk [D] float; pos [B][K], lens, count [B], parent [B][K] int32, each or
  *   NULL; rows t >= count[b] (clamped into 0..K; NULL: K) are left untouched
  * rot in multiples of 32 bytes of elements (16 in bf16, 8 in fp32; interleaved: half of that)
- * is fastest, in multiples of half as many next; other rot go element by element.
+ * is fastest, in multiples of half as many next (interleaved fp32: any even rot); other rot go element by element.
  */
 enum gdn_rope_layout { GDN_ROPE_HALVES = 0, GDN_ROPE_INTERLEAVED = 1 };
 enum gdn_rope_scaling {

@@ -379,8 +379,12 @@ void launch(const RopeArgs& a, int e, bool stream, dim3 grid, hipStream_t s)
     constexpr int E = BF16 ? 8 : 4;
     constexpr Pairs kWhole = INTERLEAVED ? kNeighbours : kHalves, kSome = INTERLEAVED ? kPart : kHalves;
     const dim3 block(kThreads);
-    if (e == 1) rope_narrow_kernel<BF16, 1, 4, kWhole, LANES><<<grid, block, 0, s>>>(a);
-    else if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, kSome, LANES><<<grid, block, 0, s>>>(a);
+    if constexpr (BF16 || !INTERLEAVED)   // (neighbours in fp32 fill 8 bytes by themselves)
+        if (e == 1) {
+            rope_narrow_kernel<BF16, 1, 4, kWhole, LANES><<<grid, block, 0, s>>>(a);
+            return;
+        }
+    if (e < E) rope_narrow_kernel<BF16, E / 2, BF16 ? 1 : 2, kSome, LANES><<<grid, block, 0, s>>>(a);
     else if (INTERLEAVED && a.rot < a.D)
         stream ? rope_kernel<BF16, kSome, true, LANES><<<grid, block, 0, s>>>(a)
                : rope_kernel<BF16, kSome, false, LANES><<<grid, block, 0, s>>>(a);
