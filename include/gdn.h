@@ -706,7 +706,8 @@ int gdn_kv_append_rope(const void *q, const long long *q_strides, const void *k,
  *   n > 0: x <- x - (frequency * n + presence)
  *   x <- x + bias of v;  x <- x * (1 / temperature) (where that is 2^-126 or more);
  *   x <- -inf where v is not allowed
- * each operation, the reciprocals too, rounded once in fp32.  out (NULL: not wanted) receives x in out_dtype, best (NULL:
+ * each operation, the reciprocals too, rounded once in fp32 (so what is divided by repetition or temperature
+ * may be a step of fp32 from the rounded quotient).  out (NULL: not wanted) receives x in out_dtype, best (NULL:
  * not wanted) the token with the largest x + noise, the lowest of equal ones, -1 where
  * every one is -inf (NaN is never the best).
  *   logits [B][K][V] dtype, row (b, t) starting logits_stride elements after

@@ -14,11 +14,13 @@
 // bits each, 16 KB for 8192 tokens), and then streams; a lane knows which of its tokens have a
 // count or a bias, and looks up those alone.
 // Every operation is one rounding of 32 bits in the order above, so that equal
-// logits stay equal and the best is the lowest of them.
+// logits stay equal and the best is the lowest of them.  The reciprocals of repetition and temperature are formed once a
+// workgroup, each rounded: a product with one is off by up to two half steps where a division is by one, and a division
+// is about ten vector instructions for each logit, in a stream whose vector instructions issue in 0.83 of the time.
 //
 // Measured: 64 rows of 131072, fp32, with noise and output (101 MB) 22.4 us, of which the stream 19.6 (5.1 TB/s);
 // 32 ragged windows of 8 rows of 131072, bf16, masks, biases and texts of 4000 (78 MB)
-// 22.9 us: the counting and what it makes the stream look up take 2 us each, joining the best 2.5, a workgroup's reads before its
+// 20.8 to 23.6 us box to box: the counting and what it makes the stream look up take 2 us each, joining the best 2.5, a workgroup's reads before its
 // stream 3; without texts, biases, masks and best 14.0.
 // With the logits of the counted tokens left to a second kernel (a hash table a sequence) the stream was 1 us shorter, and
 // that kernel's scattered reads and writes took 13.
@@ -847,9 +849,10 @@ hipError_t launch_logits(const LogitsArgs& args, bool x_bf16, bool out_bf16, hip
     a.marks = a.n_bias > 0 || (a.params && (a.history || a.tokens));
     const int text = a.params && a.history ? a.capacity : 0;
     const bool many = vectors_of(a) == 4;
-    // (Small slices have room for 32 bits, and no parts to wait for: a row of 131072 with a text of 32000 13.2 us wide, 15.6
-    // long; 8 rows, 100000 34.0 and 43.9; but 64 rows, 100000 in large slices 61 us long, 103 wide in small ones; 32 ragged
-    // windows of 8, texts of 4000 in rows of 131072 23.5 and 30.7.)
+    // By the width of the texts' buffer: their lengths are on the device.  (Small slices have room for 32 bits, and no
+    // parts to wait for: a row of 131072 with a text of 32000 13.2 us wide, 15.6 long; 8 rows, 100000 34.0 and 43.9; but 64
+    // rows, 100000 in large slices 61 us long, 103 wide in small ones; 32 ragged windows of 8, texts of 4000 in rows of
+    // 131072 23.5 and 30.7.)
     if (text > kLongText || a.n_bias > kNarrowBias || (text > kNarrowText && !many)) launch<1, kWide>(a, x_bf16, out_bf16, s);
     else if (text > kNarrowText) launch<4, kLong>(a, x_bf16, out_bf16, s);
     else many ? launch<4, kNarrow>(a, x_bf16, out_bf16, s) : launch<1, kNarrow>(a, x_bf16, out_bf16, s);

@@ -19,10 +19,13 @@
 //   - where the head goes (dense rows, or a page of the cache) is an offset a
 //     token.
 // Measured: 16384 tokens of 48 heads of 128 (bf16, into the cache, 403 MB) 77.1 us, 5.2 TB/s; 8193 of 40
-// heads of 128 (fp32, normed, 336 MB) 66.2 us; 16384 of 32 (bf16, 268 MB) 51.4 us: 97 to 100% of a copy of the same
-// bytes.  1024 tokens in trees of 16, 32 heads of 256 (34 MB) 10.4 us: a workgroup's chain of reads, 9 us from its
-// start to its last store.  Heads asked for before that chain, or a head ahead, took longer in every case (waves
-// then hold more registers, or reads come back in an order that the chain waits for).
+// heads of 128 (fp32, normed, 336 MB) 66.0 us; 16384 of 32 (bf16, 268 MB) 51.5 us: 97 to 100% of a copy of the same
+// bytes.  1024 tokens in trees of 16, 32 heads of 256 (34 MB) 10.5 us: a workgroup's chain of reads, 9 us from its
+// start to its last store.  Of these only a page id needs another read (the length); the others are waited for one by one
+// as they stand: the norms' weights before the tokens' lengths, counts and parents, those each alone, the parts' places
+// (arguments indexed by lane, so read like data) before the angles, and again before each head.  Heads asked for before
+// that chain, or a head ahead, took longer in every case (waves then hold more registers, or reads come back in an order
+// that the chain waits for).
 #include "gdn_device.h"
 #include "gdn_window_internal.h"
 
@@ -358,7 +361,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a)
     }
 }
 
-// Eight waves a SIMD: with six (ten registers more) the large windows took 3 to 6% longer.
+// Eight waves a SIMD: with six (ten registers more) the large windows took 3 to 6% longer.  For it the bf16 kernels keep
+// registers in memory: 8 bytes a lane with kPart, 12 to 20 element by element.
 template <bool BF16, Pairs PAIRS, bool STREAM, bool LANES>
 __global__ __launch_bounds__(kThreads, 8) void rope_kernel(RopeArgs a)
 {
